@@ -12,7 +12,16 @@
  *                     expansion with the tail cells carried along (lever3)
  *   qsa_sparse_attn   split-KV flash-decode over only the selected cells,
  *                     fp16 or q8_0 K/V dequantised after the gather (lever1,
- *                     sparse256, and the author's q8-compact follow-up)
+ *                     sparse256, and the author's q8-compact follow-up), or
+ *                     q4_0 K/V used as codes
+ *
+ * Around the step:
+ *
+ *   qsa_qk_norm_rope  head norms and position rotation of the projections, which
+ *                     gives the step its q, k_new and q_idx
+ *   qsa_kv_read       cache rows as values again
+ *   qsa_cells_copy, qsa_seq_fork, qsa_cache_sweep
+ *                     copying, sharing, freeing and compacting a cache's cells
  *
  * Conventions for every call:
  *  - Pointers named as device buffers are DEVICE pointers owned by the caller.
@@ -21,7 +30,8 @@
  *    of a call must be that device's memory.
  *  - A step's own inputs and outputs (q_idx, w_idx, tok_seq, tok_pos, q and
  *    out; for qsa_kv_append tok_seq, tok_pos, cells, k_new, v_new and
- *    idx_new) may instead be page-locked host memory that the device
+ *    idx_new; for qsa_qk_norm_rope its inputs and outputs but not the weights)
+ *    may instead be page-locked host memory that the device
  *    addresses directly (cudaHostAlloc, or cudaHostRegister; with unified
  *    addressing the host pointer itself): the kernels read and write them in
  *    place over the host link (NVLink-C2C on a Grace system), so a step needs
@@ -53,6 +63,11 @@
  *   k/v cache q8_0 bytes: qs int8 [n_cells][n_kv_heads][head_dim], then at byte
  *                  offset n_cells*n_kv_heads*head_dim the scales d fp16
  *                  [n_cells][n_kv_heads][head_dim/32]; value = d[c][g][i/32]*qs[c][g][i]
+ *   k/v cache q4_0 bytes: codes [n_cells][n_kv_heads][head_dim/2], 16 bytes per
+ *                  32-value block with value i of the block in the low nibble of
+ *                  byte i and value i + 16 in its high nibble, then at byte offset
+ *                  n_cells*n_kv_heads*head_dim/2 the scales d fp16
+ *                  [n_cells][n_kv_heads][head_dim/32]; value = d * (nibble - 8)
  *   blk_cells      int32 [n_slots][compress_ratio]  cell of position j*r+i of the
  *                  slot's block, -1 = not (yet) present
  *   slot_block_idx int32 [n_slots]  block index j of the slot within its sequence
@@ -88,7 +103,9 @@ typedef enum {
   QSA_ERR_DEVICE_BOUNDS = -6   /* qsa_debug_check: a kernel met an out-of-range index */
 } qsa_status;
 
-typedef enum { QSA_KV_F16 = 0, QSA_KV_Q8_0 = 1 } qsa_kv_type;
+typedef enum { QSA_KV_F16 = 0, QSA_KV_Q8_0 = 1, QSA_KV_Q4_0 = 2 } qsa_kv_type;
+/* Element types of qsa_qk_norm_rope's inputs. */
+typedef enum { QSA_ELEM_F16 = 0, QSA_ELEM_BF16 = 1, QSA_ELEM_F32 = 2 } qsa_elem_type;
 /* n_recomputed value of qsa_index_topk's scheduling hint (see there). */
 #define QSA_HINT_QUERY_BLOCKS (-1)
 
@@ -125,7 +142,10 @@ int32_t qsa_cells_per_token(const qsa_config* cfg);
  *   K/V rows of the cell <- k_new[t], v_new[t]  (fp16 [T][n_kv_heads][head_dim];
  *       kv_type f16: copied; q8_0: each 32-value block encoded with scale
  *       d = max|x| / 127 stored as fp16 and codes x * (1/d) rounded half away
- *       from zero, clamped to +-127, all in fp32)
+ *       from zero, clamped to +-127, all in fp32; q4_0: scale d = m / -8 with m
+ *       the block's first value of largest magnitude, stored as fp16, codes
+ *       floor(x * (1/d) + 8.5) clamped to 0..15, all in fp32.  A NaN in a q4_0
+ *       block makes the whole block NaN, an infinity makes its other values NaN)
  *   idx_k[cell] <- idx_new[t]  (fp16 [T][idx_dim])
  *   blk_cells[slot(seq, p / r)][p % r] <- cell
  *   dirty <- the distinct slots of the touched blocks, ascending, padded with
@@ -286,6 +306,11 @@ qsa_status qsa_index_topk_noalloc(const qsa_config* cfg, int32_t n_tokens,
  * CTA per (token, KV head) is the cluster size the cost model gives) the
  * clusters are of two CTAs taking 64-cell tiles, small enough that two
  * share an SM; the result is the same within the stated tolerance.
+ * For q4_0 K/V the codes are multiplied as integers (exactly) and only the
+ * scales' products are rounded, in fp32 (probabilities in two fp16 parts): no
+ * K, V or probability is rounded to fp16, and the output is within 2e-5
+ * max-relative of the exact result.  An infinite or NaN scale among the
+ * attended cells gives NaN.
  * count[t] == 0 gives zeros.  A cell outside [0, n_cells) is masked and
  * flagged.  The call needs no workspace (qsa_sparse_attn_workspace_size
  * returns 0; `workspace` may be NULL). */
@@ -312,7 +337,9 @@ qsa_status qsa_sparse_attn(const qsa_config* cfg, int32_t n_tokens,
  * tiles hold other cells, so the fp16 rounding of the probabilities and the
  * order of the sums differ (both within 2e-3 max-relative of the exact
  * result for fp16 K/V, 5e-3 for q8_0).  cells_pitch (top_k + r - 1)
- * must be at most 4104, else QSA_ERR_UNSUPPORTED.  Needs no workspace. */
+ * must be at most 4104, else QSA_ERR_UNSUPPORTED; so does a q4_0 cache (its
+ * rows are small enough that gathering them twice costs less than the union).
+ * Needs no workspace. */
 qsa_status qsa_sparse_attn_union(const qsa_config* cfg, int32_t n_tokens,
                                  const void* q, const void* k_cache, const void* v_cache,
                                  int64_t n_cells, const int32_t* cells, const int32_t* count,
@@ -331,7 +358,8 @@ qsa_status qsa_sparse_attn_union(const qsa_config* cfg, int32_t n_tokens,
  * flags = 0: the two calls' kernels in order (score, selection with
  * expansion, attention).
  * flags = QSA_INDEX_ATTN_IN_CLUSTER: when max_blocks <= 65,536,
- * top_k / r <= 1,024, r <= 8 and the attention's cluster size leaves each CTA
+ * top_k / r <= 1,024, r <= 8, the cache is f16 or q8_0 and the attention's
+ * cluster size leaves each CTA
  * at most 8 tiles of 128 cells (decode and small verify batches), the
  * selection and the expansion of a token's blocks run inside the attention's
  * thread-block clusters, one cluster per (token, KV head), so no kernel
@@ -370,6 +398,137 @@ uint32_t qsa_index_attn_kernels(const qsa_config* cfg, int32_t n_tokens, int32_t
                                 uint32_t flags);
 
 /* ---------------------------------------------------------------------------
+ * qsa_qk_norm_rope  (the pages take queries and keys as positioned; issue
+ * #28734, fix summary, lever2 "RMS-normed and re-RoPEd" is the same arithmetic
+ * on block keys)
+ * Head norms and position rotation in one pass, from the projections to what
+ * the step takes.  For each row x of n dims (a query head, a KV head's key: n =
+ * head_dim; an indexer query head: n = idx_dim):
+ *   y   = x / sqrt(mean(x^2) + rms_eps) * w
+ *   out = y with its first n_rot dims rotated: pair (i, i + n_rot/2) turns by
+ *         pos[axis(i)][t] * theta^(-2i/n_rot); the other dims as they are
+ * q and k_new are written as fp16 [T][n_q_heads][head_dim] and
+ * [T][n_kv_heads][head_dim]; q_idx as fp32 [T][n_idx_heads][idx_dim], all its
+ * idx_dim dims rotated by idx_pos[t] (the cache position that the block keys
+ * are rotated by), whatever `rope` says.  Arithmetic is fp32 with the angle
+ * reduced exactly in integers; each output is rounded once.
+ *
+ * qsa_rope describes the rotation of the 256-dim heads: qsa_rope_init fills it
+ * on the host, once, for a configuration (it depends on rope_theta), and calls
+ * take it by reference.  sections[a], a < n_axes <= 4: how many pairs turn by
+ * axis a's position (time, height, width, ...); n_rot = 2 * their sum, which
+ * must be a multiple of 8 (QSA_ERR_UNSUPPORTED) and at most head_dim / 2
+ * (QSA_ERR_SHAPE).  interleaved = 0: axis 0's pairs come first, then axis 1's,
+ * and so on; 1: pair i goes to axis i mod n_axes while that axis has pairs left
+ * (i / n_axes < sections[axis]) and to axis 0 otherwise (QSA_ERR_SHAPE if an
+ * axis past the first would not get its number).
+ *
+ * pos: int32 [n_axes][n_tokens], any values.  Inputs: elements of in_type
+ * (qsa_elem_type), rows of a token contiguous, *_stride elements from one token
+ * to the next (so parts of a fused projection can be passed in place); bases
+ * 16-byte aligned, strides a multiple of 16 bytes (q_idx: of 4 elements), at
+ * least a token's width when n_tokens > 1 (QSA_ERR_SHAPE).  q_in, k_in and
+ * q_idx_in may each be NULL to skip that part (its output must then be NULL
+ * too).  An output may be its own input when both are fp16 (q, k_new) or fp32
+ * (q_idx) and contiguous.  Weights fp32 [head_dim] / [idx_dim]; weights and
+ * outputs 16-byte aligned. */
+typedef struct {
+  uint32_t magic;             /* set by qsa_rope_init */
+  int32_t n_rot, n_axes;
+  uint8_t axis[128];          /* of each pair */
+  uint64_t turns[128];        /* theta^(-2i/n_rot) / (2 pi) * 2^64 */
+  uint64_t idx_turns[64];     /* the same for the idx_dim dims of q_idx */
+} qsa_rope;
+qsa_status qsa_rope_init(const qsa_config* cfg, int32_t n_axes, const int32_t* sections, int32_t interleaved,
+                         qsa_rope* rope);
+qsa_status qsa_qk_norm_rope(const qsa_config* cfg, const qsa_rope* rope, int32_t n_tokens, int32_t in_type,
+                            const int32_t* pos, const void* q_in, int64_t q_stride, const void* k_in,
+                            int64_t k_stride, const float* q_norm_w, const float* k_norm_w, void* q, void* k_new,
+                            const int32_t* idx_pos, const void* q_idx_in, int64_t q_idx_stride,
+                            const float* q_idx_norm_w, float* q_idx, qsa_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * qsa_kv_read  (the counterpart of qsa_kv_append)
+ * K and V rows of the listed cells as fp16 values: k_out[i], v_out[i] (fp16
+ * [n][n_kv_heads][head_dim], 16-byte aligned) = the rows of cell cells[i]; for
+ * q8_0 and q4_0 scale times code, rounded once.  For handing cells to a cache
+ * of another type, for saving them, for checks.  An entry < 0 is skipped, one
+ * >= n_cells skipped and flagged: those output rows are left as they were. */
+qsa_status qsa_kv_read(const qsa_config* cfg, int32_t n, const int32_t* cells, const void* k_cache,
+                       const void* v_cache, int64_t n_cells, void* k_out, void* v_out, qsa_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Cells and blocks of a cache (issue #28734, fix summary, lever2: "defrag,
+ * rollback and seq-ops" change a block's member cells; lever2b: the members
+ * live in a device table).  The layers of a model share one allocation of
+ * cells: qsa_seq_fork and qsa_cache_sweep work on the tables and give lists of
+ * cell pairs, qsa_cells_copy carries them out on each layer's rows.  All
+ * buffers are device memory.
+ *
+ * qsa_cells_copy: for i < n, the K and V rows (any kv_type, as stored) and, if
+ * idx_k is given, the indexer key of cell src[i] to cell dst[i].  A pair with
+ * an entry < 0 is skipped, one with an entry >= n_cells skipped and flagged.
+ * n_pairs: optional device count (NULL: n); pairs at and past it are not read.
+ * No cell may be the dst of two pairs, or the dst of one and the src of
+ * another; a pair with src == dst does nothing. */
+qsa_status qsa_cells_copy(const qsa_config* cfg, int32_t n, const int32_t* n_pairs, const int32_t* src,
+                          const int32_t* dst, void* k_cache, void* v_cache, void* idx_k, int64_t n_cells,
+                          qsa_stream_t stream);
+
+/* qsa_seq_fork: sequence dst_seq[f] becomes the first n_pos[f] positions of
+ * sequence src_seq[f].  Whole blocks are shared: their slots are copied into
+ * dst's block list.  A partial last block (n_pos % r cells) becomes private, so
+ * that both sequences can go on: dst's list gets tail_slot[f], whose table row
+ * holds tail_cells[f][0 .. n_pos % r) and -1, with slot_block_idx set, and
+ * copy_src / copy_dst (int32 [n_fork][r]) get the cell pairs that
+ * qsa_cells_copy has to copy (-1 elsewhere).  The pooled key of tail_slot is
+ * stale until it is pooled again (qsa_kv_append with `pooled` does so with the
+ * next position; no call scores an incomplete block).
+ * n_list: entries of seq_blk_slots; dst's part must have room for the blocks,
+ * and max_blocks is a host upper bound on n_pos / r.  src == dst gives a
+ * sequence a partial block of its own.  The dst sequences and tail slots of a
+ * call must be distinct, and no dst may be the src of another fork; tail slots
+ * and cells must not be in use.  A fork with an index out of range, without
+ * room, or past max_blocks changes nothing (pairs -1) and is flagged.
+ * n_fork <= 65535. */
+qsa_status qsa_seq_fork(const qsa_config* cfg, int32_t n_fork, const int32_t* src_seq, const int32_t* dst_seq,
+                        const int32_t* n_pos, const int32_t* tail_slot, const int32_t* tail_cells,
+                        const int64_t* seq_blk_off, int32_t* seq_blk_slots, int32_t n_seq, int64_t n_list,
+                        int32_t* blk_cells, int32_t* slot_block_idx, int64_t n_slots, int64_t n_cells,
+                        int64_t max_blocks, int32_t* copy_src, int32_t* copy_dst, qsa_stream_t stream);
+
+/* qsa_cache_sweep: what the sequences still hold, and the rest freed.
+ * Sequence s holds positions 0 .. seq_len[s] - 1 (<= 0: none; past its list:
+ * what the list has, flagged).  A slot is held if a sequence's list names it for
+ * a block that starts before seq_len; a cell is held if a held position's table
+ * entry names it.  Freeing or rolling back a sequence is therefore a smaller
+ * seq_len; shared blocks stay while anyone holds them.  Writes
+ *   counts[4]      held cells, free cells, free slots, moves
+ *   blk_cells_out  the table with every entry that names no held cell, and
+ *                  every row of a free slot, set to -1 (may be blk_cells itself)
+ *   cell_map       int32 [n_cells], optional: each cell's place afterwards
+ *                  (itself, unless compacted), -1 if free
+ *   free_cells     int32 [n_cells], optional: the free cells, ascending
+ *   free_slots     int32 [n_slots], optional: the free slots, ascending
+ * flags = QSA_SWEEP_COMPACT: the held cells also move together into cells
+ * 0 .. n_held - 1.  The i-th held cell at or past n_held goes to the i-th free
+ * cell before it: move_src / move_dst (int32 [n_cells / 2]) get the pairs, to be
+ * carried out by qsa_cells_copy with n_pairs = counts + 3 on every layer before
+ * the cells are used (sources and destinations are disjoint); the table and
+ * cell_map name the new places, free_cells the cells from n_held on.  cell_map,
+ * move_src and move_dst are then required.  Entries of the lists past their
+ * counts are left as they were.
+ * Indices out of range are skipped and flagged.  workspace:
+ * qsa_cache_sweep_workspace_size bytes, 256-byte aligned, any contents. */
+#define QSA_SWEEP_COMPACT 1u
+size_t qsa_cache_sweep_workspace_size(const qsa_config* cfg, int64_t n_cells, int64_t n_slots);
+qsa_status qsa_cache_sweep(const qsa_config* cfg, uint32_t flags, const int32_t* seq_len, const int64_t* seq_blk_off,
+                           const int32_t* seq_blk_slots, int32_t n_seq, int64_t n_list, const int32_t* blk_cells,
+                           int32_t* blk_cells_out, int64_t n_slots, int64_t n_cells, int32_t* counts,
+                           int32_t* cell_map, int32_t* free_cells, int32_t* free_slots, int32_t* move_src,
+                           int32_t* move_dst, void* workspace, size_t ws_bytes, qsa_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Host helpers (no GPU).
  *
  * qsa_blocks_dirty (issue #28734, fix summary, lever2: "host-side structural
@@ -400,7 +559,9 @@ qsa_status qsa_debug_check(qsa_stream_t stream, uint32_t* flags);
  * histogram when one token per sequence), 2 threshold histogram of
  * token-tiled scores, 3 cluster select + expansion (qsa_index_topk), 4
  * attention (qsa_sparse_attn), 5 append (qsa_kv_append), 6 selection,
- * expansion and attention in one cluster kernel (qsa_index_attn).  `before`/`after`
+ * expansion and attention in one cluster kernel (qsa_index_attn), 7 head norms
+ * (qsa_qk_norm_rope), 8 qsa_kv_read, 9 qsa_cells_copy, 10 qsa_seq_fork, 11 the
+ * kernels of qsa_cache_sweep together.  `before`/`after`
  * are cudaEvent_t handles; NULL clears.  QSA_ERR_INVALID_ARG for an unknown
  * id. */
 qsa_status qsa_profile_kernel(int32_t kernel, void* before, void* after);

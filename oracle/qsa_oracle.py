@@ -39,7 +39,10 @@ def kv_rows(cfg: dict, cache: np.ndarray, n_cells: int, cells: Sequence[int], g:
     f16: the stored half values.  q8_0 ([ISSUE] q8-compact follow-up; the
     README section 1 runs "q8_0 KV cache"): blocks of 32 int8 values along the
     head dimension with one fp16 scale d each; value = float(d) * q.  Byte
-    layout: qs int8 [n_cells][G][D] followed by d fp16 [n_cells][G][D/32]."""
+    layout: qs int8 [n_cells][G][D] followed by d fp16 [n_cells][G][D/32].
+    q4_0: codes [n_cells][G][D/2], value i of a 32-value block in the low nibble
+    of the block's byte i and value i + 16 in its high nibble, followed by the
+    same scales; value = float(d) * (code - 8)."""
     G, D = cfg["n_kv_heads"], cfg["head_dim"]
     cells = np.asarray(cells, dtype=np.int64)
     if cfg["kv_type"] == "f16":
@@ -53,6 +56,13 @@ def kv_rows(cfg: dict, cache: np.ndarray, n_cells: int, cells: Sequence[int], g:
         q = qs[cells, g, :].astype(np.float64)
         scale = d[cells, g, :].astype(np.float64)
         return q * np.repeat(scale, 32, axis=1)
+    if cfg["kv_type"] == "q4_0":
+        raw = np.asarray(cache).view(np.uint8)
+        nq = n_cells * G * D // 2
+        b = raw[:nq].reshape(n_cells, G, D // 32, 16)[cells, g].astype(np.int64)
+        d = raw[nq:nq + n_cells * G * (D // 32) * 2].view(np.float16).reshape(n_cells, G, D // 32)
+        code = np.concatenate([b % 16, b // 16], axis=-1) - 8
+        return (code * d[cells, g].astype(np.float64)[..., None]).reshape(len(cells), D)
     raise ValueError(cfg["kv_type"])
 
 
@@ -280,6 +290,26 @@ def q8_0_block(x32: np.ndarray):
     return q, np.float16(d)
 
 
+def q4_0_block(x32: np.ndarray):
+    """q4_0 encoding of one block of 32 values: scale d = m / -8 with m the
+    first value of largest magnitude (so m gets code 0 and is exact up to the
+    scale's rounding), codes floor(x * (1/d) + 8.5) clamped to 0..15, every
+    operation in float32; d is stored as fp16.  A block of zeros gives d = 0,
+    codes 8.  Returns (codes int [32], d float16)."""
+    x = np.asarray(x32, dtype=np.float32).reshape(32)
+    m = np.float32(0.0)
+    for v in x:
+        if abs(v) > abs(m):
+            m = v
+    d = np.float32(m / np.float32(-8.0))
+    inv = np.float32(np.float32(1.0) / d) if d != 0 else np.float32(0.0)
+    codes = np.zeros(32, dtype=np.int64)
+    for i, v in enumerate(x):
+        t = np.float32(np.float32(v * inv) + np.float32(8.5))
+        codes[i] = min(15, max(0, int(np.floor(t))))
+    return codes, np.float16(d)
+
+
 def kv_append(cfg: dict, tok_seq, tok_pos, cells, k_new, v_new, idx_new, k_cache, v_cache, idx_k,
               n_cells: int, blk_cells, seq_blk_off, seq_blk_slots, n_dirty: int, inplace: bool = False):
     """Write the step's new cells into the caches and the block table, and
@@ -287,7 +317,7 @@ def kv_append(cfg: dict, tok_seq, tok_pos, cells, k_new, v_new, idx_new, k_cache
     device table; lever2: only dirtied blocks are re-pooled, their count padded
     to a power of two by the caller).  For token t at position p of sequence
     s occupying cell c: K/V rows of c <- k_new[t], v_new[t] (fp16 copied, or
-    q8_0-encoded per 32-value block by q8_0_block), idx_k[c] <- idx_new[t],
+    encoded per 32-value block by q8_0_block or q4_0_block), idx_k[c] <- idx_new[t],
     blk_cells[slot(s, p // r)][p % r] <- c.  dirty = the distinct slots of the
     touched blocks, ascending, padded with -1 to n_dirty entries.
     Returns updated copies (k_cache, v_cache, idx_k, blk_cells) and dirty
@@ -310,6 +340,16 @@ def kv_append(cfg: dict, tok_seq, tok_pos, cells, k_new, v_new, idx_new, k_cache
                 cache.reshape(n_cells, G, D)[c] = rows
                 continue
             raw = cache.view(np.uint8)
+            if cfg["kv_type"] == "q4_0":
+                nq = n_cells * G * D // 2
+                qs = raw[:nq].reshape(n_cells, G, D // 2)
+                dd = raw[nq:nq + n_cells * G * (D // 32) * 2].view(np.float16).reshape(n_cells, G, D // 32)
+                for g in range(G):
+                    for b in range(D // 32):
+                        code, d = q4_0_block(np.asarray(rows[g, 32 * b:32 * b + 32], dtype=np.float32))
+                        qs[c, g, 16 * b:16 * b + 16] = code[:16] + 16 * code[16:]
+                        dd[c, g, b] = d
+                continue
             nq = n_cells * G * D
             qs = raw[:nq].view(np.int8).reshape(n_cells, G, D)
             dd = raw[nq:nq + n_cells * G * (D // 32) * 2].view(np.float16).reshape(n_cells, G, D // 32)

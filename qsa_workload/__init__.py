@@ -2,7 +2,7 @@
 
 This module is shared by the CPU oracle, the tests and the benchmark. It only
 draws random numbers and lays them out (cell allocation, block tables, the
-q8_0 byte layout of the K/V cache); it holds none of the step's arithmetic
+q8_0 and q4_0 byte layouts of the K/V cache); it holds none of the step's arithmetic
 (no pooling, scoring, selection or attention).
 
 Workloads follow the shapes of the llama.cpp qwen4exp issue ("decode slows
@@ -15,5 +15,6 @@ from .gen import (  # noqa: F401
     Workload,
     default_cfg,
     make_workload,
+    quantize_q4_0,
     quantize_q8_0,
 )

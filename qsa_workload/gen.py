@@ -10,6 +10,9 @@ Layouts (shared by every consumer):
   idx_k      fp16  [n_cells][idx_dim]                  per-cell indexer key
   k/v cache  fp16  [n_cells][n_kv_heads][head_dim]     (kv_type "f16")
              q8_0  bytes: qs int8 [n_cells][G][D] then d fp16 [n_cells][G][D/32]
+             q4_0  bytes: codes [n_cells][G][D/2] (value i of a 32-value block in
+                   the low nibble of its byte i, value i + 16 in the high one)
+                   then d fp16 [n_cells][G][D/32]
   blk_cells  int32 [n_slots][r]   cell of position j*r+i of the slot's block, -1 = absent
   slot_block_idx int32 [n_slots]  block index j of the slot within its sequence
   seq_blk_off int64 [n_seq+1], seq_blk_slots int32: block j of seq s -> slot
@@ -61,6 +64,25 @@ def quantize_q8_0(x: np.ndarray):
     return q.reshape(x.shape), d.astype(np.float16)
 
 
+def quantize_q4_0(x: np.ndarray):
+    """q4_0 encoding of the last axis in blocks of 32: d = m / -8 with m the
+    first value of largest magnitude, code = floor(x * (1/d) + 8.5) clamped to
+    0..15, d stored as fp16.
+
+    Returns (codes uint8 with last axis D/2, d fp16 with last axis D/32)."""
+    x = np.asarray(x, dtype=np.float32)
+    lead, D = x.shape[:-1], x.shape[-1]
+    xb = x.reshape(*lead, D // 32, 32)
+    m = np.take_along_axis(xb, np.abs(xb).argmax(axis=-1)[..., None], axis=-1)
+    d = m * np.float32(-0.125)
+    inv = np.zeros_like(d)
+    nz = d != 0
+    inv[nz] = np.float32(1.0) / d[nz]
+    n = np.clip(np.floor(xb * inv + np.float32(8.5)), 0, 15).astype(np.uint8)
+    codes = n[..., :16] | (n[..., 16:] << 4)
+    return codes.reshape(*lead, D // 2), d[..., 0].astype(np.float16)
+
+
 @dataclasses.dataclass
 class Step:
     """Inputs of one step: T query tokens."""
@@ -84,7 +106,7 @@ class Workload:
     n_seq: int
     n_cells: int
     idx_k: np.ndarray                # fp16 [n_cells][DI]
-    k_cache: np.ndarray              # fp16 [n][G][D] or uint8 q8_0 bytes
+    k_cache: np.ndarray              # fp16 [n][G][D] or uint8 q8_0 / q4_0 bytes
     v_cache: np.ndarray
     seq_cells: List[np.ndarray]      # per seq: int32 cell of each position (all steps)
     prompt_len: List[int]
@@ -165,17 +187,18 @@ def _normal_f16(rng, shape, chunk_rows=65536):
     return out
 
 
-def _normal_q8_0(rng, n_cells, G, D, keep=None, chunk_rows=65536):
-    """q8_0 cache bytes of N(0,1) rows rounded to fp16 (the K/V precision a
-    model writes), and the fp16 rows of the sorted cells `keep` (the cells
-    appended by the steps, so that an append can be fed the same rows)."""
-    qs = np.empty((n_cells, G, D), dtype=np.int8)
+def _normal_quantized(rng, n_cells, G, D, kv_type, keep=None, chunk_rows=65536):
+    """q8_0 or q4_0 cache bytes of N(0,1) rows rounded to fp16 (the K/V
+    precision a model writes), and the fp16 rows of the sorted cells `keep` (the
+    cells appended by the steps, so that an append can be fed the same rows)."""
+    quantize = {"q8_0": quantize_q8_0, "q4_0": quantize_q4_0}[kv_type]
+    qs = np.empty((n_cells, G, D), dtype=np.int8) if kv_type == "q8_0" else np.empty((n_cells, G, D // 2), np.uint8)
     d = np.empty((n_cells, G, D // 32), dtype=np.float16)
     kept = np.empty((0 if keep is None else len(keep), G, D), dtype=np.float16)
     for a in range(0, n_cells, chunk_rows):
         b = min(n_cells, a + chunk_rows)
         x = rng.standard_normal((b - a, G, D), dtype=np.float32).astype(np.float16)
-        qs[a:b], d[a:b] = quantize_q8_0(x.astype(np.float32))
+        qs[a:b], d[a:b] = quantize(x.astype(np.float32))
         if keep is not None:
             lo, hi = np.searchsorted(keep, [a, b])
             kept[lo:hi] = x[keep[lo:hi] - a]
@@ -323,9 +346,9 @@ def make_workload(name: str = "custom", *, n_seq: Optional[int] = None,
         k_cache = _normal_f16(np.random.default_rng(s_k), (n_cells, G, D))
         v_cache = _normal_f16(np.random.default_rng(s_v), (n_cells, G, D))
         k_src, v_src = k_cache[new_cells], v_cache[new_cells]
-    elif kv_type == "q8_0":
-        k_cache, k_src = _normal_q8_0(np.random.default_rng(s_k), n_cells, G, D, keep=new_cells)
-        v_cache, v_src = _normal_q8_0(np.random.default_rng(s_v), n_cells, G, D, keep=new_cells)
+    elif kv_type in ("q8_0", "q4_0"):
+        k_cache, k_src = _normal_quantized(np.random.default_rng(s_k), n_cells, G, D, kv_type, keep=new_cells)
+        v_cache, v_src = _normal_quantized(np.random.default_rng(s_v), n_cells, G, D, kv_type, keep=new_cells)
     else:
         raise ValueError(kv_type)
 

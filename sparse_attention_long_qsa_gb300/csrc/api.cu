@@ -23,7 +23,7 @@ qsa_status check_cfg(const qsa_config* c) {
   if (c->n_q_heads <= 0 || c->n_kv_heads <= 0 || c->head_dim <= 0 || c->n_idx_heads <= 0 ||
       c->idx_dim <= 0 || c->compress_ratio <= 0 || c->top_k <= 0)
     return QSA_ERR_INVALID_ARG;
-  if (c->kv_type != QSA_KV_F16 && c->kv_type != QSA_KV_Q8_0) return QSA_ERR_INVALID_ARG;
+  if (c->kv_type != QSA_KV_F16 && c->kv_type != QSA_KV_Q8_0 && c->kv_type != QSA_KV_Q4_0) return QSA_ERR_INVALID_ARG;
   if (!(c->rope_theta > 0.f) || !(c->rms_eps >= 0.f) || !std::isfinite(c->attn_scale) ||
       !std::isfinite(c->rope_theta))
     return QSA_ERR_INVALID_ARG;
@@ -80,6 +80,24 @@ qsa_status fill_index_args(const qsa_config* cfg, int32_t n_tokens, int32_t max_
   a->n_sel_blocks = cfg->top_k / cfg->compress_ratio;
   a->cells_pitch = cfg->top_k + cfg->compress_ratio - 1;
   return QSA_OK;
+}
+
+// qsa_sparse_attn_union takes this configuration.
+bool union_supported(const qsa_config* cfg) {
+  return cfg->kv_type != QSA_KV_Q4_0 && cfg->top_k + cfg->compress_ratio - 1 <= union_attn_max_pitch();
+}
+// The selection may run inside the attention clusters (f16 and q8_0 caches).
+bool in_cluster_asked(const qsa_config* cfg, uint32_t flags) {
+  return cfg->kv_type != QSA_KV_Q4_0 && (flags & QSA_INDEX_ATTN_IN_CLUSTER) != 0u;
+}
+
+constexpr uint32_t kRopeMagic = 0x51524f50u;
+
+// Bytes of a cell's K (or V) codes and scales in the cache.
+void cell_bytes(const qsa_config* cfg, int* codes, int* scales) {
+  const int values = cfg->n_kv_heads * kHeadDim;
+  *codes = cfg->kv_type == QSA_KV_F16 ? 2 * values : cfg->kv_type == QSA_KV_Q8_0 ? values : values / 2;
+  *scales = cfg->kv_type == QSA_KV_F16 ? 0 : values / 16;
 }
 
 }  // namespace
@@ -201,6 +219,7 @@ qsa_status attn_args(const qsa_config* cfg, int32_t n_tokens, const void* q, con
   a->n_tokens = n_tokens;
   a->n_kv_heads = cfg->n_kv_heads;
   a->kv_q8 = cfg->kv_type == QSA_KV_Q8_0;
+  a->kv_q4 = cfg->kv_type == QSA_KV_Q4_0;
   a->q = static_cast<const __half*>(q);
   a->k_cache = k_cache;
   a->v_cache = v_cache;
@@ -236,7 +255,7 @@ qsa_status qsa_sparse_attn_union(const qsa_config* cfg, int32_t n_tokens, const 
   const qsa_status st = attn_args(cfg, n_tokens, q, k_cache, v_cache, n_cells, cells, count, out, workspace,
                                   ws_bytes, &a);
   if (st != QSA_OK) return st;
-  if (cfg->top_k + cfg->compress_ratio - 1 > union_attn_max_pitch()) return QSA_ERR_UNSUPPORTED;
+  if (!union_supported(cfg)) return QSA_ERR_UNSUPPORTED;
   if (n_tokens == 0) return QSA_OK;
   unsigned* err = error_word();
   if (err == nullptr) return QSA_ERR_CUDA;
@@ -258,7 +277,7 @@ qsa_status qsa_index_attn(const qsa_config* cfg, int32_t n_tokens, int32_t max_t
   constexpr uint32_t kFlags = QSA_INDEX_ATTN_IN_CLUSTER | QSA_INDEX_ATTN_UNION;
   if (n_cells < 0 || (flags & ~kFlags) != 0u || flags == kFlags) return QSA_ERR_INVALID_ARG;
   const bool by_union = (flags & QSA_INDEX_ATTN_UNION) != 0u;
-  if (by_union && cfg->top_k + cfg->compress_ratio - 1 > union_attn_max_pitch()) return QSA_ERR_UNSUPPORTED;
+  if (by_union && !union_supported(cfg)) return QSA_ERR_UNSUPPORTED;
   if (n_cells > kMaxI32) return QSA_ERR_UNSUPPORTED;
   if (n_tokens == 0) return QSA_OK;
   if (!blk_cells || !cells || !count || !q || !k_cache || !v_cache || !out) return QSA_ERR_INVALID_ARG;
@@ -277,6 +296,7 @@ qsa_status qsa_index_attn(const qsa_config* cfg, int32_t n_tokens, int32_t max_t
   a.n_tokens = n_tokens;
   a.n_kv_heads = cfg->n_kv_heads;
   a.kv_q8 = cfg->kv_type == QSA_KV_Q8_0;
+  a.kv_q4 = cfg->kv_type == QSA_KV_Q4_0;
   a.q = static_cast<const __half*>(q);
   a.k_cache = k_cache;
   a.v_cache = v_cache;
@@ -295,8 +315,7 @@ qsa_status qsa_index_attn(const qsa_config* cfg, int32_t n_tokens, int32_t max_t
     return from_cuda(e);
   }
   bool fused = false;
-  return from_cuda(launch_index_attn(ia, a, cells, count, workspace, (flags & QSA_INDEX_ATTN_IN_CLUSTER) != 0u,
-                                     err, cs, &fused));
+  return from_cuda(launch_index_attn(ia, a, cells, count, workspace, in_cluster_asked(cfg, flags), err, cs, &fused));
 }
 
 uint32_t qsa_index_attn_kernels(const qsa_config* cfg, int32_t n_tokens, int32_t n_seq, int64_t max_blocks,
@@ -304,10 +323,9 @@ uint32_t qsa_index_attn_kernels(const qsa_config* cfg, int32_t n_tokens, int32_t
   if (check_cfg(cfg) != QSA_OK || n_tokens <= 0) return 0u;
   constexpr uint32_t kFlags = QSA_INDEX_ATTN_IN_CLUSTER | QSA_INDEX_ATTN_UNION;
   if ((flags & ~kFlags) != 0u || flags == kFlags) return 0u;
-  if ((flags & QSA_INDEX_ATTN_UNION) != 0u && cfg->top_k + cfg->compress_ratio - 1 > qsa::union_attn_max_pitch())
-    return 0u;
+  if ((flags & QSA_INDEX_ATTN_UNION) != 0u && !union_supported(cfg)) return 0u;
   bool fused = false;
-  if ((flags & QSA_INDEX_ATTN_IN_CLUSTER) != 0u && qsa::index_attn_plan(n_tokens, cfg->n_kv_heads, cfg->kv_type == QSA_KV_Q8_0,
+  if (in_cluster_asked(cfg, flags) && qsa::index_attn_plan(n_tokens, cfg->n_kv_heads, cfg->kv_type == QSA_KV_Q8_0,
                            cfg->top_k + cfg->compress_ratio - 1, max_blocks > 0 ? max_blocks : 1,
                            cfg->top_k / cfg->compress_ratio, cfg->compress_ratio, &fused) != cudaSuccess) {
     (void)cudaGetLastError();
@@ -345,6 +363,242 @@ qsa_status qsa_kv_append(const qsa_config* cfg, int32_t n_new, const int32_t* to
                                  v_cache, static_cast<__half*>(idx_k), n_cells, blk_cells, n_slots, seq_blk_off,
                                  seq_blk_slots, n_seq, dirty, n_dirty, slot_block_idx, norm_w, pooled, err,
                                  reinterpret_cast<cudaStream_t>(stream)));
+}
+
+qsa_status qsa_rope_init(const qsa_config* cfg, int32_t n_axes, const int32_t* sections, int32_t interleaved,
+                         qsa_rope* rope) {
+  const qsa_status st = check_cfg(cfg);
+  if (st != QSA_OK) return st;
+  if (rope == nullptr || sections == nullptr || n_axes < 1 || (interleaved != 0 && interleaved != 1))
+    return QSA_ERR_INVALID_ARG;
+  if (n_axes > 4) return QSA_ERR_UNSUPPORTED;
+  int64_t pairs = 0;
+  for (int a = 0; a < n_axes; ++a) {
+    if (sections[a] < 0) return QSA_ERR_INVALID_ARG;
+    pairs += sections[a];
+  }
+  if (pairs > kHeadDim / 2) return QSA_ERR_SHAPE;
+  if (pairs % 8 != 0) return QSA_ERR_UNSUPPORTED;
+  qsa_rope o{};
+  o.magic = kRopeMagic;
+  o.n_rot = (int32_t)(2 * pairs);   // a multiple of 16: a lane's 8 dims have one partner lane
+  o.n_axes = n_axes;
+  if (interleaved == 0) {
+    int i = 0;
+    for (int a = 0; a < n_axes; ++a)
+      for (int k = 0; k < sections[a]; ++k) o.axis[i++] = (uint8_t)a;
+  } else {
+    for (int a = 1; a < n_axes; ++a)   // pair a + k * n_axes for k < sections[a] has to exist
+      if (sections[a] > 0 && (int64_t)(sections[a] - 1) * n_axes + a >= pairs) return QSA_ERR_SHAPE;
+    for (int i = 0; i < (int)pairs; ++i) {
+      const int a = i % n_axes;
+      o.axis[i] = (uint8_t)(i / n_axes < sections[a] ? a : 0);
+    }
+  }
+  for (int i = 0; i < (int)pairs; ++i) o.turns[i] = turn_of(cfg->rope_theta, -(double)i / (double)pairs);
+  for (int i = 0; i < kIdxDim / 2; ++i) o.idx_turns[i] = turn_of(cfg->rope_theta, (-2.0 * i) / (double)kIdxDim);
+  *rope = o;
+  return QSA_OK;
+}
+
+qsa_status qsa_qk_norm_rope(const qsa_config* cfg, const qsa_rope* rope, int32_t n_tokens, int32_t in_type,
+                            const int32_t* pos, const void* q_in, int64_t q_stride, const void* k_in,
+                            int64_t k_stride, const float* q_norm_w, const float* k_norm_w, void* q, void* k_new,
+                            const int32_t* idx_pos, const void* q_idx_in, int64_t q_idx_stride,
+                            const float* q_idx_norm_w, float* q_idx, qsa_stream_t stream) {
+  qsa_status st = check_cfg(cfg);
+  if (st != QSA_OK) return st;
+  if (rope == nullptr || rope->magic != kRopeMagic || rope->n_rot < 0 || rope->n_rot > kHeadDim ||
+      rope->n_rot % 16 != 0 || rope->n_axes < 1 || rope->n_axes > 4 || n_tokens < 0)
+    return QSA_ERR_INVALID_ARG;
+  for (int i = 0; i < rope->n_rot / 2; ++i)
+    if (rope->axis[i] >= rope->n_axes) return QSA_ERR_INVALID_ARG;
+  if (in_type != QSA_ELEM_F16 && in_type != QSA_ELEM_BF16 && in_type != QSA_ELEM_F32) return QSA_ERR_INVALID_ARG;
+  if (n_tokens == 0) return QSA_OK;
+  const int64_t per16 = in_type == QSA_ELEM_F32 ? 4 : 8;   // elements in 16 bytes
+  const int64_t per_idx = 4;                               // the indexer's rows load 4 elements per lane
+  if ((q_in || k_in) && rope->n_rot > 0 && (pos == nullptr || !aligned(pos, 4))) return QSA_ERR_INVALID_ARG;
+  struct Part {
+    const void* in;
+    int64_t stride, width, unit;
+    const float* w;
+    const void* out;
+  };
+  const Part parts[3] = {{q_in, q_stride, (int64_t)cfg->n_q_heads * kHeadDim, per16, q_norm_w, q},
+                         {k_in, k_stride, (int64_t)cfg->n_kv_heads * kHeadDim, per16, k_norm_w, k_new},
+                         {q_idx_in, q_idx_stride, (int64_t)kIdxHeads * kIdxDim, per_idx, q_idx_norm_w, q_idx}};
+  for (const Part& p : parts) {
+    if (p.in == nullptr) {
+      if (p.out != nullptr) return QSA_ERR_INVALID_ARG;
+      continue;
+    }
+    if (p.w == nullptr || p.out == nullptr || !aligned(p.w, 16) || !aligned(p.out, 16)) return QSA_ERR_INVALID_ARG;
+    if (!aligned(p.in, 16) || p.stride < 0 || p.stride % p.unit != 0) return QSA_ERR_INVALID_ARG;
+    if (n_tokens > 1 && p.stride < p.width) return QSA_ERR_SHAPE;
+  }
+  if (q_idx_in != nullptr && (idx_pos == nullptr || !aligned(idx_pos, 4))) return QSA_ERR_INVALID_ARG;
+  if (q_in == nullptr && k_in == nullptr && q_idx_in == nullptr) return QSA_OK;
+  NormRopeArgs a{};
+  a.n_tokens = n_tokens;
+  a.Hq = cfg->n_q_heads;
+  a.G = cfg->n_kv_heads;
+  a.pos = pos;
+  a.idx_pos = idx_pos;
+  a.q_in = q_in;
+  a.q_stride = q_stride;
+  a.k_in = k_in;
+  a.k_stride = k_stride;
+  a.qi_in = q_idx_in;
+  a.qi_stride = q_idx_stride;
+  a.q_w = q_norm_w;
+  a.k_w = k_norm_w;
+  a.qi_w = q_idx_norm_w;
+  a.q = static_cast<__half*>(q);
+  a.k = static_cast<__half*>(k_new);
+  a.qi = q_idx;
+  a.eps = cfg->rms_eps;
+  return from_cuda(launch_norm_rope(a, *rope, in_type, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+qsa_status qsa_kv_read(const qsa_config* cfg, int32_t n, const int32_t* cells, const void* k_cache,
+                       const void* v_cache, int64_t n_cells, void* k_out, void* v_out, qsa_stream_t stream) {
+  const qsa_status st = check_cfg(cfg);
+  if (st != QSA_OK) return st;
+  if (n < 0 || n_cells < 0) return QSA_ERR_INVALID_ARG;
+  if (n_cells > kMaxI32) return QSA_ERR_UNSUPPORTED;
+  if (n == 0) return QSA_OK;
+  if (!cells || !k_cache || !v_cache || !k_out || !v_out) return QSA_ERR_INVALID_ARG;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_out, 16) || !aligned(v_out, 16))
+    return QSA_ERR_INVALID_ARG;
+  unsigned* err = error_word();
+  if (err == nullptr) return QSA_ERR_CUDA;
+  ReadArgs a{};
+  a.n = n;
+  a.G = cfg->n_kv_heads;
+  a.kv_type = cfg->kv_type;
+  a.cells = cells;
+  a.k_cache = static_cast<const unsigned char*>(k_cache);
+  a.v_cache = static_cast<const unsigned char*>(v_cache);
+  a.n_cells = n_cells;
+  a.k_out = static_cast<__half*>(k_out);
+  a.v_out = static_cast<__half*>(v_out);
+  return from_cuda(launch_kv_read(a, err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+qsa_status qsa_cells_copy(const qsa_config* cfg, int32_t n, const int32_t* n_pairs, const int32_t* src,
+                          const int32_t* dst, void* k_cache, void* v_cache, void* idx_k, int64_t n_cells,
+                          qsa_stream_t stream) {
+  const qsa_status st = check_cfg(cfg);
+  if (st != QSA_OK) return st;
+  if (n < 0 || n_cells < 0) return QSA_ERR_INVALID_ARG;
+  if (n_cells > kMaxI32) return QSA_ERR_UNSUPPORTED;
+  if (n == 0) return QSA_OK;
+  if (!src || !dst || !k_cache || !v_cache) return QSA_ERR_INVALID_ARG;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(idx_k, 16)) return QSA_ERR_INVALID_ARG;
+  unsigned* err = error_word();
+  if (err == nullptr) return QSA_ERR_CUDA;
+  int codes = 0, scales = 0;
+  cell_bytes(cfg, &codes, &scales);
+  CopyArgs a{};
+  a.n = n;
+  a.n_dev = n_pairs;
+  a.src = src;
+  a.dst = dst;
+  a.n_cells = n_cells;
+  a.base[0] = static_cast<unsigned char*>(k_cache);
+  a.base[1] = static_cast<unsigned char*>(v_cache);
+  a.base[2] = a.base[0] + n_cells * codes;
+  a.base[3] = a.base[1] + n_cells * codes;
+  a.base[4] = static_cast<unsigned char*>(idx_k);
+  a.len[0] = a.len[1] = codes / 16;
+  a.len[2] = a.len[3] = scales / 16;
+  a.len[4] = idx_k != nullptr ? kIdxDim * 2 / 16 : 0;
+  for (int k = 0; k < 5; ++k) a.chunks += a.len[k];
+  return from_cuda(launch_cells_copy(a, err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+qsa_status qsa_seq_fork(const qsa_config* cfg, int32_t n_fork, const int32_t* src_seq, const int32_t* dst_seq,
+                        const int32_t* n_pos, const int32_t* tail_slot, const int32_t* tail_cells,
+                        const int64_t* seq_blk_off, int32_t* seq_blk_slots, int32_t n_seq, int64_t n_list,
+                        int32_t* blk_cells, int32_t* slot_block_idx, int64_t n_slots, int64_t n_cells,
+                        int64_t max_blocks, int32_t* copy_src, int32_t* copy_dst, qsa_stream_t stream) {
+  const qsa_status st = check_cfg(cfg);
+  if (st != QSA_OK) return st;
+  if (n_fork < 0 || n_seq < 0 || n_list < 0 || n_slots < 0 || n_cells < 0 || max_blocks < 0) return QSA_ERR_INVALID_ARG;
+  if (n_fork > 65535 || n_slots > kMaxI32 || n_cells > kMaxI32 || n_list > kMaxI32 || max_blocks > kMaxI32)
+    return QSA_ERR_UNSUPPORTED;
+  if (n_fork == 0) return QSA_OK;
+  if (!src_seq || !dst_seq || !n_pos || !tail_slot || !tail_cells || !seq_blk_off || !seq_blk_slots || !blk_cells ||
+      !slot_block_idx || !copy_src || !copy_dst || n_seq == 0)
+    return QSA_ERR_INVALID_ARG;
+  if (!aligned(seq_blk_off, 8)) return QSA_ERR_INVALID_ARG;
+  unsigned* err = error_word();
+  if (err == nullptr) return QSA_ERR_CUDA;
+  ForkArgs a{};
+  a.n = n_fork;
+  a.r = cfg->compress_ratio;
+  a.src_seq = src_seq;
+  a.dst_seq = dst_seq;
+  a.n_pos = n_pos;
+  a.tail_slot = tail_slot;
+  a.tail_cells = tail_cells;
+  a.seq_blk_off = seq_blk_off;
+  a.seq_blk_slots = seq_blk_slots;
+  a.n_seq = n_seq;
+  a.n_list = n_list;
+  a.blk_cells = blk_cells;
+  a.slot_block_idx = slot_block_idx;
+  a.n_slots = n_slots;
+  a.n_cells = n_cells;
+  a.max_blocks = max_blocks;
+  a.copy_src = copy_src;
+  a.copy_dst = copy_dst;
+  return from_cuda(launch_seq_fork(a, err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t qsa_cache_sweep_workspace_size(const qsa_config* cfg, int64_t n_cells, int64_t n_slots) {
+  if (check_cfg(cfg) != QSA_OK || n_cells < 0 || n_slots < 0 || n_cells > kMaxI32 || n_slots > kMaxI32) return 0;
+  return sweep_workspace_bytes(n_cells, n_slots);
+}
+
+qsa_status qsa_cache_sweep(const qsa_config* cfg, uint32_t flags, const int32_t* seq_len, const int64_t* seq_blk_off,
+                           const int32_t* seq_blk_slots, int32_t n_seq, int64_t n_list, const int32_t* blk_cells,
+                           int32_t* blk_cells_out, int64_t n_slots, int64_t n_cells, int32_t* counts,
+                           int32_t* cell_map, int32_t* free_cells, int32_t* free_slots, int32_t* move_src,
+                           int32_t* move_dst, void* workspace, size_t ws_bytes, qsa_stream_t stream) {
+  const qsa_status st = check_cfg(cfg);
+  if (st != QSA_OK) return st;
+  if (n_seq < 0 || n_list < 0 || n_slots < 0 || n_cells < 0 || (flags & ~QSA_SWEEP_COMPACT) != 0u)
+    return QSA_ERR_INVALID_ARG;
+  if (n_cells > kMaxI32 || n_slots > kMaxI32 || n_list > kMaxI32) return QSA_ERR_UNSUPPORTED;
+  const bool compact = (flags & QSA_SWEEP_COMPACT) != 0u;
+  if (!seq_len || !seq_blk_off || !seq_blk_slots || n_seq == 0 || !blk_cells || !blk_cells_out || !counts)
+    return QSA_ERR_INVALID_ARG;
+  if (compact && (!cell_map || !move_src || !move_dst)) return QSA_ERR_INVALID_ARG;
+  if (!aligned(seq_blk_off, 8)) return QSA_ERR_INVALID_ARG;
+  if (workspace == nullptr || !aligned(workspace, 256) || ws_bytes < sweep_workspace_bytes(n_cells, n_slots))
+    return QSA_ERR_WORKSPACE;
+  unsigned* err = error_word();
+  if (err == nullptr) return QSA_ERR_CUDA;
+  SweepArgs a{};
+  a.seq_len = seq_len;
+  a.seq_blk_off = seq_blk_off;
+  a.seq_blk_slots = seq_blk_slots;
+  a.n_seq = n_seq;
+  a.n_list = n_list;
+  a.blk_cells = blk_cells;
+  a.blk_cells_out = blk_cells_out;
+  a.n_slots = n_slots;
+  a.n_cells = n_cells;
+  a.r = cfg->compress_ratio;
+  a.compact = compact ? 1 : 0;
+  a.counts = counts;
+  a.cell_map = cell_map;
+  a.free_cells = free_cells;
+  a.free_slots = free_slots;
+  a.move_src = move_src;
+  a.move_dst = move_dst;
+  return from_cuda(launch_cache_sweep(a, workspace, err, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 qsa_status qsa_blocks_dirty(const int32_t* old_tbl, const int32_t* new_tbl, int64_t n_slots,

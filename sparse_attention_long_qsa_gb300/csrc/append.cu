@@ -9,7 +9,10 @@
 // between writing its cells and re-pooling their blocks.  q8_0 (the author's
 // q8-compact follow-up; README section 1 runs a q8_0 K/V cache): blocks of 32
 // values, scale d = max|x| / 127 stored as fp16, codes x * (1/d) rounded half
-// away from zero, all in fp32.
+// away from zero, all in fp32.  q4_0: blocks of 32 values, scale d = m / -8
+// with m the first value of largest magnitude, codes floor(x * (1/d) + 8.5)
+// clamped to 0..15 (each operation rounded to fp32, no fused multiply-add),
+// value i in the low nibble of byte i, value i + 16 in its high nibble.
 //
 // One warp per (token, row): rows 0..G-1 are the K heads, G..2G-1 the V
 // heads, 2G the indexer key together with the table entry; that warp of each
@@ -35,7 +38,7 @@ struct AppendArgs {
   int n_new;
   int G;
   int r;
-  int kv_q8;
+  int kv_type;
   const int32_t* tok_seq;
   const int32_t* tok_pos;
   const int32_t* cell;
@@ -212,12 +215,12 @@ k_append(const AppendArgs a, const Turns turns, unsigned* err) {
     const __half* src = (kind < a.G ? a.k_new : a.v_new) + ((int64_t)t * a.G + g) * kHeadDim;
     unsigned char* cache = kind < a.G ? a.k_cache : a.v_cache;
     const uint4 raw = ok ? __ldg(reinterpret_cast<const uint4*>(src) + lane) : make_uint4(0, 0, 0, 0);
-    if (!a.kv_q8) {
+    if (a.kv_type == QSA_KV_F16) {
       grid_dep_wait();
       if (ok) reinterpret_cast<uint4*>(cache + (c * a.G + g) * kHeadDim * 2)[lane] = raw;
       return;
     }
-    // q8_0: lanes 4b..4b+3 hold the 32 values of block b
+    // q8_0, q4_0: lanes 4b..4b+3 hold the 32 values of block b
     const __half2* h = reinterpret_cast<const __half2*>(&raw);
     float x[8];
 #pragma unroll
@@ -225,6 +228,45 @@ k_append(const AppendArgs a, const Turns turns, unsigned* err) {
       const float2 f = __half22float2(h[i]);
       x[2 * i] = f.x;
       x[2 * i + 1] = f.y;
+    }
+    if (a.kv_type == QSA_KV_Q4_0) {
+      float m = 0.f;
+      bool nan = false;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (fabsf(x[i]) > fabsf(m)) m = x[i];
+        nan |= x[i] != x[i];
+      }
+#pragma unroll
+      for (int o = 1; o <= 2; o <<= 1) {   // equal magnitudes: the lower lane's value
+        const float y = __shfl_xor_sync(kFull, m, o);
+        if (fabsf(y) > fabsf(m) || (fabsf(y) == fabsf(m) && (lane & o))) m = y;
+      }
+      // a NaN anywhere in a block makes its scale, and so every value, NaN
+      if ((__ballot_sync(kFull, nan) >> (lane & ~3)) & 15u) m = __int_as_float(0x7fffffff);
+      const float d = m * -0.125f;
+      const float inv = d != 0.f ? 1.0f / d : 0.f;
+      uint32_t n0 = 0u, n1 = 0u;   // the codes of values 0..3 and 4..7, a byte each
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float v0 = floorf(__fadd_rn(__fmul_rn(x[i], inv), 8.5f));
+        const float v1 = floorf(__fadd_rn(__fmul_rn(x[i + 4], inv), 8.5f));
+        n0 |= (uint32_t)fminf(fmaxf(v0, 0.f), 15.f) << (8 * i);
+        n1 |= (uint32_t)fminf(fmaxf(v1, 0.f), 15.f) << (8 * i);
+      }
+      // lanes 2 and 3 of a block hold its values 16..31: the high nibbles
+      n0 |= __shfl_down_sync(kFull, n0, 2) << 4;
+      n1 |= __shfl_down_sync(kFull, n1, 2) << 4;
+      grid_dep_wait();
+      if (ok && (lane & 2) == 0) {
+        const int64_t cg = c * a.G + g;
+        reinterpret_cast<uint2*>(cache + cg * (kHeadDim / 2) + (lane >> 2) * 16)[lane & 1] = make_uint2(n0, n1);
+        if ((lane & 1) == 0) {
+          __half* sc = reinterpret_cast<__half*>(cache + a.n_cells * (int64_t)a.G * (kHeadDim / 2));
+          sc[cg * (kHeadDim / 32) + (lane >> 2)] = __float2half_rn(d);
+        }
+      }
+      return;
     }
     float amax = 0.f;
 #pragma unroll
@@ -337,7 +379,7 @@ cudaError_t launch_append(const qsa_config& cfg, int n_new, const int32_t* tok_s
   a.n_new = n_new;
   a.G = cfg.n_kv_heads;
   a.r = cfg.compress_ratio;
-  a.kv_q8 = cfg.kv_type == QSA_KV_Q8_0;
+  a.kv_type = cfg.kv_type;
   a.tok_seq = tok_seq;
   a.tok_pos = tok_pos;
   a.cell = cell;
@@ -359,7 +401,8 @@ cudaError_t launch_append(const qsa_config& cfg, int n_new, const int32_t* tok_s
   a.norm_w = norm_w;
   a.pooled = pooled;
   a.eps = cfg.rms_eps;
-  const Turns turns = make_turns(cfg.rope_theta);
+  Turns turns{};
+  if (pooled != nullptr) turns = turns_of(cfg.rope_theta);
   const int64_t warps = (int64_t)n_new * (2 * cfg.n_kv_heads + 1);
   const unsigned blocks = (unsigned)ceil_div(warps, kAppWarps) + 1;   // + the dirty-list CTA
   prof_before(kKAppend, stream);

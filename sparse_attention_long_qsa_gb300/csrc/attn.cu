@@ -1396,7 +1396,9 @@ size_t attn_workspace_bytes(int, int, int) { return 0; }
 cudaError_t launch_sparse_attn(const AttnArgs& a, void*, unsigned* err, cudaStream_t stream) {
   if (a.n_tokens <= 0) return cudaSuccess;
   prof_before(kKAttn, stream);
-  cudaError_t e = a.kv_q8 ? launch_plain<true>(a, err, stream) : launch_plain<false>(a, err, stream);
+  cudaError_t e = a.kv_q4   ? launch_attn_q4(a, err, stream)
+                  : a.kv_q8 ? launch_plain<true>(a, err, stream)
+                            : launch_plain<false>(a, err, stream);
   prof_after(kKAttn, stream);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();

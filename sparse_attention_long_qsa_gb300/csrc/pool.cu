@@ -77,7 +77,7 @@ cudaError_t launch_pool_update(const qsa_config& cfg, const __half* idx_k, int64
                                cudaStream_t stream) {
   if (n_dirty <= 0) return cudaSuccess;
   const unsigned blocks = (unsigned)ceil_div(n_dirty, kPoolWarps);
-  const Turns turns = make_turns(cfg.rope_theta);
+  const Turns turns = turns_of(cfg.rope_theta);
   prof_before(kKPool, stream);
   cudaError_t e = launch_pdl(k_pool_update, dim3(blocks), dim3(kPoolWarps * 32), 0, stream, 1, idx_k, n_cells,
                              blk_cells, slot_block_idx, n_slots, dirty, n_dirty, norm_w, pooled,

@@ -44,6 +44,19 @@ inline Turns make_turns(float theta) {
   return turns;
 }
 
+// make_turns of the thread's last theta, kept: 64 powers and extended-precision
+// divisions cost the host more than a launch (long double is done in software
+// on aarch64).
+inline const Turns& turns_of(float theta) {
+  thread_local float of = 0.f;   // no valid theta is zero
+  thread_local Turns turns{};
+  if (of != theta) {
+    turns = make_turns(theta);
+    of = theta;
+  }
+  return turns;
+}
+
 // cos and sin of 2*pi*(u / 2^64): the fraction of a turn is split into an
 // fp32 hi part (top 24 bits, exact) and the rest, then
 //   sin(pi*(x_hi + x_lo)) ~ sinpi(x_hi) + pi*x_lo*cospi(x_hi)

@@ -204,7 +204,8 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
 // ------------------------------------------------------ measurement hook
 // Kernel ids of qsa_profile_kernel (include/qsa.h).
 enum KernelId : int { kKPool = 0, kKScore = 1, kKHist = 2, kKFinal = 3, kKAttn = 4, kKAppend = 5,
-                      kKFused = 6, kNumKernels = 7 };
+                      kKFused = 6, kKNormRope = 7, kKRead = 8, kKCopy = 9, kKFork = 10, kKSweep = 11,
+                      kNumKernels = 12 };
 struct ProfileHook {
   cudaEvent_t before[kNumKernels];
   cudaEvent_t after[kNumKernels];
@@ -277,6 +278,7 @@ struct AttnArgs {
   int n_tokens;
   int n_kv_heads;
   int kv_q8;
+  int kv_q4;
   const __half* q;
   const void* k_cache;
   const void* v_cache;
@@ -294,6 +296,8 @@ cudaError_t launch_sparse_attn(const AttnArgs& a, void* ws, unsigned* err, cudaS
 // (attn_union.cu); cells_pitch <= union_attn_max_pitch().
 cudaError_t launch_sparse_attn_union(const AttnArgs& a, unsigned* err, cudaStream_t stream);
 int union_attn_max_pitch();
+// Attention over a q4_0 cache (attn_q4.cu); launch_sparse_attn calls it.
+cudaError_t launch_attn_q4(const AttnArgs& a, unsigned* err, cudaStream_t stream);
 // qsa_index_attn: the qsa_index_topk kernels and the attention kernel, or
 // (in_cluster, when its limits hold: *fused = true) the score kernels and
 // then the selection and the attention in one cluster kernel.
@@ -313,5 +317,106 @@ cudaError_t launch_append(const qsa_config& cfg, int n_new, const int32_t* tok_s
                           int64_t n_slots, const int64_t* seq_blk_off, const int32_t* seq_blk_slots, int n_seq,
                           int32_t* dirty, int n_dirty, const int32_t* slot_block_idx, const float* norm_w,
                           float* pooled, unsigned* err, cudaStream_t stream);
+
+// Head norms with the rotation (norm_rope.cu).  Null inputs are skipped.
+struct NormRopeArgs {
+  int n_tokens;
+  int Hq, G;
+  const int32_t* pos;       // [n_axes][n_tokens]
+  const int32_t* idx_pos;   // [n_tokens]
+  const void* q_in;
+  int64_t q_stride;         // elements between a token's rows and the next token's
+  const void* k_in;
+  int64_t k_stride;
+  const void* qi_in;
+  int64_t qi_stride;
+  const float* q_w;
+  const float* k_w;
+  const float* qi_w;
+  __half* q;
+  __half* k;
+  float* qi;
+  float eps;
+};
+cudaError_t launch_norm_rope(const NormRopeArgs& a, const qsa_rope& rope, int elem, cudaStream_t stream);
+// theta^exponent / (2 pi) as a 64-bit fixed-point fraction of a turn.
+unsigned long long turn_of(double theta, double exponent);
+
+// Cache upkeep (cache_ops.cu).
+struct ReadArgs {
+  int n;
+  int G;
+  int kv_type;
+  const int32_t* cells;
+  const unsigned char* k_cache;
+  const unsigned char* v_cache;
+  int64_t n_cells;
+  __half* k_out;
+  __half* v_out;
+};
+cudaError_t launch_kv_read(const ReadArgs& a, unsigned* err, cudaStream_t stream);
+
+struct CopyArgs {
+  int n;
+  const int32_t* n_dev;     // may be null
+  const int32_t* src;
+  const int32_t* dst;
+  int64_t n_cells;
+  unsigned char* base[5];   // contiguous runs of a cell: K and V codes, K and V scales, indexer key
+  int len[5];               // 16-byte chunks per cell of each (0: none)
+  int chunks;               // their sum
+};
+cudaError_t launch_cells_copy(const CopyArgs& a, unsigned* err, cudaStream_t stream);
+
+struct ForkArgs {
+  int n;
+  int r;
+  const int32_t* src_seq;
+  const int32_t* dst_seq;
+  const int32_t* n_pos;
+  const int32_t* tail_slot;
+  const int32_t* tail_cells;
+  const int64_t* seq_blk_off;
+  int32_t* seq_blk_slots;
+  int n_seq;
+  int64_t n_list;
+  int32_t* blk_cells;
+  int32_t* slot_block_idx;
+  int64_t n_slots;
+  int64_t n_cells;
+  int64_t max_blocks;
+  int32_t* copy_src;
+  int32_t* copy_dst;
+};
+cudaError_t launch_seq_fork(const ForkArgs& a, unsigned* err, cudaStream_t stream);
+
+struct SweepArgs {
+  const int32_t* seq_len;
+  const int64_t* seq_blk_off;
+  const int32_t* seq_blk_slots;
+  int n_seq;
+  int64_t n_list;
+  const int32_t* blk_cells;
+  int32_t* blk_cells_out;
+  int64_t n_slots;
+  int64_t n_cells;
+  int r;
+  int compact;
+  int32_t* counts;
+  int32_t* cell_map;
+  int32_t* free_cells;
+  int32_t* free_slots;
+  int32_t* move_src;
+  int32_t* move_dst;
+  // workspace (launch_cache_sweep fills these)
+  unsigned* cell_bits;
+  unsigned* slot_bits;
+  unsigned* cell_sums;
+  unsigned* slot_sums;
+  int64_t cell_tiles;
+  int64_t slot_tiles;
+};
+size_t sweep_workspace_bytes(int64_t n_cells, int64_t n_slots);
+cudaError_t launch_cache_sweep(const SweepArgs& a, void* ws, unsigned* err, cudaStream_t stream);
 
 }  // namespace qsa

@@ -8,6 +8,10 @@ runs a step as the C-ABI calls on one stream:
     full_step:  kv_append(new cells, re-pooling the blocks they dirty) ->
                 index_attn(tokens)  (index top-k and sparse attention in one call)
 
+and around the steps: norm_rope (the step's q, k_new and q_idx from the
+projections), fork (a sequence sharing another's blocks) and release (freeing
+what no sequence holds, optionally moving the rest together).
+
 It holds no arithmetic of its own.
 """
 from __future__ import annotations
@@ -60,6 +64,7 @@ class QSALayer:
         self.ws_attn = torch.empty(qsa.sparse_attn_workspace_size(self.cfg, T),
                                    dtype=torch.uint8, device=device)
         self._dirty = None
+        self._heads = self._sweep = self._ws_sweep = None
 
     @classmethod
     def from_workload(cls, wl, step: int = 0, max_tokens: Optional[int] = None, device="cuda"):
@@ -139,6 +144,64 @@ class QSALayer:
         self.index_attn(tok_seq, tok_pos, q_idx, w_idx, q, recomputed="query_blocks", stream=stream,
                         in_cluster=in_cluster, out=out, union=union)
         return self.out[:int(tok_pos.numel())] if out is None else out
+
+    def norm_rope(self, rope, pos, q_in, k_in, q_norm_w, k_norm_w, q_idx_in, idx_pos, q_idx_norm_w, stream=None):
+        """Head norms and rotation of T tokens' projections into the layer's
+        buffers; returns (q, k_new, q_idx) as full_step takes them."""
+        T, c = int(q_in.shape[0]), self.cfgd
+        if self._heads is None or self._heads[0].shape[0] < T:
+            n = max(T, self.max_tokens)
+            new = lambda h, d, t: torch.empty((n, h, d), dtype=t, device=self.device)  # noqa: E731
+            self._heads = (new(c["n_q_heads"], c["head_dim"], torch.float16),
+                           new(c["n_kv_heads"], c["head_dim"], torch.float16),
+                           new(c["n_idx_heads"], c["idx_dim"], torch.float32))
+        q, k, qi = (x[:T] for x in self._heads)
+        qsa.qk_norm_rope(self.cfg, rope, pos, q_in, k_in, q_norm_w, k_norm_w, q, k, q_idx_in, idx_pos,
+                         q_idx_norm_w, qi, stream)
+        return q, k, qi
+
+    def kv_read(self, cells, stream=None):
+        """K and V rows of the listed cells as fp16 [n][n_kv_heads][head_dim]."""
+        shape = (int(cells.numel()), self.cfgd["n_kv_heads"], self.cfgd["head_dim"])
+        k, v = (torch.zeros(shape, dtype=torch.float16, device=self.device) for _ in range(2))
+        qsa.kv_read(self.cfg, cells, self.k_cache, self.v_cache, self.n_cells, k, v, stream)
+        return k, v
+
+    def fork(self, src_seq, dst_seq, n_pos, tail_slot, tail_cells, stream=None):
+        """Sequence dst_seq[f] becomes the first n_pos[f] positions of
+        src_seq[f] (int32 CUDA tensors; tail_cells [n_fork][r]): the block
+        lists and tables, and this layer's rows of the private tail cells.
+        Returns the (source, destination) cell pairs, for other layers."""
+        n, r = int(src_seq.numel()), self.cfgd["compress_ratio"]
+        pairs = torch.empty((2, n, r), dtype=torch.int32, device=self.device)
+        # the lists bound every sequence's blocks
+        qsa.seq_fork(self.cfg, src_seq, dst_seq, n_pos, tail_slot, tail_cells, self.seq_blk_off, self.seq_blk_slots,
+                     self.blk_cells, self.slot_block_idx, int(self.seq_blk_slots.numel()), pairs[0], pairs[1],
+                     self.n_cells, stream)
+        qsa.cells_copy(self.cfg, pairs[0], pairs[1], self.k_cache, self.v_cache, self.idx_k, self.n_cells,
+                       stream=stream)
+        return pairs[0], pairs[1]
+
+    def release(self, seq_len, compact=False, stream=None):
+        """Free what the sequences no longer hold (seq_len: int32 CUDA tensor,
+        positions each one keeps); compact: also move the held cells to the
+        front, this layer's rows with them.  Returns a dict of the sweep's
+        outputs (counts, cell_map, free_cells, free_slots, move_src, move_dst)."""
+        n, dev = self.n_cells, self.device
+        if self._sweep is None:
+            i32 = lambda m: torch.full((m,), -1, dtype=torch.int32, device=dev)  # noqa: E731
+            self._sweep = dict(counts=i32(4), cell_map=i32(n), free_cells=i32(n), free_slots=i32(self.n_slots),
+                               move_src=i32(n // 2), move_dst=i32(n // 2))
+            self._ws_sweep = torch.empty(qsa.cache_sweep_workspace_size(self.cfg, n, self.n_slots),
+                                         dtype=torch.uint8, device=dev)
+        s = self._sweep
+        qsa.cache_sweep(self.cfg, seq_len, self.seq_blk_off, self.seq_blk_slots, self.blk_cells, self.blk_cells, n,
+                        s["counts"], self._ws_sweep, compact, s["cell_map"], s["free_cells"], s["free_slots"],
+                        s["move_src"], s["move_dst"], stream)
+        if compact:
+            qsa.cells_copy(self.cfg, s["move_src"], s["move_dst"], self.k_cache, self.v_cache, self.idx_k, n,
+                           s["counts"][3:], stream)
+        return s
 
     def set_cells(self, slots, rows):
         """Write block-table rows (the append of new cells), device side."""

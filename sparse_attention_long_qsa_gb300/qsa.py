@@ -20,6 +20,8 @@ LIB_PATH = os.path.join(_HERE, "libqsa.so")
 QSA_OK = 0
 QSA_KV_F16 = 0
 QSA_KV_Q8_0 = 1
+QSA_KV_Q4_0 = 2
+QSA_SWEEP_COMPACT = 1
 QSA_HINT_QUERY_BLOCKS = -1
 QSA_INDEX_ATTN_IN_CLUSTER = 1
 QSA_INDEX_ATTN_UNION = 2
@@ -31,10 +33,13 @@ EXPORTS = ("qsa_config_init", "qsa_cells_per_token", "qsa_pool_update", "qsa_ind
            "qsa_index_topk_workspace_size", "qsa_index_topk", "qsa_index_topk_noalloc",
            "qsa_sparse_attn_workspace_size",
            "qsa_sparse_attn", "qsa_sparse_attn_union", "qsa_index_attn", "qsa_index_attn_kernels", "qsa_kv_append", "qsa_blocks_dirty",
+           "qsa_rope_init", "qsa_qk_norm_rope", "qsa_kv_read", "qsa_cells_copy", "qsa_seq_fork",
+           "qsa_cache_sweep_workspace_size", "qsa_cache_sweep",
            "qsa_debug_check", "qsa_profile_kernel", "qsa_index_topk_kernels", "qsa_status_string")
 
 # Kernel ids of qsa_profile_kernel.
-KERNELS = {"pool": 0, "score": 1, "hist": 2, "select": 3, "attn": 4, "append": 5, "select_attn": 6}
+KERNELS = {"pool": 0, "score": 1, "hist": 2, "select": 3, "attn": 4, "append": 5, "select_attn": 6,
+           "norm_rope": 7, "read": 8, "copy": 9, "fork": 10, "sweep": 11}
 
 
 class QSAError(RuntimeError):
@@ -50,6 +55,12 @@ class Config(ctypes.Structure):
                 ("top_k", ctypes.c_int32), ("rope_theta", ctypes.c_float),
                 ("rms_eps", ctypes.c_float), ("attn_scale", ctypes.c_float),
                 ("kv_type", ctypes.c_int32)]
+
+
+class Rope(ctypes.Structure):
+    """The rotation of the 256-dim heads (qsa_rope); made by rope_config."""
+    _fields_ = [("magic", ctypes.c_uint32), ("n_rot", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+                ("axis", ctypes.c_uint8 * 128), ("turns", ctypes.c_uint64 * 128), ("idx_turns", ctypes.c_uint64 * 64)]
 
 
 _lib = None
@@ -108,6 +119,22 @@ def _load():
     L.qsa_kv_append.argtypes = [CP, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P, _I64, _P, _P, _I32,
                                 _P, _I32, _P, _P, _P, _P]
     L.qsa_kv_append.restype = _I32
+    RP = ctypes.POINTER(Rope)
+    L.qsa_rope_init.argtypes = [CP, _I32, ctypes.POINTER(_I32), _I32, RP]
+    L.qsa_rope_init.restype = _I32
+    L.qsa_qk_norm_rope.argtypes = [CP, RP, _I32, _I32, _P, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _I64, _P, _P, _P]
+    L.qsa_qk_norm_rope.restype = _I32
+    L.qsa_kv_read.argtypes = [CP, _I32, _P, _P, _P, _I64, _P, _P, _P]
+    L.qsa_kv_read.restype = _I32
+    L.qsa_cells_copy.argtypes = [CP, _I32, _P, _P, _P, _P, _P, _P, _I64, _P]
+    L.qsa_cells_copy.restype = _I32
+    L.qsa_seq_fork.argtypes = [CP, _I32, _P, _P, _P, _P, _P, _P, _P, _I32, _I64, _P, _P, _I64, _I64, _I64, _P, _P, _P]
+    L.qsa_seq_fork.restype = _I32
+    L.qsa_cache_sweep_workspace_size.argtypes = [CP, _I64, _I64]
+    L.qsa_cache_sweep_workspace_size.restype = _SZ
+    L.qsa_cache_sweep.argtypes = [CP, ctypes.c_uint32, _P, _P, _P, _I32, _I64, _P, _P, _I64, _I64,
+                                  _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
+    L.qsa_cache_sweep.restype = _I32
     L.qsa_blocks_dirty.argtypes = [_P, _P, _I64, _I32, _P, _I32, ctypes.POINTER(_I32), _I32]
     L.qsa_blocks_dirty.restype = _I32
     L.qsa_debug_check.argtypes = [_P, ctypes.POINTER(ctypes.c_uint32)]
@@ -124,12 +151,12 @@ def _load():
 
 def config(**over) -> Config:
     """The qwen4exp QSA layer's configuration, with fields overridden by name
-    (kv_type may be given as "f16" / "q8_0")."""
+    (kv_type may be given as "f16" / "q8_0" / "q4_0")."""
     c = Config()
     _check(lib().qsa_config_init(ctypes.byref(c)), "qsa_config_init")
     for k, v in over.items():
         if k == "kv_type" and isinstance(v, str):
-            v = {"f16": QSA_KV_F16, "q8_0": QSA_KV_Q8_0}[v]
+            v = {"f16": QSA_KV_F16, "q8_0": QSA_KV_Q8_0, "q4_0": QSA_KV_Q4_0}[v]
         if not hasattr(c, k):
             raise KeyError(k)
         setattr(c, k, v)
@@ -155,7 +182,12 @@ def _stream(stream):
     return stream.cuda_stream
 
 
-def _ptr(t, dtype, name, allow_none=False, host_ok=False):
+def _elem_types():
+    import torch
+    return {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+
+def _ptr(t, dtype, name, allow_none=False, host_ok=False, strided=False):
     """Device address of a CUDA tensor on the current device.  host_ok: a
     step's own inputs and outputs may instead be page-locked (pinned) host
     tensors, which the kernels read and write in place over the host link."""
@@ -176,7 +208,7 @@ def _ptr(t, dtype, name, allow_none=False, host_ok=False):
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
+    if not strided and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
@@ -335,6 +367,181 @@ def kv_append(cfg, tok_seq, tok_pos, cells, k_new, v_new, idx_new, k_cache, v_ca
         _ptr(seq_blk_slots, torch.int32, "seq_blk_slots"), int(seq_blk_off.numel()) - 1,
         _ptr(dirty, torch.int32, "dirty"), int(dirty.numel()), *pool_args, _stream(stream))
     _check(st, "qsa_kv_append")
+
+
+def rope_config(sections, interleaved: bool = False, cfg: Optional[Config] = None) -> Rope:
+    """The rotation qk_norm_rope applies to the query and key heads, made once
+    per model: sections[a] pairs of dims turn by position axis a, dealt to the
+    axes one after the other or (interleaved) in turn; 2 * sum(sections) dims
+    of a head are rotated.  cfg: whose rope_theta (default config())."""
+    sec = [int(x) for x in sections]
+    r = Rope()
+    c = config() if cfg is None else cfg
+    _check(lib().qsa_rope_init(ctypes.byref(c), len(sec), (_I32 * max(len(sec), 1))(*sec), int(bool(interleaved)),
+                               ctypes.byref(r)), "qsa_rope_init")
+    return r
+
+
+def _head_rows(t, heads: int, dim: int, name: str):
+    """Address, tokens and token stride of a [T][heads][dim] tensor whose
+    heads are contiguous within a token (a slice of a fused projection)."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [T][{heads}][{dim}], got {list(t.shape)}")
+    s = t.stride()
+    if s[2] != 1 or (heads > 1 and s[1] != dim):
+        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {list(s)}")
+    return s[0]
+
+
+def qk_norm_rope(cfg, rope: Rope, pos, q_in, k_in, q_norm_w, k_norm_w, q, k_new, q_idx_in=None, idx_pos=None,
+                 q_idx_norm_w=None, q_idx=None, stream=None):
+    """Head norms and position rotation in one pass: q, k_new (fp16) and, if
+    given, q_idx (fp32) from the projections q_in [T][n_q_heads][head_dim],
+    k_in [T][n_kv_heads][head_dim] and q_idx_in [T][n_idx_heads][idx_dim]
+    (fp16, bf16 or fp32, one type; tokens may be strided).  pos: int32
+    [n_axes][T]; idx_pos: int32 [T].  q_in or k_in may be None (with its
+    output)."""
+    import torch
+    L = lib()
+    given = [x for x in (q_in, k_in, q_idx_in) if x is not None]
+    if not given:
+        raise ValueError("one of q_in, k_in and q_idx_in is required")
+    T, dt = int(given[0].shape[0]), given[0].dtype
+    elem = _elem_types().get(dt)
+    if elem is None:
+        raise TypeError(f"inputs must be fp16, bf16 or fp32, got {dt}")
+
+    def part(x, w, out, heads, dim, name, out_dtype):
+        if x is None:
+            if out is not None:
+                raise ValueError(f"the output of {name} is given without it")
+            return None, 0, None, None
+        stride = _head_rows(x, heads, dim, name)
+        if x.shape[0] != T or out is None or out.numel() != T * heads * dim:
+            raise ValueError(f"{name} and its output must hold {T} tokens")
+        if w is None or w.numel() != dim:
+            raise ValueError(f"the norm weight of {name} must hold {dim} values")
+        return (_ptr(x, dt, name, host_ok=True, strided=True), stride, _ptr(w, torch.float32, "norm weight"),
+                _io(out, out_dtype, "output"))
+
+    qp, qs, qw, qo = part(q_in, q_norm_w, q, cfg.n_q_heads, cfg.head_dim, "q_in", torch.float16)
+    kp, ks, kw, ko = part(k_in, k_norm_w, k_new, cfg.n_kv_heads, cfg.head_dim, "k_in", torch.float16)
+    ip, is_, iw, io = part(q_idx_in, q_idx_norm_w, q_idx, cfg.n_idx_heads, cfg.idx_dim, "q_idx_in", torch.float32)
+    if (qp or kp) and pos.numel() != rope.n_axes * T:
+        raise ValueError(f"pos must hold {rope.n_axes} x {T} positions")
+    if ip and idx_pos.numel() != T:
+        raise ValueError(f"idx_pos must hold {T} positions")
+    st = L.qsa_qk_norm_rope(
+        ctypes.byref(cfg), ctypes.byref(rope), T, elem, _io(pos, torch.int32, "pos") if pos is not None else None,
+        qp, qs, kp, ks, qw, kw, qo, ko, _io(idx_pos, torch.int32, "idx_pos") if idx_pos is not None else None,
+        ip, is_, iw, io, _stream(stream))
+    _check(st, "qsa_qk_norm_rope")
+
+
+def kv_read(cfg, cells, k_cache, v_cache, n_cells: int, k_out, v_out, stream=None):
+    """K and V rows of the listed cells as fp16 values, [n][n_kv_heads][head_dim]
+    each (entries < 0 are skipped)."""
+    import torch
+    n = int(cells.numel())
+    want = n * cfg.n_kv_heads * cfg.head_dim
+    if k_out.numel() != want or v_out.numel() != want:
+        raise ValueError(f"k_out and v_out must hold {n} rows")
+    _check_cache(cfg, k_cache, v_cache, n_cells)
+    st = lib().qsa_kv_read(ctypes.byref(cfg), n, _ptr(cells, torch.int32, "cells"), _ptr(k_cache, None, "k_cache"),
+                           _ptr(v_cache, None, "v_cache"), int(n_cells), _ptr(k_out, torch.float16, "k_out"),
+                           _ptr(v_out, torch.float16, "v_out"), _stream(stream))
+    _check(st, "qsa_kv_read")
+
+
+def cache_bytes(cfg, n_cells: int) -> int:
+    """Bytes of the K (or V) cache of n_cells cells."""
+    values = cfg.n_kv_heads * cfg.head_dim
+    return int(n_cells) * (2 * values if cfg.kv_type == QSA_KV_F16 else
+                           values + values // 16 if cfg.kv_type == QSA_KV_Q8_0 else values // 2 + values // 16)
+
+
+def _check_cache(cfg, k_cache, v_cache, n_cells: int):
+    need = cache_bytes(cfg, n_cells)
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t.numel() * t.element_size() < need:
+            raise ValueError(f"{name} holds {t.numel() * t.element_size()} bytes, {n_cells} cells need {need}")
+
+
+def cells_copy(cfg, src, dst, k_cache, v_cache, idx_k, n_cells: int, n_pairs=None, stream=None):
+    """Copy the K and V rows (as stored) and, unless idx_k is None, the
+    indexer key of cell src[i] to cell dst[i].  n_pairs: optional int32 CUDA
+    tensor of one element, how many of the pairs count."""
+    import torch
+    n = int(src.numel())
+    if dst.numel() != n:
+        raise ValueError("src and dst must have the same length")
+    _check_cache(cfg, k_cache, v_cache, n_cells)
+    if idx_k is not None and idx_k.numel() < int(n_cells) * cfg.idx_dim:
+        raise ValueError(f"idx_k must hold {n_cells} rows")
+    st = lib().qsa_cells_copy(
+        ctypes.byref(cfg), n, _ptr(n_pairs, torch.int32, "n_pairs", allow_none=True), _ptr(src, torch.int32, "src"),
+        _ptr(dst, torch.int32, "dst"), _ptr(k_cache, None, "k_cache"), _ptr(v_cache, None, "v_cache"),
+        _ptr(idx_k, torch.float16, "idx_k", allow_none=True), int(n_cells), _stream(stream))
+    _check(st, "qsa_cells_copy")
+
+
+def seq_fork(cfg, src_seq, dst_seq, n_pos, tail_slot, tail_cells, seq_blk_off, seq_blk_slots, blk_cells,
+             slot_block_idx, max_blocks: int, copy_src, copy_dst, n_cells: int = 2**31 - 1, stream=None):
+    """Sequence dst_seq[f] becomes the first n_pos[f] positions of src_seq[f]:
+    whole blocks shared, a partial last block private (tail_slot[f],
+    tail_cells[f]); copy_src / copy_dst [n_fork][r] get the pairs for
+    cells_copy."""
+    import torch
+    n, r = int(src_seq.numel()), cfg.compress_ratio
+    for t, name, want in ((dst_seq, "dst_seq", n), (n_pos, "n_pos", n), (tail_slot, "tail_slot", n),
+                          (tail_cells, "tail_cells", n * r), (copy_src, "copy_src", n * r),
+                          (copy_dst, "copy_dst", n * r)):
+        if t.numel() != want:
+            raise ValueError(f"{name} must hold {want} values")
+    n_slots = int(blk_cells.shape[0])
+    if blk_cells.numel() != n_slots * r or slot_block_idx.numel() < n_slots:
+        raise ValueError("blk_cells must be [n_slots][r] and slot_block_idx hold n_slots values")
+    st = lib().qsa_seq_fork(
+        ctypes.byref(cfg), n, _ptr(src_seq, torch.int32, "src_seq"), _ptr(dst_seq, torch.int32, "dst_seq"),
+        _ptr(n_pos, torch.int32, "n_pos"), _ptr(tail_slot, torch.int32, "tail_slot"),
+        _ptr(tail_cells, torch.int32, "tail_cells"), _ptr(seq_blk_off, torch.int64, "seq_blk_off"),
+        _ptr(seq_blk_slots, torch.int32, "seq_blk_slots"), int(seq_blk_off.numel()) - 1, int(seq_blk_slots.numel()),
+        _ptr(blk_cells, torch.int32, "blk_cells"), _ptr(slot_block_idx, torch.int32, "slot_block_idx"),
+        n_slots, int(n_cells), int(max_blocks),
+        _ptr(copy_src, torch.int32, "copy_src"), _ptr(copy_dst, torch.int32, "copy_dst"), _stream(stream))
+    _check(st, "qsa_seq_fork")
+
+
+def cache_sweep_workspace_size(cfg, n_cells: int, n_slots: int) -> int:
+    return int(lib().qsa_cache_sweep_workspace_size(ctypes.byref(cfg), int(n_cells), int(n_slots)))
+
+
+def cache_sweep(cfg, seq_len, seq_blk_off, seq_blk_slots, blk_cells, blk_cells_out, n_cells: int, counts, workspace,
+                compact: bool = False, cell_map=None, free_cells=None, free_slots=None, move_src=None,
+                move_dst=None, stream=None):
+    """Free what the sequences no longer hold (seq_len[s] positions each), and
+    with compact=True plan the moves that bring the held cells together:
+    counts[4] = held cells, free cells, free slots, moves; see qsa.h."""
+    import torch
+    n_slots, n = int(blk_cells.shape[0]), int(n_cells)
+    n_seq = int(seq_blk_off.numel()) - 1
+    for t, name, want in ((seq_len, "seq_len", n_seq), (counts, "counts", 4), (cell_map, "cell_map", n),
+                          (free_cells, "free_cells", n), (free_slots, "free_slots", n_slots),
+                          (move_src, "move_src", n // 2), (move_dst, "move_dst", n // 2),
+                          (blk_cells, "blk_cells", n_slots * cfg.compress_ratio),
+                          (blk_cells_out, "blk_cells_out", n_slots * cfg.compress_ratio)):
+        if t is not None and t.numel() < want:
+            raise ValueError(f"{name} must hold {want} values, got {t.numel()}")
+    i32 = torch.int32
+    st = lib().qsa_cache_sweep(
+        ctypes.byref(cfg), QSA_SWEEP_COMPACT if compact else 0, _ptr(seq_len, i32, "seq_len"),
+        _ptr(seq_blk_off, torch.int64, "seq_blk_off"), _ptr(seq_blk_slots, i32, "seq_blk_slots"), n_seq,
+        int(seq_blk_slots.numel()), _ptr(blk_cells, i32, "blk_cells"), _ptr(blk_cells_out, i32, "blk_cells_out"),
+        n_slots, n, _ptr(counts, i32, "counts"), _ptr(cell_map, i32, "cell_map", allow_none=True),
+        _ptr(free_cells, i32, "free_cells", allow_none=True), _ptr(free_slots, i32, "free_slots", allow_none=True),
+        _ptr(move_src, i32, "move_src", allow_none=True), _ptr(move_dst, i32, "move_dst", allow_none=True),
+        _ptr(workspace, torch.uint8, "workspace"), int(workspace.numel()), _stream(stream))
+    _check(st, "qsa_cache_sweep")
 
 
 def blocks_dirty(old_tbl: np.ndarray, new_tbl: np.ndarray, pad_pow2_min: int = 4) -> np.ndarray:
