@@ -43,22 +43,27 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kChunk = 16;                       // cells of one warp step
 constexpr int kRow = 144;                        // 128 B codes + 16 B scales: ldmatrix rows 144 B apart do not conflict
 constexpr int kStageBytes = 2 * kChunk * kRow;   // K rows, then V rows
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 constexpr int kMaxCluster = 16;
 constexpr float kLazy = 8.f;                     // log2 of how far a probability may exceed 1
+constexpr int kFixed = 4;                        // a CTA's prologue and merge, in chunks
 constexpr int kNoExp = 32;                       // no scale of V seen yet
 constexpr int kBlocks = kHeadDim / 32;           // q4_0 blocks of a row
 
+constexpr int kPitch = kHeadDim + 4;             // floats between two heads of a warp's o: its stores do not conflict
+
 template <int kWarps>
 struct Smem {
-  alignas(16) unsigned char stage[kWarps][kStages][kStageBytes];   // after the loop: each warp's o, fp32 [8][256]
+  alignas(16) unsigned char stage[kWarps][kStages][kStageBytes];   // after the loop: each warp's o, fp32 [8][kPitch]
+  uint4 q[kBlocks][2][32];                       // a lane's query fragment of a block and step: {a0, 0, a2, 0}
+  float4 kd[kWarps][kBlocks][4];                 // a chunk's K scales: block, l4 -> cells 2 l4 + {0, 1, 8, 9}
+  uint2 vd[kWarps][kBlocks][4];                  // its V scales times 2^wexp, the same as four halves
   float m[kWarps][kGqa], l[kWarps][kGqa];
-  int k[kWarps];                                 // exponent of the warp's weights
-  float po[kMaxCluster * kGqa * (kHeadDim / kMaxCluster)];   // the cluster's partials of this CTA's dims
-  float pm[kMaxCluster][2 * kGqa];               // their (max, sum)
+  alignas(16) float po[kGqa * kHeadDim];         // the cluster's partials of this CTA's dims: [NC][8][256 / NC]
+  alignas(16) float pm[kMaxCluster][2 * kGqa];   // their (max, sum)
   float w[kMaxCluster][kGqa];
 };
-static_assert(kStages * kStageBytes >= kGqa * kHeadDim * 4, "a warp's o fits in its stages");
+static_assert(kStages * kStageBytes >= kGqa * kPitch * 4, "a warp's o fits in its stages");
 
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
@@ -72,11 +77,45 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4])
                : "r"(addr)
                : "memory");
 }
+__device__ __forceinline__ void ldmatrix2(uint32_t addr, uint32_t (&r)[2]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];\n" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix2_trans(uint32_t addr, uint32_t (&r)[2]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];\n"
+               : "=r"(r[0]), "=r"(r[1])
+               : "r"(addr)
+               : "memory");
+}
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same from zero.
+__device__ __forceinline__ void mma0(float (&c)[4], uint4 a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+               : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+               : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
+}
+// 2^x; results below the normal range are zero
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+// (x & m) | o in one instruction
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t o) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;\n" : "=r"(r) : "r"(x), "r"(m), "r"(o));
+  return r;
+}
+// s += d * c, two fp32 values each
+__device__ __forceinline__ void fma2(float2& s, float dx, float dy, float cx, float cy) {
+  asm("{\n .reg .b64 s, d, c;\n mov.b64 s, {%0, %1};\n mov.b64 d, {%2, %3};\n mov.b64 c, {%4, %5};\n"
+      " fma.rn.f32x2 s, d, c, s;\n mov.b64 {%0, %1}, s;\n}\n"
+      : "+f"(s.x), "+f"(s.y)
+      : "f"(dx), "f"(dy), "f"(cx), "f"(cy));
 }
 __device__ __forceinline__ uint32_t bits(__half2 h) {
   uint32_t u;
@@ -95,7 +134,7 @@ __device__ __forceinline__ __half2 pow2h(int k) {
 }
 
 template <int kWarps>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, 12 / kWarps)
 k_attn_q4(const AttnArgs a, unsigned* err) {
   extern __shared__ unsigned char smem_raw[];
   Smem<kWarps>& sm = *reinterpret_cast<Smem<kWarps>*>(smem_raw);
@@ -105,34 +144,37 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
   const int g = blockIdx.y, t = blockIdx.z;
   const uint32_t rank = cluster_rank(), NC = cluster_size();
   const int G = a.n_kv_heads, Hq = G * kGqa;
+
   // ---- the query fragments of head gid (an input: read before the wait).
   // Block b, step s: k index 2 l4 + {0, 1} is dim 32 b + 4 l4 + s + {0, 2},
   // k index 8 + 2 l4 + {0, 1} the dim 16 further (divided by 16).  A power of
-  // two per head brings its largest query to [2^14, 2^15) first, so that small
-  // queries keep their bits through that division.
-  uint32_t qa[kBlocks][2][2];
-  float qbias[kBlocks];
-  float scale;   // of a score, to the log2 domain: without the queries' and the codes' powers of two
+  // two per head brings its largest query to [2^6, 2^7) first, so that small
+  // queries keep their bits through that division and -8 * (a block's sum)
+  // stays in range.
+  float scale0, scale24;      // of a score, to the log2 domain: without the queries' (and the codes') power of two
+  uint32_t bias_hi = 0u, bias_lo = 0u;   // -8 * the sums of blocks 2 l4, 2 l4 + 1, in two parts
   {
     const __half* q = a.q + ((int64_t)t * Hq + g * kGqa + gid) * kHeadDim;
+    uint32_t x[kBlocks][2][2];
     __half2 qmax = __float2half2_rn(0.f);
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
       const uint2 lo = *reinterpret_cast<const uint2*>(q + 32 * b + 4 * l4);
       const uint2 hi = *reinterpret_cast<const uint2*>(q + 32 * b + 16 + 4 * l4);
-      qa[b][0][0] = __byte_perm(lo.x, lo.y, 0x5410);
-      qa[b][1][0] = __byte_perm(lo.x, lo.y, 0x7632);
-      qa[b][0][1] = __byte_perm(hi.x, hi.y, 0x5410);
-      qa[b][1][1] = __byte_perm(hi.x, hi.y, 0x7632);
+      x[b][0][0] = __byte_perm(lo.x, lo.y, 0x5410);
+      x[b][1][0] = __byte_perm(lo.x, lo.y, 0x7632);
+      x[b][0][1] = __byte_perm(hi.x, hi.y, 0x5410);
+      x[b][1][1] = __byte_perm(hi.x, hi.y, 0x7632);
       qmax = __hmax2(qmax, __hmax2(__habs2(half2_of(lo.x)), __habs2(half2_of(lo.y))));
       qmax = __hmax2(qmax, __hmax2(__habs2(half2_of(hi.x)), __habs2(half2_of(hi.y))));
     }
     qmax = __hmax2(qmax, half2_of(__shfl_xor_sync(kFull, bits(qmax), 1)));
     qmax = __hmax2(qmax, half2_of(__shfl_xor_sync(kFull, bits(qmax), 2)));
-    const int e = 29 - (int)((bits(__hmax2(qmax, __lowhigh2highlow(qmax))) & 0x7fffu) >> 10);   // -2 .. 29
+    const int e = 21 - (int)((bits(__hmax2(qmax, __lowhigh2highlow(qmax))) & 0x7fffu) >> 10);   // -10 .. 21
     const int e0 = min(e, 15);
     const __half2 up0 = pow2h(e0), up1 = pow2h(e - e0), sixteenth = __float2half2_rn(0.0625f);
-    scale = a.attn_scale * 1.4426950408889634f * exp2f((float)(24 - e));
+    scale0 = a.attn_scale * 1.4426950408889634f * exp2f((float)-e);
+    scale24 = scale0 * 16777216.0f;
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
       float s = 0.f;
@@ -140,14 +182,23 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const __half2 x = __hmul2(__hmul2(half2_of(qa[b][i][j]), up0), up1);
-          const float2 f = __half22float2(x);
+          const __half2 y = __hmul2(__hmul2(half2_of(x[b][i][j]), up0), up1);
+          const float2 f = __half22float2(y);
           s += f.x + f.y;
-          qa[b][i][j] = bits(j ? __hmul2(x, sixteenth) : x);
+          x[b][i][j] = bits(j ? __hmul2(y, sixteenth) : y);
         }
+      if (b % kWarps == warp) {
+        sm.q[b][0][lane] = make_uint4(x[b][0][0], 0u, x[b][0][1], 0u);
+        sm.q[b][1][lane] = make_uint4(x[b][1][0], 0u, x[b][1][1], 0u);
+      }
       s += __shfl_xor_sync(kFull, s, 1);
       s += __shfl_xor_sync(kFull, s, 2);
-      qbias[b] = s * (-8.0f / 16777216.0f);
+      s *= -8.f;
+      const __half h = __float2half_rn(s), l = __float2half_rn(s - __half2float(h));
+      if ((b >> 1) == l4) {
+        bias_hi |= (uint32_t)__half_as_ushort(h) << (16 * (b & 1));
+        bias_lo |= (uint32_t)__half_as_ushort(l) << (16 * (b & 1));
+      }
     }
   }
   cluster_arrive();   // waited for before anything is pushed to a peer
@@ -160,36 +211,50 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
   // chunks go round the cluster's CTAs first, so a short list uses all of them
   const int first = warp * (int)NC + (int)rank, step = kWarps * (int)NC;
 
+  const uint32_t ring = smem_u32(sm.stage[warp]);
   const unsigned char* kc = static_cast<const unsigned char*>(a.k_cache);
   const unsigned char* vc = static_cast<const unsigned char*>(a.v_cache);
-  const int64_t codes = a.n_cells * (int64_t)G * (kHeadDim / 2);   // where the scales start
-  const uint32_t ring = smem_u32(sm.stage[warp]);
+  const uint32_t pitch = (uint32_t)G * (kHeadDim / 2);                          // code bytes of a cell
+  // Eight lanes copy a row's codes: a copy of whole 128-byte lines costs the
+  // load unit a quarter of one that touches 16 lines in part.
+  const unsigned char* kcodes = kc + g * (kHeadDim / 2) + (lane & 7) * 16;
+  const unsigned char* vcodes = vc + g * (kHeadDim / 2) + (lane & 7) * 16;
+  const unsigned char* scales = (lane < 16 ? kc : vc) + a.n_cells * (int64_t)pitch + g * (2 * kBlocks);
 
-  // the ids of a chunk: lanes i and i + 16 hold cell i (-1: none)
-  auto cell_of = [&](int chunk) -> int {
+  // the ids of a chunk as listed, lanes i and i + 16 holding cell i (past the
+  // list: kPast); looked at only a step later, so that nothing waits on the load
+  constexpr int kPast = (int)0x80000000u;
+  auto listed = [&](int chunk) -> int {
     const int i = chunk * kChunk + (lane & 15);
-    if (chunk >= n_chunks || i >= cnt) return -1;
-    const int c = crow[i];
-    if (c < 0 || c >= a.n_cells) {
-      atomicOr(err, kErrCell);
-      return -1;
-    }
-    return c;
+    return i < cnt ? crow[i] : kPast;
+  };
+  auto checked = [&](int c) -> int {
+    if ((unsigned)c < (unsigned)a.n_cells) return c;
+    if (c != kPast) atomicOr(err, kErrCell);
+    return -1;
   };
   // copies a chunk's rows into a stage; missing cells become zeros
-  auto fetch = [&](int cell, int st) {
+  auto fetch = [&](int cell, unsigned ok, int st) {
     const uint32_t dst = ring + (uint32_t)st * kStageBytes;
+    const uint32_t at = dst + (lane >> 3) * kRow + (lane & 7) * 16;
+    const uint32_t id = (uint32_t)max(cell, 0);
+    cp_async16(dst + lane * kRow + 128, scales + (uint64_t)id * (pitch >> 3), cell >= 0);
+    if (ok == kFull) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = 4 * i + (lane >> 3);
-      const int c = __shfl_sync(kFull, cell, row);
-      const int64_t off = ((int64_t)(c < 0 ? 0 : c) * G + g) * (kHeadDim / 2) + (lane & 7) * 16;
-      const uint32_t at = dst + row * kRow + (lane & 7) * 16;
-      cp_async16(at, kc + off, c >= 0);
-      cp_async16(at + kChunk * kRow, vc + off, c >= 0);
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t off = (uint64_t)__shfl_sync(kFull, id, 4 * i + (lane >> 3)) * pitch;
+        cp_async16(at + 4 * i * kRow, kcodes + off, true);
+        cp_async16(at + (4 * i + kChunk) * kRow, vcodes + off, true);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t off = (uint64_t)__shfl_sync(kFull, id, 4 * i + (lane >> 3)) * pitch;
+        const bool have = (ok >> (4 * i + (lane >> 3))) & 1u;
+        cp_async16(at + 4 * i * kRow, kcodes + off, have);
+        cp_async16(at + (4 * i + kChunk) * kRow, vcodes + off, have);
+      }
     }
-    const int64_t off = codes + ((int64_t)(cell < 0 ? 0 : cell) * G + g) * (2 * kBlocks);
-    cp_async16(dst + lane * kRow + 128, (lane < 16 ? kc : vc) + off, cell >= 0);
   };
 
   float acc[kBlocks][2][4];
@@ -201,103 +266,112 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
       for (int j = 0; j < 4; ++j) acc[b][i][j] = 0.f;
   float run_m = -INFINITY, run_l = 0.f;   // head gid; run_l: this thread's cells only
   int wexp = kNoExp;                      // weights carry 2^wexp
-  unsigned long long valid = 0;           // of the chunks in flight, oldest first: which of the 16 cells exist
+  unsigned valid[kStages - 1] = {};       // of the chunks in flight, oldest first: which of the 16 cells exist
 
-  int ahead = cell_of(first);
+  int ahead = listed(first);
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) {
     const int chunk = first + s * step;
     if (chunk < n_chunks) {
-      valid |= (unsigned long long)(__ballot_sync(kFull, ahead >= 0) & 0xffffu) << (16 * s);
-      fetch(ahead, s);
+      const int cell = checked(ahead);
+      valid[s] = __ballot_sync(kFull, cell >= 0);
+      fetch(cell, valid[s], s);
     }
     asm volatile("cp.async.commit_group;\n" ::: "memory");
-    ahead = cell_of(chunk + step);
+    ahead = listed(chunk + step);
   }
+  __syncthreads();   // the query fragments are in place
 
   int st = 0;
 #pragma unroll 1
   for (int chunk = first; chunk < n_chunks; chunk += step) {
     asm volatile("cp.async.wait_group %0;\n" ::"n"(kStages - 2) : "memory");
     __syncwarp();   // every lane's copies of this stage are in; the stage fetched next has been read by all
-    const unsigned ok = (unsigned)valid & 0xffffu;
-    valid >>= 16;
+    const unsigned ok = valid[0];   // bits i and i + 16: cell i
+#pragma unroll
+    for (int i = 0; i + 1 < kStages - 1; ++i) valid[i] = valid[i + 1];
     {
       const int nchunk = chunk + (kStages - 1) * step;
       if (nchunk < n_chunks) {
-        valid |= (unsigned long long)(__ballot_sync(kFull, ahead >= 0) & 0xffffu) << (16 * (kStages - 2));
-        fetch(ahead, st == 0 ? kStages - 1 : st - 1);
+        const int cell = checked(ahead);
+        valid[kStages - 2] = __ballot_sync(kFull, cell >= 0);
+        fetch(cell, valid[kStages - 2], st == 0 ? kStages - 1 : st - 1);
       }
       asm volatile("cp.async.commit_group;\n" ::: "memory");
-      ahead = cell_of(nchunk + step);
+      ahead = listed(nchunk + step);
     }
     const uint32_t sk = ring + (uint32_t)st * kStageBytes, sv = sk + kChunk * kRow;
     st = st == kStages - 1 ? 0 : st + 1;
 
+    // ---- the chunk's scales, laid out once for all lanes.  ldmatrix gives this
+    // thread those of cells 2 l4 + {0, 1, 8, 9} in block gid.
+    float off[2][4];
+    __half2 dv[2];
+    {
+      uint32_t d[2];
+      ldmatrix2(sk + (lane & 15) * kRow + 128, d);   // cell 8 j + gid, blocks 2 l4, 2 l4 + 1
+      // the codes' offset: sum over the blocks of d_K * (-8 * sum of q), k = block, once per part
+      const uint4 bias = make_uint4(bias_hi, 0u, bias_lo, 0u);
+      mma0(off[0], bias, d[0], d[0]);
+      mma0(off[1], bias, d[1], d[1]);
+      ldmatrix2_trans(sk + (lane & 15) * kRow + 128, d);
+      const float2 d0 = __half22float2(half2_of(d[0])), d1 = __half22float2(half2_of(d[1]));
+      sm.kd[warp][gid][l4] = make_float4(d0.x, d0.y, d1.x, d1.y);
+      ldmatrix2_trans(sv + (lane & 15) * kRow + 128, d);
+      dv[0] = half2_of(d[0]), dv[1] = half2_of(d[1]);
+    }
+    // the largest scale of V sets the weights' exponent: d_max * 2^want lies in
+    // [2^5, 2^6) (or below, at the exponent's ends)
+    const uint32_t dm = bits(__hmax2(__habs2(dv[0]), __habs2(dv[1])));
+    const uint32_t db = __reduce_max_sync(kFull, max(dm >> 16, dm & 0xffffu));
+    const int want = min(15, max(-10, 20 - (int)(db >> 10)));
+    const int nexp = db != 0u && want < wexp - 1 ? want : wexp;
+    {
+      const __half2 up = pow2h(nexp == kNoExp ? 0 : nexp);
+      sm.vd[warp][gid][l4] = make_uint2(bits(__hmul2(dv[0], up)), bits(__hmul2(dv[1], up)));
+    }
+    __syncwarp();
+
     // ---- scores: s[j][e] = q_gid . K of cell 8 j + 2 l4 + e
-    float s[2][2] = {};
+    float2 s[2] = {};
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      uint32_t dk[2][4];   // scales of the two cells, 8 halves each
+    for (int bq = 0; bq < 2; ++bq) {   // four blocks: lane l's address is row l % 8 of block 4 bq + l / 8
+      uint32_t w[2][4];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t at = sk + (8 * j + 2 * l4 + e) * kRow + 128;
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n"
-                     : "=r"(dk[e][0]), "=r"(dk[e][1]), "=r"(dk[e][2]), "=r"(dk[e][3])
-                     : "r"(at)
-                     : "memory");
-      }
+      for (int j = 0; j < 2; ++j) ldmatrix4(sk + (8 * j + (lane & 7)) * kRow + (4 * bq + (lane >> 3)) * 16, w[j]);
 #pragma unroll
-      for (int bq = 0; bq < 2; ++bq) {   // four blocks: lane l's address is row l % 8 of block 4 bq + l / 8
-        uint32_t w[4];
-        ldmatrix4(sk + (8 * j + (lane & 7)) * kRow + (4 * bq + (lane >> 3)) * 16, w);
+      for (int i = 0; i < 4; ++i) {
+        const int b = 4 * bq + i;
+        const uint4 q0 = sm.q[b][0][lane], q1 = sm.q[b][1][lane];
+        const float4 d = sm.kd[warp][b][l4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int b = 4 * bq + i;
-          float c[4] = {qbias[b], qbias[b], 0.f, 0.f};   // rows 8..15 (no head) are not used
-          mma(c, qa[b][0][0], 0u, qa[b][0][1], 0u, w[i] & 0x000f000fu, w[i] & 0x00f000f0u);
-          const uint32_t u = w[i] >> 8;
-          mma(c, qa[b][1][0], 0u, qa[b][1][1], 0u, u & 0x000f000fu, u & 0x00f000f0u);
-          const float2 d0 = __half22float2(half2_of(dk[0][b >> 1])), d1 = __half22float2(half2_of(dk[1][b >> 1]));
-          s[j][0] = fmaf((b & 1) ? d0.y : d0.x, c[0], s[j][0]);
-          s[j][1] = fmaf((b & 1) ? d1.y : d1.x, c[1], s[j][1]);
+        for (int j = 0; j < 2; ++j) {
+          float c[4];   // rows 8..15 (no head) are not used
+          mma0(c, q0, w[j][i] & 0x000f000fu, w[j][i] & 0x00f000f0u);
+          const uint32_t u = w[j][i] >> 8;
+          mma(c, q1.x, q1.y, q1.z, q1.w, u & 0x000f000fu, u & 0x00f000f0u);
+          fma2(s[j], j ? d.z : d.x, j ? d.w : d.y, c[0], c[1]);
         }
       }
     }
     // ---- softmax of head gid over the 16 cells (a quad holds them)
-    float p[2][2], cm = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 2; ++j) {
+      s[j].x = fmaf(off[j][0], scale0, s[j].x * scale24);
+      s[j].y = fmaf(off[j][1], scale0, s[j].y * scale24);
+    }
+    if (ok != kFull) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        s[j][e] = ((ok >> (8 * j + 2 * l4 + e)) & 1u) ? s[j][e] * scale : -INFINITY;
-        cm = fmaxf(cm, s[j][e]);
-      }
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (!((ok >> (8 * j + 2 * l4 + e)) & 1u)) (e ? s[j].y : s[j].x) = -INFINITY;
+    }
+    float cm = fmaxf(fmaxf(s[0].x, s[0].y), fmaxf(s[1].x, s[1].y));
     cm = fmaxf(cm, __shfl_xor_sync(kFull, cm, 1));
     cm = fmaxf(cm, __shfl_xor_sync(kFull, cm, 2));
-    // scales of V: their largest magnitude sets the weights' exponent
-    uint32_t dv[2][2][4];
-    __half2 dmax = __float2half2_rn(0.f);
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t at = sv + (8 * j + 2 * l4 + e) * kRow + 128;
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n"
-                     : "=r"(dv[j][e][0]), "=r"(dv[j][e][1]), "=r"(dv[j][e][2]), "=r"(dv[j][e][3])
-                     : "r"(at)
-                     : "memory");
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dmax = __hmax2(dmax, __habs2(half2_of(dv[j][e][i])));
-      }
-    dmax = __hmax2(dmax, half2_of(__shfl_xor_sync(kFull, bits(dmax), 1)));
-    dmax = __hmax2(dmax, half2_of(__shfl_xor_sync(kFull, bits(dmax), 2)));
-    const uint32_t db = bits(__hmax2(dmax, __lowhigh2highlow(dmax))) & 0x7fffu;
-    // d_max * 2^want lies in [2^5, 2^6) (or below, at the exponent's ends)
-    const int want = min(15, max(-10, 20 - (int)(db >> 10)));
     const bool grow = cm > run_m + kLazy;
-    if (__any_sync(kFull, grow) || (db != 0u && want < wexp - 1)) {
-      const int nexp = db != 0u && want < wexp - 1 ? want : wexp;
+    if (__any_sync(kFull, grow) || nexp != wexp) {
       const float nm = grow ? cm : run_m;
       const float f = run_m == -INFINITY ? 0.f : exp2f(run_m - nm);
       run_l *= f;
@@ -313,19 +387,16 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
           acc[b][i][2] *= f0, acc[b][i][3] *= f1;
         }
     }
+    const float base = run_m == -INFINITY ? 0.f : run_m;   // no cell yet: every s is -inf
     __half2 ph[2], pl[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        p[j][e] = run_m == -INFINITY ? 0.f : exp2f(s[j][e] - run_m);
-        run_l += p[j][e];
-      }
-      ph[j] = __floats2half2_rn(p[j][0], p[j][1]);
+      const float p0 = ex2(s[j].x - base), p1 = ex2(s[j].y - base);
+      run_l += p0 + p1;
+      ph[j] = __floats2half2_rn(p0, p1);
       const float2 h = __half22float2(ph[j]);
-      pl[j] = __floats2half2_rn(p[j][0] - h.x, p[j][1] - h.y);
+      pl[j] = __floats2half2_rn(p0 - h.x, p1 - h.y);
     }
-    const __half2 up = pow2h(wexp == kNoExp ? 0 : wexp);
 
     // ---- o^T[dim][head] += V^T . w, per block of 32 dims: tile i, row gid is
     // dim 32 b + 2 gid + i, row gid + 8 the dim 16 further (16 times too large)
@@ -336,24 +407,22 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int b = 2 * bp + i;
-        uint32_t wh[2], wl[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const __half2 d = __hmul2(half2_of(__byte_perm(dv[j][0][b >> 1], dv[j][1][b >> 1], (b & 1) ? 0x7632 : 0x5410)), up);
-          const __half2 h = __hmul2(ph[j], d);
-          wh[j] = bits(h);
-          wl[j] = bits(__hfma2(pl[j], d, __hfma2(ph[j], d, __hneg2(h))));
-        }
+        const uint2 d = sm.vd[warp][b][l4];
+        const __half2 d0 = half2_of(d.x), d1 = half2_of(d.y);
+        const __half2 h0 = __hmul2(ph[0], d0), h1 = __hmul2(ph[1], d1);
+        const uint32_t wh0 = bits(h0), wh1 = bits(h1);
+        const uint32_t wl0 = bits(__hfma2(pl[0], d0, __hfma2(ph[0], d0, __hneg2(h0))));
+        const uint32_t wl1 = bits(__hfma2(pl[1], d1, __hfma2(ph[1], d1, __hneg2(h1))));
         const __half2 c1 = half2_of(0x64086408u), c16 = half2_of(0x64806480u);   // 1024 + 8, 1024 + 128
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const uint32_t x0 = k ? v[2 * i] >> 8 : v[2 * i], x1 = k ? v[2 * i + 1] >> 8 : v[2 * i + 1];
-          const uint32_t a0 = bits(__hsub2(half2_of((x0 & 0x000f000fu) | 0x64006400u), c1));
-          const uint32_t a1 = bits(__hsub2(half2_of((x0 & 0x00f000f0u) | 0x64006400u), c16));
-          const uint32_t a2 = bits(__hsub2(half2_of((x1 & 0x000f000fu) | 0x64006400u), c1));
-          const uint32_t a3 = bits(__hsub2(half2_of((x1 & 0x00f000f0u) | 0x64006400u), c16));
-          mma(acc[b][k], a0, a1, a2, a3, wh[0], wh[1]);
-          mma(acc[b][k], a0, a1, a2, a3, wl[0], wl[1]);
+          const uint32_t a0 = bits(__hsub2(half2_of(and_or(x0, 0x000f000fu, 0x64006400u)), c1));
+          const uint32_t a1 = bits(__hsub2(half2_of(and_or(x0, 0x00f000f0u, 0x64006400u)), c16));
+          const uint32_t a2 = bits(__hsub2(half2_of(and_or(x1, 0x000f000fu, 0x64006400u)), c1));
+          const uint32_t a3 = bits(__hsub2(half2_of(and_or(x1, 0x00f000f0u, 0x64006400u)), c16));
+          mma(acc[b][k], a0, a1, a2, a3, wh0, wh1);
+          mma(acc[b][k], a0, a1, a2, a3, wl0, wl1);
         }
       }
     }
@@ -368,52 +437,72 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
     sm.l[warp][gid] = run_l;
   }
   __syncthreads();   // also: every warp is done with its stages
-  float cta_m[2];    // of heads 2 l4, 2 l4 + 1
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    cta_m[e] = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) cta_m[e] = fmaxf(cta_m[e], sm.m[w][2 * l4 + e]);
-  }
   {
-    float* o = reinterpret_cast<float*>(sm.stage[warp]);   // [8][256]
+    float* o = reinterpret_cast<float*>(sm.stage[warp]);   // [8][kPitch]
     const float back = wexp == kNoExp ? 0.f : exp2f((float)-wexp);
-    float f[2];
+    float f[2];   // of heads 2 l4, 2 l4 + 1
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm.m[w][2 * l4 + e]);
       const float mw = sm.m[warp][2 * l4 + e];
-      f[e] = mw == -INFINITY ? 0.f : exp2f(mw - cta_m[e]) * back;
+      f[e] = mw == -INFINITY ? 0.f : exp2f(mw - m) * back;
     }
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int e = 0; e < 2; ++e) {
+        float* p = o + (2 * l4 + e) * kPitch + 32 * b + 2 * gid;
+        *reinterpret_cast<float2*>(p) = make_float2(acc[b][0][e] * f[e], acc[b][1][e] * f[e]);
+        *reinterpret_cast<float2*>(p + 16) =
+            make_float2(acc[b][0][2 + e] * (f[e] * 0.0625f), acc[b][1][2 + e] * (f[e] * 0.0625f));
+      }
+  }
+  // the CTA's (max, sum) of head h in threads h < 8
+  float cta_m = -INFINITY, cta_l = 0.f;
+  if (tid < kGqa) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          o[(2 * l4 + e) * kHeadDim + 32 * b + 2 * gid + i] = acc[b][i][e] * f[e];
-          o[(2 * l4 + e) * kHeadDim + 32 * b + 2 * gid + i + 16] = acc[b][i][2 + e] * f[e] * 0.0625f;
-        }
+    for (int w = 0; w < kWarps; ++w) cta_m = fmaxf(cta_m, sm.m[w][tid]);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+      cta_l += sm.m[w][tid] == -INFINITY ? 0.f : sm.l[w][tid] * exp2f(sm.m[w][tid] - cta_m);
+    if (NC == 1) sm.w[0][tid] = cta_l != 0.f ? 1.0f / cta_l : 0.f;
   }
   __syncthreads();
-  cluster_wait();   // every CTA of the cluster runs
-  // thread h < 8: the CTA's (max, sum) of head h to every CTA of the cluster
-  if (tid < kGqa) {
-    float m = -INFINITY, l = 0.f;
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm.m[w][tid]);
-    for (int w = 0; w < kWarps; ++w) l += sm.m[w][tid] == -INFINITY ? 0.f : sm.l[w][tid] * exp2f(sm.m[w][tid] - m);
-    for (uint32_t r = 0; r < NC; ++r) {
-      st_dsmem_f32(dsmem_addr(&sm.pm[rank][tid], r), m);
-      st_dsmem_f32(dsmem_addr(&sm.pm[rank][kGqa + tid], r), l);
+  // four dims of a head, summed over the warps
+  auto sum4 = [&](int i) -> float4 {
+    const int h = i >> 6, d = (i & 63) * 4;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm.stage[w]) + h * kPitch + d);
+      o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
     }
+    return o;
+  };
+  float* out = a.out + ((int64_t)t * Hq + g * kGqa) * kHeadDim;
+  if (NC == 1) {
+    for (int i = tid; i < kGqa * kHeadDim / 4; i += kThreads) {
+      const float4 o = sum4(i);
+      const float w = sm.w[0][i >> 6];
+      reinterpret_cast<float4*>(out)[i] = make_float4(o.x * w, o.y * w, o.z * w, o.w * w);
+    }
+    cluster_wait();
+    return;
   }
+  cluster_wait();   // every CTA of the cluster runs
+  if (tid < kGqa)
+    for (uint32_t r = 0; r < NC; ++r) {
+      st_dsmem_f32(dsmem_addr(&sm.pm[rank][tid], r), cta_m);
+      st_dsmem_f32(dsmem_addr(&sm.pm[rank][kGqa + tid], r), cta_l);
+    }
   // partial o: dims [r * 256 / NC, ...) go to CTA r
   const int dpc = kHeadDim / (int)NC;
-  for (int i = tid; i < kGqa * kHeadDim; i += kThreads) {
-    float o = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) o += reinterpret_cast<const float*>(sm.stage[w])[i];
-    const int h = i >> 8, d = i & (kHeadDim - 1);
-    st_dsmem_f32(dsmem_addr(&sm.po[((int)rank * kGqa + h) * dpc + d % dpc], (uint32_t)(d / dpc)), o);
+  for (int i = tid; i < kGqa * kHeadDim / 4; i += kThreads) {
+    const float4 o = sum4(i);
+    const int h = i >> 6, d = (i & 63) * 4;
+    st_dsmem_f32x4(dsmem_addr(&sm.po[((int)rank * kGqa + h) * dpc + d % dpc], (uint32_t)(d / dpc)), o);
   }
   cluster_sync();   // all pushes have landed; nobody touches a peer after this
   if (tid < kGqa) {
@@ -431,7 +520,7 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
     const int h = i / dpc, e = i % dpc;
     float o = 0.f;
     for (int r = 0; r < (int)NC; ++r) o = fmaf(sm.w[r][h], sm.po[(r * kGqa + h) * dpc + e], o);
-    a.out[((int64_t)t * Hq + g * kGqa + h) * kHeadDim + (int)rank * dpc + e] = o;
+    out[h * kHeadDim + (int)rank * dpc + e] = o;
   }
 }
 
@@ -488,26 +577,41 @@ cudaError_t launch(const AttnArgs& a, int nc, unsigned* err, cudaStream_t stream
                     dim3(kWarps * 32), sizeof(Smem<kWarps>), stream, (unsigned)nc, a, err);
 }
 
+// Cluster size for kWarps warps a CTA, and the time it is reckoned to take in
+// units of a warp's chunk: the CTAs' waves, each as long as a warp's chunks
+// and a fixed part (prologue, merge).
+template <int kWarps>
+cudaError_t plan(int64_t clusters, int chunks, int* nc, int64_t* cost) {
+  const int* active = nullptr;
+  const cudaError_t e = max_clusters<kWarps>(&active);
+  if (e != cudaSuccess) return e;
+  *nc = 1;
+  *cost = -1;
+  for (int i = 0; i < 5; ++i) {
+    const int c = 16 >> i;
+    if (active[i] <= 0 || (c > 1 && (c - 1) * kWarps >= chunks)) continue;
+    const int64_t waves = ceil_div(clusters, (int64_t)active[i]);
+    const int64_t w = waves * (kFixed + ceil_div((int64_t)chunks, (int64_t)c * kWarps));
+    if (*cost < 0 || w < *cost) {
+      *cost = w;
+      *nc = c;
+    }
+  }
+  return cudaSuccess;
+}
+
 }  // namespace
 
 cudaError_t launch_attn_q4(const AttnArgs& a, unsigned* err, cudaStream_t stream) {
-  constexpr int kWarps = 4;
-  const int* active = nullptr;
-  cudaError_t e = max_clusters<kWarps>(&active);
-  if (e != cudaSuccess) return e;
   const int chunks = (int)ceil_div(a.cells_pitch, kChunk);
   const int64_t clusters = (int64_t)a.n_tokens * a.n_kv_heads;
-  // the largest cluster whose warps all have a chunk and that runs in one
-  // wave; past one wave at every size, single CTAs (no cluster to wait for)
-  int nc = 1;
-  for (int i = 0; i < 5; ++i) {
-    const int c = 16 >> i;
-    if (active[i] > 0 && clusters <= active[i] && (c == 1 || (c - 1) * kWarps < chunks)) {
-      nc = c;
-      break;
-    }
-  }
-  return launch<kWarps>(a, nc, err, stream);
+  int nc4 = 1, nc12 = 1;
+  int64_t cost4 = 0, cost12 = 0;
+  cudaError_t e = plan<4>(clusters, chunks, &nc4, &cost4);
+  if (e == cudaSuccess) e = plan<12>(clusters, chunks, &nc12, &cost12);
+  if (e != cudaSuccess) return e;
+  if (cost12 < cost4) return launch<12>(a, nc12, err, stream);
+  return launch<4>(a, nc4, err, stream);
 }
 
 }  // namespace qsa

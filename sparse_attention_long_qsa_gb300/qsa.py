@@ -175,8 +175,8 @@ def _check(st: int, what: str):
 
 def _stream(stream):
     import torch
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:   # current_stream() would build a Stream object for it
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -192,6 +192,9 @@ def _ptr(t, dtype, name, allow_none=False, host_ok=False, strided=False):
     step's own inputs and outputs may instead be page-locked (pinned) host
     tensors, which the kernels read and write in place over the host link."""
     import torch
+    if t.__class__ is torch.Tensor and (dtype is None or t.dtype is dtype) and (strided or t.is_contiguous()) \
+            and t.get_device() == torch._C._cuda_getDevice():   # -1 for host memory
+        return t.data_ptr()
     if t is None:
         if allow_none:
             return None
