@@ -55,9 +55,9 @@ constexpr int kPitch = kHeadDim + 4;             // floats between two heads of 
 template <int kWarps>
 struct Smem {
   alignas(16) unsigned char stage[kWarps][kStages][kStageBytes];   // after the loop: each warp's o, fp32 [8][kPitch]
-  uint4 q[kBlocks][2][32];                       // a lane's query fragment of a block and step: {a0, 0, a2, 0}
-  float4 kd[kWarps][kBlocks][4];                 // a chunk's K scales: block, l4 -> cells 2 l4 + {0, 1, 8, 9}
-  uint2 vd[kWarps][kBlocks][4];                  // its V scales times 2^wexp, the same as four halves
+  uint4 q[kBlocks][32];                          // a lane's query fragments of a block: step 0, step 1
+  float4 kd[kWarps][kBlocks][8];                 // a chunk's K scales: block, gid -> cells gid, gid + 8, each twice
+  uint2 vd[kWarps][kBlocks][4];                  // its V scales times 2^wexp: block, l4 -> cells 2 l4 + {0, 1, 8, 9}
   float m[kWarps][kGqa], l[kWarps][kGqa];
   alignas(16) float po[kGqa * kHeadDim];         // the cluster's partials of this CTA's dims: [NC][8][256 / NC]
   alignas(16) float pm[kMaxCluster][2 * kGqa];   // their (max, sum)
@@ -93,10 +93,17 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // The same from zero.
-__device__ __forceinline__ void mma0(float (&c)[4], uint4 a, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                     uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
-               : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-               : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// An 8 x 8 tile of halves, two of a row per lane, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  return y;
 }
 // 2^x; results below the normal range are zero
 __device__ __forceinline__ float ex2(float x) {
@@ -145,13 +152,13 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
   const uint32_t rank = cluster_rank(), NC = cluster_size();
   const int G = a.n_kv_heads, Hq = G * kGqa;
 
-  // ---- the query fragments of head gid (an input: read before the wait).
-  // Block b, step s: k index 2 l4 + {0, 1} is dim 32 b + 4 l4 + s + {0, 2},
+  // ---- the query fragments, column gid = head gid (an input: read before the
+  // wait).  Block b, step s: k index 2 l4 + {0, 1} is dim 32 b + 4 l4 + s + {0, 2},
   // k index 8 + 2 l4 + {0, 1} the dim 16 further (divided by 16).  A power of
   // two per head brings its largest query to [2^6, 2^7) first, so that small
   // queries keep their bits through that division and -8 * (a block's sum)
   // stays in range.
-  float scale0, scale24;      // of a score, to the log2 domain: without the queries' (and the codes') power of two
+  float scale[2];   // of heads 2 l4, 2 l4 + 1's scores, to the log2 domain: without the queries' power of two
   uint32_t bias_hi = 0u, bias_lo = 0u;   // -8 * the sums of blocks 2 l4, 2 l4 + 1, in two parts
   {
     const __half* q = a.q + ((int64_t)t * Hq + g * kGqa + gid) * kHeadDim;
@@ -173,8 +180,9 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
     const int e = 21 - (int)((bits(__hmax2(qmax, __lowhigh2highlow(qmax))) & 0x7fffu) >> 10);   // -10 .. 21
     const int e0 = min(e, 15);
     const __half2 up0 = pow2h(e0), up1 = pow2h(e - e0), sixteenth = __float2half2_rn(0.0625f);
-    scale0 = a.attn_scale * 1.4426950408889634f * exp2f((float)-e);
-    scale24 = scale0 * 16777216.0f;
+    const float mine = a.attn_scale * 1.4426950408889634f * exp2f((float)-e);
+    scale[0] = __shfl_sync(kFull, mine, 8 * l4);
+    scale[1] = __shfl_sync(kFull, mine, 8 * l4 + 4);
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
       float s = 0.f;
@@ -187,10 +195,7 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
           s += f.x + f.y;
           x[b][i][j] = bits(j ? __hmul2(y, sixteenth) : y);
         }
-      if (b % kWarps == warp) {
-        sm.q[b][0][lane] = make_uint4(x[b][0][0], 0u, x[b][0][1], 0u);
-        sm.q[b][1][lane] = make_uint4(x[b][1][0], 0u, x[b][1][1], 0u);
-      }
+      if (b % kWarps == warp) sm.q[b][lane] = make_uint4(x[b][0][0], x[b][0][1], x[b][1][0], x[b][1][1]);
       s += __shfl_xor_sync(kFull, s, 1);
       s += __shfl_xor_sync(kFull, s, 2);
       s *= -8.f;
@@ -264,7 +269,8 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[b][i][j] = 0.f;
-  float run_m = -INFINITY, run_l = 0.f;   // head gid; run_l: this thread's cells only
+  // of heads 2 l4, 2 l4 + 1; run_l: this thread's cells only
+  float run_m[2] = {-INFINITY, -INFINITY}, run_l[2] = {0.f, 0.f};
   int wexp = kNoExp;                      // weights carry 2^wexp
   unsigned valid[kStages - 1] = {};       // of the chunks in flight, oldest first: which of the 16 cells exist
 
@@ -303,20 +309,19 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
     const uint32_t sk = ring + (uint32_t)st * kStageBytes, sv = sk + kChunk * kRow;
     st = st == kStages - 1 ? 0 : st + 1;
 
-    // ---- the chunk's scales, laid out once for all lanes.  ldmatrix gives this
-    // thread those of cells 2 l4 + {0, 1, 8, 9} in block gid.
-    float off[2][4];
+    // ---- the chunk's scales, laid out once for all lanes.  The transposing
+    // ldmatrix gives this thread those of cells 2 l4 + {0, 1, 8, 9} in block gid.
+    float off[4];
     __half2 dv[2];
     {
       uint32_t d[2];
-      ldmatrix2(sk + (lane & 15) * kRow + 128, d);   // cell 8 j + gid, blocks 2 l4, 2 l4 + 1
+      ldmatrix2(sk + (lane & 15) * kRow + 128, d);   // cells gid, gid + 8; blocks 2 l4, 2 l4 + 1
       // the codes' offset: sum over the blocks of d_K * (-8 * sum of q), k = block, once per part
-      const uint4 bias = make_uint4(bias_hi, 0u, bias_lo, 0u);
-      mma0(off[0], bias, d[0], d[0]);
-      mma0(off[1], bias, d[1], d[1]);
+      mma0(off, d[0], d[1], d[0], d[1], bias_hi, bias_lo);
       ldmatrix2_trans(sk + (lane & 15) * kRow + 128, d);
       const float2 d0 = __half22float2(half2_of(d[0])), d1 = __half22float2(half2_of(d[1]));
-      sm.kd[warp][gid][l4] = make_float4(d0.x, d0.y, d1.x, d1.y);
+      sm.kd[warp][gid][2 * l4] = make_float4(d0.x, d0.x, d1.x, d1.x);
+      sm.kd[warp][gid][2 * l4 + 1] = make_float4(d0.y, d0.y, d1.y, d1.y);
       ldmatrix2_trans(sv + (lane & 15) * kRow + 128, d);
       dv[0] = half2_of(d[0]), dv[1] = half2_of(d[1]);
     }
@@ -332,70 +337,74 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
     }
     __syncwarp();
 
-    // ---- scores: s[j][e] = q_gid . K of cell 8 j + 2 l4 + e
+    // ---- scores: s[j] of cell gid + 8 j with heads 2 l4, 2 l4 + 1
     float2 s[2] = {};
 #pragma unroll
-    for (int bq = 0; bq < 2; ++bq) {   // four blocks: lane l's address is row l % 8 of block 4 bq + l / 8
-      uint32_t w[2][4];
+    for (int bp = 0; bp < 4; ++bp) {   // two blocks: lane l's address is row l % 16 of block 2 bp + l / 16
+      uint32_t w[4];
+      ldmatrix4(sk + (lane & 15) * kRow + (2 * bp + (lane >> 4)) * 16, w);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) ldmatrix4(sk + (8 * j + (lane & 7)) * kRow + (4 * bq + (lane >> 3)) * 16, w[j]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int b = 4 * bq + i;
-        const uint4 q0 = sm.q[b][0][lane], q1 = sm.q[b][1][lane];
-        const float4 d = sm.kd[warp][b][l4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float c[4];   // rows 8..15 (no head) are not used
-          mma0(c, q0, w[j][i] & 0x000f000fu, w[j][i] & 0x00f000f0u);
-          const uint32_t u = w[j][i] >> 8;
-          mma(c, q1.x, q1.y, q1.z, q1.w, u & 0x000f000fu, u & 0x00f000f0u);
-          fma2(s[j], j ? d.z : d.x, j ? d.w : d.y, c[0], c[1]);
-        }
+      for (int i = 0; i < 2; ++i) {
+        const int b = 2 * bp + i;
+        const uint4 q = sm.q[b][lane];
+        const float4 d = sm.kd[warp][b][gid];
+        const uint32_t w0 = w[2 * i], w1 = w[2 * i + 1], u0 = w0 >> 8, u1 = w1 >> 8;
+        float c[4];
+        mma0(c, w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, q.x, q.y);
+        mma(c, u0 & 0x000f000fu, u1 & 0x000f000fu, u0 & 0x00f000f0u, u1 & 0x00f000f0u, q.z, q.w);
+        fma2(s[0], d.x, d.y, c[0], c[1]);
+        fma2(s[1], d.z, d.w, c[2], c[3]);
       }
     }
-    // ---- softmax of head gid over the 16 cells (a quad holds them)
+    // ---- softmax of the two heads over the 16 cells (8 lanes hold them)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      s[j].x = fmaf(off[j][0], scale0, s[j].x * scale24);
-      s[j].y = fmaf(off[j][1], scale0, s[j].y * scale24);
+    for (int j = 0; j < 2; ++j) {   // the codes' 2^24 is taken back here
+      s[j].x = fmaf(s[j].x, 16777216.0f, off[2 * j]) * scale[0];
+      s[j].y = fmaf(s[j].y, 16777216.0f, off[2 * j + 1]) * scale[1];
     }
     if (ok != kFull) {
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (!((ok >> (8 * j + 2 * l4 + e)) & 1u)) (e ? s[j].y : s[j].x) = -INFINITY;
+        if (!((ok >> (gid + 8 * j)) & 1u)) s[j] = make_float2(-INFINITY, -INFINITY);
     }
-    float cm = fmaxf(fmaxf(s[0].x, s[0].y), fmaxf(s[1].x, s[1].y));
-    cm = fmaxf(cm, __shfl_xor_sync(kFull, cm, 1));
-    cm = fmaxf(cm, __shfl_xor_sync(kFull, cm, 2));
-    const bool grow = cm > run_m + kLazy;
-    if (__any_sync(kFull, grow) || nexp != wexp) {
-      const float nm = grow ? cm : run_m;
-      const float f = run_m == -INFINITY ? 0.f : exp2f(run_m - nm);
-      run_l *= f;
-      run_m = nm;
+    float cm[2] = {fmaxf(s[0].x, s[1].x), fmaxf(s[0].y, s[1].y)};
+#pragma unroll
+    for (int o = 4; o <= 16; o <<= 1)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) cm[h] = fmaxf(cm[h], __shfl_xor_sync(kFull, cm[h], o));
+    if (__any_sync(kFull, cm[0] > run_m[0] + kLazy || cm[1] > run_m[1] + kLazy) || nexp != wexp) {
+      float f[2];
       const float fe = wexp == kNoExp ? 1.f : exp2f((float)(nexp - wexp));   // accumulators of an unset exponent are zero
       wexp = nexp;
-      const float f0 = __shfl_sync(kFull, f, 8 * l4) * fe, f1 = __shfl_sync(kFull, f, 8 * l4 + 4) * fe;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float nm = cm[h] > run_m[h] + kLazy ? cm[h] : run_m[h];
+        f[h] = run_m[h] == -INFINITY ? 0.f : exp2f(run_m[h] - nm);
+        run_l[h] *= f[h];
+        run_m[h] = nm;
+        f[h] *= fe;
+      }
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          acc[b][i][0] *= f0, acc[b][i][1] *= f1;
-          acc[b][i][2] *= f0, acc[b][i][3] *= f1;
+          acc[b][i][0] *= f[0], acc[b][i][1] *= f[1];
+          acc[b][i][2] *= f[0], acc[b][i][3] *= f[1];
         }
     }
-    const float base = run_m == -INFINITY ? 0.f : run_m;   // no cell yet: every s is -inf
+    // probabilities in two parts, then from (cell, heads) to (head, cells)
+    const float base0 = run_m[0] == -INFINITY ? 0.f : run_m[0];   // no cell yet: every s is -inf
+    const float base1 = run_m[1] == -INFINITY ? 0.f : run_m[1];
     __half2 ph[2], pl[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const float p0 = ex2(s[j].x - base), p1 = ex2(s[j].y - base);
-      run_l += p0 + p1;
-      ph[j] = __floats2half2_rn(p0, p1);
-      const float2 h = __half22float2(ph[j]);
-      pl[j] = __floats2half2_rn(p0 - h.x, p1 - h.y);
+      const float p0 = ex2(s[j].x - base0), p1 = ex2(s[j].y - base1);
+      run_l[0] += p0;
+      run_l[1] += p1;
+      const __half2 hi = __floats2half2_rn(p0, p1);
+      const float2 h = __half22float2(hi);
+      ph[j] = half2_of(transposed(bits(hi)));
+      pl[j] = half2_of(transposed(bits(__floats2half2_rn(p0 - h.x, p1 - h.y))));
     }
 
     // ---- o^T[dim][head] += V^T . w, per block of 32 dims: tile i, row gid is
@@ -414,27 +423,33 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
         const uint32_t wl0 = bits(__hfma2(pl[0], d0, __hfma2(ph[0], d0, __hneg2(h0))));
         const uint32_t wl1 = bits(__hfma2(pl[1], d1, __hfma2(ph[1], d1, __hneg2(h1))));
         const __half2 c1 = half2_of(0x64086408u), c16 = half2_of(0x64806480u);   // 1024 + 8, 1024 + 128
+        uint32_t x[2][4];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const uint32_t x0 = k ? v[2 * i] >> 8 : v[2 * i], x1 = k ? v[2 * i + 1] >> 8 : v[2 * i + 1];
-          const uint32_t a0 = bits(__hsub2(half2_of(and_or(x0, 0x000f000fu, 0x64006400u)), c1));
-          const uint32_t a1 = bits(__hsub2(half2_of(and_or(x0, 0x00f000f0u, 0x64006400u)), c16));
-          const uint32_t a2 = bits(__hsub2(half2_of(and_or(x1, 0x000f000fu, 0x64006400u)), c1));
-          const uint32_t a3 = bits(__hsub2(half2_of(and_or(x1, 0x00f000f0u, 0x64006400u)), c16));
-          mma(acc[b][k], a0, a1, a2, a3, wh0, wh1);
-          mma(acc[b][k], a0, a1, a2, a3, wl0, wl1);
+          x[k][0] = bits(__hsub2(half2_of(and_or(x0, 0x000f000fu, 0x64006400u)), c1));
+          x[k][1] = bits(__hsub2(half2_of(and_or(x0, 0x00f000f0u, 0x64006400u)), c16));
+          x[k][2] = bits(__hsub2(half2_of(and_or(x1, 0x000f000fu, 0x64006400u)), c1));
+          x[k][3] = bits(__hsub2(half2_of(and_or(x1, 0x00f000f0u, 0x64006400u)), c16));
         }
+        mma(acc[b][0], x[0][0], x[0][1], x[0][2], x[0][3], wh0, wh1);
+        mma(acc[b][1], x[1][0], x[1][1], x[1][2], x[1][3], wh0, wh1);
+        mma(acc[b][0], x[0][0], x[0][1], x[0][2], x[0][3], wl0, wl1);
+        mma(acc[b][1], x[1][0], x[1][1], x[1][2], x[1][3], wl0, wl1);
       }
     }
   }
   asm volatile("cp.async.wait_all;\n" ::: "memory");
 
   // ---- merge the CTA's warps (in warp order)
-  run_l += __shfl_xor_sync(kFull, run_l, 1);
-  run_l += __shfl_xor_sync(kFull, run_l, 2);
-  if (l4 == 0) {
-    sm.m[warp][gid] = run_m;
-    sm.l[warp][gid] = run_l;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int o = 4; o <= 16; o <<= 1) run_l[h] += __shfl_xor_sync(kFull, run_l[h], o);
+    if (gid == 0) {
+      sm.m[warp][2 * l4 + h] = run_m[h];
+      sm.l[warp][2 * l4 + h] = run_l[h];
+    }
   }
   __syncthreads();   // also: every warp is done with its stages
   {
