@@ -10,15 +10,15 @@
 // head (about 2,000 cycles per 128 cells on an SM), several times the gather
 // itself, and the tensor core would use 8 of the 16 columns it needs at least.
 // mma.sync takes its operands from registers: ldmatrix hands each thread
-// exactly the nibbles of its fragment, and masking them in place makes fp16
-// operands (0..15 in the low mantissa bits are the subnormals n * 2^-24, which
-// the tensor cores multiply exactly).
+// exactly the nibbles of its fragment, and two instructions make two of them
+// fp16 operands.
 //
 // Both products are exact in their codes; no K or V value is ever rounded:
 //   Q.K  per 32-value block with integer codes, the block's sum then scaled by
-//        d_K in fp32; the code's offset of 8 enters as the accumulator's start
-//        value -8 * sum_i q_i.  Codes in bits 4..7 of a half weigh 16 times
-//        more: their queries are divided by 16.
+//        d_K in fp32.  Codes in bits 4..7 of a half weigh 16 times more: their
+//        queries are divided by 16.  (Masked codes without the offset of 8 are
+//        subnormals, n * 2^-24, and would save the subtraction, but the tensor
+//        core then drops low bits of the queries: scores off by 1e-6.)
 //   P.V  d_V is folded into the probabilities: w = p * d_V, split into two
 //        fp16 parts (22 bits), two products into one fp32 accumulator.  A
 //        common power of two keeps w off the fp16 range's ends.
@@ -43,11 +43,15 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kChunk = 16;                       // cells of one warp step
 constexpr int kRow = 144;                        // 128 B codes + 16 B scales: ldmatrix rows 144 B apart do not conflict
 constexpr int kStageBytes = 2 * kChunk * kRow;   // K rows, then V rows
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 constexpr int kMaxCluster = 16;
-constexpr float kLazy = 8.f;                     // log2 of how far a probability may exceed 1
+// Probabilities are held as 2^(s - m + kUp) so that their low fp16 part, 2^-11
+// of them, stays a normal half for all that count; s may pass the running
+// maximum m by kLazy before m follows.  2^(kUp + kLazy) <= 2^15.
+constexpr float kUp = 7.f, kLazy = 8.f;
 constexpr int kFixed = 4;                        // a CTA's prologue and merge, in chunks
 constexpr int kNoExp = 32;                       // no scale of V seen yet
+constexpr float kNoMax = -3.0e38f;               // no cell seen yet (below every score, and finite)
 constexpr int kBlocks = kHeadDim / 32;           // q4_0 blocks of a row
 
 constexpr int kPitch = kHeadDim + 4;             // floats between two heads of a warp's o: its stores do not conflict
@@ -56,7 +60,8 @@ template <int kWarps>
 struct Smem {
   alignas(16) unsigned char stage[kWarps][kStages][kStageBytes];   // after the loop: each warp's o, fp32 [8][kPitch]
   uint4 q[kBlocks][32];                          // a lane's query fragments of a block: step 0, step 1
-  float4 kd[kWarps][kBlocks][8];                 // a chunk's K scales: block, gid -> cells gid, gid + 8, each twice
+  float4 kd[kWarps][kBlocks][9];                 // a chunk's K scales: block, gid -> cells gid, gid + 8, each twice
+                                                 // (blocks 144 B apart: their stores do not conflict)
   uint2 vd[kWarps][kBlocks][4];                  // its V scales times 2^wexp: block, l4 -> cells 2 l4 + {0, 1, 8, 9}
   float m[kWarps][kGqa], l[kWarps][kGqa];
   alignas(16) float po[kGqa * kHeadDim];         // the cluster's partials of this CTA's dims: [NC][8][256 / NC]
@@ -134,14 +139,23 @@ __device__ __forceinline__ __half2 half2_of(uint32_t u) {
   memcpy(&h, &u, 4);
   return h;
 }
-// 2^k as a half, k in [-14, 15]
+// Codes less 8 as halves: those in bits 0..3 of x's two halves, and 16 times
+// those in bits 4..7.  A code put under the exponent of 1024 is 1024 + code (or
+// + 16 codes); taking off 1024 + 8 (or + 128) is exact.
+__device__ __forceinline__ uint32_t low_codes(uint32_t x) {
+  return bits(__hsub2(half2_of(and_or(x, 0x000f000fu, 0x64006400u)), half2_of(0x64086408u)));
+}
+__device__ __forceinline__ uint32_t high_codes(uint32_t x) {
+  return bits(__hsub2(half2_of(and_or(x, 0x00f000f0u, 0x64006400u)), half2_of(0x64806480u)));
+}
+// 2^k as a half, k in [-24, 15]
 __device__ __forceinline__ __half2 pow2h(int k) {
-  const uint32_t e = (uint32_t)(k + 15) << 10;
+  const uint32_t e = k >= -14 ? (uint32_t)(k + 15) << 10 : 1u << (k + 24);
   return half2_of(e | (e << 16));
 }
 
 template <int kWarps>
-__global__ void __launch_bounds__(kWarps * 32, 12 / kWarps)
+__global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
 k_attn_q4(const AttnArgs a, unsigned* err) {
   extern __shared__ unsigned char smem_raw[];
   Smem<kWarps>& sm = *reinterpret_cast<Smem<kWarps>*>(smem_raw);
@@ -156,10 +170,8 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
   // wait).  Block b, step s: k index 2 l4 + {0, 1} is dim 32 b + 4 l4 + s + {0, 2},
   // k index 8 + 2 l4 + {0, 1} the dim 16 further (divided by 16).  A power of
   // two per head brings its largest query to [2^6, 2^7) first, so that small
-  // queries keep their bits through that division and -8 * (a block's sum)
-  // stays in range.
+  // queries keep their bits through that division.
   float scale[2];   // of heads 2 l4, 2 l4 + 1's scores, to the log2 domain: without the queries' power of two
-  uint32_t bias_hi = 0u, bias_lo = 0u;   // -8 * the sums of blocks 2 l4, 2 l4 + 1, in two parts
   {
     const __half* q = a.q + ((int64_t)t * Hq + g * kGqa + gid) * kHeadDim;
     uint32_t x[kBlocks][2][2];
@@ -185,25 +197,14 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
     scale[1] = __shfl_sync(kFull, mine, 8 * l4 + 4);
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
-      float s = 0.f;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const __half2 y = __hmul2(__hmul2(half2_of(x[b][i][j]), up0), up1);
-          const float2 f = __half22float2(y);
-          s += f.x + f.y;
           x[b][i][j] = bits(j ? __hmul2(y, sixteenth) : y);
         }
       if (b % kWarps == warp) sm.q[b][lane] = make_uint4(x[b][0][0], x[b][0][1], x[b][1][0], x[b][1][1]);
-      s += __shfl_xor_sync(kFull, s, 1);
-      s += __shfl_xor_sync(kFull, s, 2);
-      s *= -8.f;
-      const __half h = __float2half_rn(s), l = __float2half_rn(s - __half2float(h));
-      if ((b >> 1) == l4) {
-        bias_hi |= (uint32_t)__half_as_ushort(h) << (16 * (b & 1));
-        bias_lo |= (uint32_t)__half_as_ushort(l) << (16 * (b & 1));
-      }
     }
   }
   cluster_arrive();   // waited for before anything is pushed to a peer
@@ -269,9 +270,11 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[b][i][j] = 0.f;
-  // of heads 2 l4, 2 l4 + 1; run_l: this thread's cells only
-  float run_m[2] = {-INFINITY, -INFINITY}, run_l[2] = {0.f, 0.f};
+  // of heads 2 l4, 2 l4 + 1; run_m: a running maximum less kUp, run_l: this thread's cells only
+  float run_m[2] = {kNoMax, kNoMax}, run_l[2] = {0.f, 0.f};
   int wexp = kNoExp;                      // weights carry 2^wexp
+  uint32_t dlim = 0u;                     // the largest V scale (as bits) that wexp allows
+  __half2 up = pow2h(0);                  // 2^wexp
   unsigned valid[kStages - 1] = {};       // of the chunks in flight, oldest first: which of the 16 cells exist
 
   int ahead = listed(first);
@@ -311,13 +314,9 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
 
     // ---- the chunk's scales, laid out once for all lanes.  The transposing
     // ldmatrix gives this thread those of cells 2 l4 + {0, 1, 8, 9} in block gid.
-    float off[4];
     __half2 dv[2];
     {
       uint32_t d[2];
-      ldmatrix2(sk + (lane & 15) * kRow + 128, d);   // cells gid, gid + 8; blocks 2 l4, 2 l4 + 1
-      // the codes' offset: sum over the blocks of d_K * (-8 * sum of q), k = block, once per part
-      mma0(off, d[0], d[1], d[0], d[1], bias_hi, bias_lo);
       ldmatrix2_trans(sk + (lane & 15) * kRow + 128, d);
       const float2 d0 = __half22float2(half2_of(d[0])), d1 = __half22float2(half2_of(d[1]));
       sm.kd[warp][gid][2 * l4] = make_float4(d0.x, d0.x, d1.x, d1.x);
@@ -325,16 +324,17 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
       ldmatrix2_trans(sv + (lane & 15) * kRow + 128, d);
       dv[0] = half2_of(d[0]), dv[1] = half2_of(d[1]);
     }
-    // the largest scale of V sets the weights' exponent: d_max * 2^want lies in
-    // [2^5, 2^6) (or below, at the exponent's ends)
+    // the largest scale of V sets the weights' exponent: d_max * 2^wexp lies in
+    // [2^-2, 2^-1) (below, for subnormal scales) when it is set, and stays below 1
     const uint32_t dm = bits(__hmax2(__habs2(dv[0]), __habs2(dv[1])));
     const uint32_t db = __reduce_max_sync(kFull, max(dm >> 16, dm & 0xffffu));
-    const int want = min(15, max(-10, 20 - (int)(db >> 10)));
-    const int nexp = db != 0u && want < wexp - 1 ? want : wexp;
-    {
-      const __half2 up = pow2h(nexp == kNoExp ? 0 : nexp);
-      sm.vd[warp][gid][l4] = make_uint2(bits(__hmul2(dv[0], up)), bits(__hmul2(dv[1], up)));
+    int nexp = wexp;
+    if (db > dlim) {
+      nexp = 13 - (int)(db >> 10);   // -18 .. 13
+      dlim = ((uint32_t)(15 - nexp) << 10) - 1u;
+      up = pow2h(nexp);
     }
+    sm.vd[warp][gid][l4] = make_uint2(bits(__hmul2(dv[0], up)), bits(__hmul2(dv[1], up)));
     __syncwarp();
 
     // ---- scores: s[j] of cell gid + 8 j with heads 2 l4, 2 l4 + 1
@@ -350,36 +350,31 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
         const float4 d = sm.kd[warp][b][gid];
         const uint32_t w0 = w[2 * i], w1 = w[2 * i + 1], u0 = w0 >> 8, u1 = w1 >> 8;
         float c[4];
-        mma0(c, w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, q.x, q.y);
-        mma(c, u0 & 0x000f000fu, u1 & 0x000f000fu, u0 & 0x00f000f0u, u1 & 0x00f000f0u, q.z, q.w);
+        mma0(c, low_codes(w0), low_codes(w1), high_codes(w0), high_codes(w1), q.x, q.y);
+        mma(c, low_codes(u0), low_codes(u1), high_codes(u0), high_codes(u1), q.z, q.w);
         fma2(s[0], d.x, d.y, c[0], c[1]);
         fma2(s[1], d.z, d.w, c[2], c[3]);
       }
     }
     // ---- softmax of the two heads over the 16 cells (8 lanes hold them)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {   // the codes' 2^24 is taken back here
-      s[j].x = fmaf(s[j].x, 16777216.0f, off[2 * j]) * scale[0];
-      s[j].y = fmaf(s[j].y, 16777216.0f, off[2 * j + 1]) * scale[1];
+    float cm[2] = {fmaxf(s[0].x * scale[0], s[1].x * scale[0]), fmaxf(s[0].y * scale[1], s[1].y * scale[1])};
+    if (ok != kFull) {   // missing cells: p = 0
+      const bool h0 = (ok >> gid) & 1u, h1 = (ok >> (gid + 8)) & 1u;
+      cm[0] = fmaxf(h0 ? s[0].x * scale[0] : -INFINITY, h1 ? s[1].x * scale[0] : -INFINITY);
+      cm[1] = fmaxf(h0 ? s[0].y * scale[1] : -INFINITY, h1 ? s[1].y * scale[1] : -INFINITY);
     }
-    if (ok != kFull) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        if (!((ok >> (gid + 8 * j)) & 1u)) s[j] = make_float2(-INFINITY, -INFINITY);
-    }
-    float cm[2] = {fmaxf(s[0].x, s[1].x), fmaxf(s[0].y, s[1].y)};
 #pragma unroll
     for (int o = 4; o <= 16; o <<= 1)
 #pragma unroll
       for (int h = 0; h < 2; ++h) cm[h] = fmaxf(cm[h], __shfl_xor_sync(kFull, cm[h], o));
-    if (__any_sync(kFull, cm[0] > run_m[0] + kLazy || cm[1] > run_m[1] + kLazy) || nexp != wexp) {
+    if (__any_sync(kFull, cm[0] > run_m[0] + (kUp + kLazy) || cm[1] > run_m[1] + (kUp + kLazy)) || nexp != wexp) {
       float f[2];
       const float fe = wexp == kNoExp ? 1.f : exp2f((float)(nexp - wexp));   // accumulators of an unset exponent are zero
       wexp = nexp;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float nm = cm[h] > run_m[h] + kLazy ? cm[h] : run_m[h];
-        f[h] = run_m[h] == -INFINITY ? 0.f : exp2f(run_m[h] - nm);
+        const float nm = cm[h] > run_m[h] + (kUp + kLazy) ? cm[h] - kUp : run_m[h];
+        f[h] = exp2f(run_m[h] - nm);
         run_l[h] *= f[h];
         run_m[h] = nm;
         f[h] *= fe;
@@ -393,12 +388,11 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
         }
     }
     // probabilities in two parts, then from (cell, heads) to (head, cells)
-    const float base0 = run_m[0] == -INFINITY ? 0.f : run_m[0];   // no cell yet: every s is -inf
-    const float base1 = run_m[1] == -INFINITY ? 0.f : run_m[1];
     __half2 ph[2], pl[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const float p0 = ex2(s[j].x - base0), p1 = ex2(s[j].y - base1);
+      float p0 = ex2(fmaf(s[j].x, scale[0], -run_m[0])), p1 = ex2(fmaf(s[j].y, scale[1], -run_m[1]));
+      if (ok != kFull && !((ok >> (gid + 8 * j)) & 1u)) p0 = p1 = 0.f;
       run_l[0] += p0;
       run_l[1] += p1;
       const __half2 hi = __floats2half2_rn(p0, p1);
@@ -422,15 +416,14 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
         const uint32_t wh0 = bits(h0), wh1 = bits(h1);
         const uint32_t wl0 = bits(__hfma2(pl[0], d0, __hfma2(ph[0], d0, __hneg2(h0))));
         const uint32_t wl1 = bits(__hfma2(pl[1], d1, __hfma2(ph[1], d1, __hneg2(h1))));
-        const __half2 c1 = half2_of(0x64086408u), c16 = half2_of(0x64806480u);   // 1024 + 8, 1024 + 128
         uint32_t x[2][4];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const uint32_t x0 = k ? v[2 * i] >> 8 : v[2 * i], x1 = k ? v[2 * i + 1] >> 8 : v[2 * i + 1];
-          x[k][0] = bits(__hsub2(half2_of(and_or(x0, 0x000f000fu, 0x64006400u)), c1));
-          x[k][1] = bits(__hsub2(half2_of(and_or(x0, 0x00f000f0u, 0x64006400u)), c16));
-          x[k][2] = bits(__hsub2(half2_of(and_or(x1, 0x000f000fu, 0x64006400u)), c1));
-          x[k][3] = bits(__hsub2(half2_of(and_or(x1, 0x00f000f0u, 0x64006400u)), c16));
+          x[k][0] = low_codes(x0);
+          x[k][1] = high_codes(x0);
+          x[k][2] = low_codes(x1);
+          x[k][3] = high_codes(x1);
         }
         mma(acc[b][0], x[0][0], x[0][1], x[0][2], x[0][3], wh0, wh1);
         mma(acc[b][1], x[1][0], x[1][1], x[1][2], x[1][3], wh0, wh1);
@@ -458,11 +451,10 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
     float f[2];   // of heads 2 l4, 2 l4 + 1
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float m = -INFINITY;
+      float m = kNoMax;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm.m[w][2 * l4 + e]);
-      const float mw = sm.m[warp][2 * l4 + e];
-      f[e] = mw == -INFINITY ? 0.f : exp2f(mw - m) * back;
+      f[e] = exp2f(sm.m[warp][2 * l4 + e] - m) * back;
     }
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b)
@@ -475,13 +467,13 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
       }
   }
   // the CTA's (max, sum) of head h in threads h < 8
-  float cta_m = -INFINITY, cta_l = 0.f;
+  float cta_m = kNoMax, cta_l = 0.f;
   if (tid < kGqa) {
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) cta_m = fmaxf(cta_m, sm.m[w][tid]);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
-      cta_l += sm.m[w][tid] == -INFINITY ? 0.f : sm.l[w][tid] * exp2f(sm.m[w][tid] - cta_m);
+      cta_l += sm.l[w][tid] * exp2f(sm.m[w][tid] - cta_m);
     if (NC == 1) sm.w[0][tid] = cta_l != 0.f ? 1.0f / cta_l : 0.f;
   }
   __syncthreads();
@@ -521,10 +513,10 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
   }
   cluster_sync();   // all pushes have landed; nobody touches a peer after this
   if (tid < kGqa) {
-    float m = -INFINITY, l = 0.f;
+    float m = kNoMax, l = 0.f;
     for (int r = 0; r < (int)NC; ++r) m = fmaxf(m, sm.pm[r][tid]);
     for (int r = 0; r < (int)NC; ++r) {
-      const float w = sm.pm[r][tid] == -INFINITY ? 0.f : exp2f(sm.pm[r][tid] - m);
+      const float w = exp2f(sm.pm[r][tid] - m);
       sm.w[r][tid] = w;
       l += w * sm.pm[r][kGqa + tid];
     }
@@ -620,12 +612,12 @@ cudaError_t plan(int64_t clusters, int chunks, int* nc, int64_t* cost) {
 cudaError_t launch_attn_q4(const AttnArgs& a, unsigned* err, cudaStream_t stream) {
   const int chunks = (int)ceil_div(a.cells_pitch, kChunk);
   const int64_t clusters = (int64_t)a.n_tokens * a.n_kv_heads;
-  int nc4 = 1, nc12 = 1;
-  int64_t cost4 = 0, cost12 = 0;
+  int nc4 = 1, nc8 = 1;
+  int64_t cost4 = 0, cost8 = 0;
   cudaError_t e = plan<4>(clusters, chunks, &nc4, &cost4);
-  if (e == cudaSuccess) e = plan<12>(clusters, chunks, &nc12, &cost12);
+  if (e == cudaSuccess) e = plan<8>(clusters, chunks, &nc8, &cost8);
   if (e != cudaSuccess) return e;
-  if (cost12 < cost4) return launch<12>(a, nc12, err, stream);
+  if (cost8 < cost4) return launch<8>(a, nc8, err, stream);
   return launch<4>(a, nc4, err, stream);
 }
 
