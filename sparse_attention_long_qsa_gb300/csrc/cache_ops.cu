@@ -69,43 +69,50 @@ k_kv_read(const ReadArgs a, unsigned* err) {
 
 // ----------------------------------------------------------- qsa_cells_copy
 // A cell is up to five contiguous runs of 16-byte chunks (K and V codes, K and
-// V scales, the indexer key).  One warp per pair walks all of them, the loads
-// of a batch issued before its stores.
+// V scales, the indexer key).  A lane keeps the addresses of its chunks of cell
+// 0, at most kCopyBatch (all of a cell's for two fp16 heads), and a warp walks
+// the pairs: the batch's loads, the next pair's cells, then the stores.
 constexpr int kCopyBatch = 5;
+constexpr int kCopyPerSm = 4;   // CTAs that share an SM
 
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCopyPerSm)
 k_cells_copy(const CopyArgs a, unsigned* err) {
   grid_dep_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int64_t warps = (int64_t)gridDim.x * kWarps, first = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int64_t n = a.n_dev ? min((int64_t)max(*a.n_dev, 0), (int64_t)a.n) : (int64_t)a.n;
-  if (i >= n) return;
-  const int64_t s = a.src[i], d = a.dst[i];
-  if (s < 0 || d < 0) return;
-  if (s >= a.n_cells || d >= a.n_cells) {
-    if (lane == 0) atomicOr(err, kErrCell);
-    return;
-  }
   for (int c0 = 0; c0 < a.chunks; c0 += 32 * kCopyBatch) {
-    uint4 v[kCopyBatch];
-    unsigned char* to[kCopyBatch];
+    unsigned char* at[kCopyBatch];
+    unsigned pitch[kCopyBatch];   // 0: no such chunk
 #pragma unroll
     for (int b = 0; b < kCopyBatch; ++b) {
       int c = c0 + b * 32 + lane;
-      to[b] = nullptr;
-      if (c >= a.chunks) continue;
-      int run = 0;
+      at[b] = nullptr;
+      pitch[b] = 0u;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (c >= a.len[run]) c -= a.len[run], ++run;
-      unsigned char* base = a.base[run];
-      const int64_t pitch = (int64_t)a.len[run] * 16;
-      v[b] = *reinterpret_cast<const uint4*>(base + s * pitch + c * 16);
-      to[b] = base + d * pitch + c * 16;
+      for (int k = 0; k < 5; ++k) {
+        if (pitch[b] == 0u && c < a.len[k]) {
+          at[b] = a.base[k] + c * 16;
+          pitch[b] = (unsigned)a.len[k] * 16u;
+        }
+        c -= a.len[k];
+      }
     }
+    int s = -1, d = -1;
+    if (first < n) s = a.src[first], d = a.dst[first];
+    for (int64_t i = first; i < n; i += warps) {
+      const bool in = (unsigned)s < (unsigned)a.n_cells && (unsigned)d < (unsigned)a.n_cells;
+      if (!in && s >= 0 && d >= 0 && lane == 0) atomicOr(err, kErrCell);
+      uint4 v[kCopyBatch];
 #pragma unroll
-    for (int b = 0; b < kCopyBatch; ++b)
-      if (to[b]) *reinterpret_cast<uint4*>(to[b]) = v[b];
+      for (int b = 0; b < kCopyBatch; ++b)
+        if (in && pitch[b]) v[b] = *reinterpret_cast<const uint4*>(at[b] + (uint64_t)(unsigned)s * pitch[b]);
+      const unsigned to = (unsigned)d;
+      if (i + warps < n) s = a.src[i + warps], d = a.dst[i + warps];
+#pragma unroll
+      for (int b = 0; b < kCopyBatch; ++b)
+        if (in && pitch[b]) *reinterpret_cast<uint4*>(at[b] + (uint64_t)to * pitch[b]) = v[b];
+    }
   }
   __threadfence();
 }
@@ -361,7 +368,10 @@ cudaError_t launch_kv_read(const ReadArgs& a, unsigned* err, cudaStream_t stream
 cudaError_t launch_cells_copy(const CopyArgs& a, unsigned* err, cudaStream_t stream) {
   if (a.n <= 0) return cudaSuccess;
   prof_before(kKCopy, stream);
-  cudaError_t e = launch_pdl(k_cells_copy, dim3((unsigned)ceil_div(a.n, kWarps)), dim3(kThreads), 0, stream, 1, a, err);
+  const int64_t ctas = ceil_div(a.n, kWarps);
+  constexpr int64_t kResident = 152 * kCopyPerSm;
+  cudaError_t e = launch_pdl(k_cells_copy, dim3((unsigned)(ctas < kResident ? ctas : kResident)), dim3(kThreads), 0,
+                             stream, 1, a, err);
   prof_after(kKCopy, stream);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
