@@ -16,7 +16,7 @@
 //
 // One warp per (token, row): rows 0..G-1 are the K heads, G..2G-1 the V
 // heads, 2G the indexer key together with the table entry; that warp of each
-// block's first new token then re-pools the block.  An extra last CTA builds
+// block's first new token then re-pools the block.  An extra first CTA builds
 // the dirty list: the distinct slots, ascending, padded with -1.
 // Everything is read and encoded before the grid-dependency wait (the new
 // rows are inputs, not outputs of the preceding kernel); only the stores wait.
@@ -107,17 +107,18 @@ k_append(const AppendArgs a, const Turns turns, unsigned* err) {
   grid_dep_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kPer = kAppendMaxTokens / kAppThreads;   // tokens per thread in the dirty-list CTA
-  const bool dirty_cta = blockIdx.x == gridDim.x - 1;
+  static_assert(kPer == 4, "the dirty list sorts four registers a thread");
+  const bool dirty_cta = blockIdx.x == 0;   // first: its sort is the launch's longest work
   // this thread's tokens' ids, loaded together with the sequences' block
   // offsets (one dependent load less on the way to the slots)
   const int rows = 2 * a.G + 1;
-  const int64_t w = (int64_t)blockIdx.x * kAppWarps + warp;
+  const int64_t w = ((int64_t)blockIdx.x - 1) * kAppWarps + warp;
   const bool active = !dirty_cta && w < (int64_t)a.n_new * rows;
   const int t = active ? (int)(w / rows) : 0;
   NewTok mine[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
-    const int u = dirty_cta ? tid + k * kAppThreads : t;
+    const int u = dirty_cta ? warp * (32 * kPer) + 32 * k + lane : t;
     mine[k] = ((dirty_cta && u < a.n_new) || (!dirty_cta && k == 0 && active)) ? load_tok(a, u) : NewTok{-1, -1, -1};
   }
   __shared__ int64_t s_off_buf[kAppOffCache + 1];
@@ -138,39 +139,56 @@ k_append(const AppendArgs a, const Turns turns, unsigned* err) {
     // ---- the dirty list (n_new <= kAppendMaxTokens): every token's slot
     // (INT_MAX for an invalid token and past n_new), a bitonic sort of the
     // next power of two >= n_new, then the first of every run of equal slots
-    // compacted in order: the distinct slots, ascending
+    // compacted in order: the distinct slots, ascending.  Thread (warp, lane)
+    // holds elements 128 warp + 32 k + lane, k < 4, in registers, so that only
+    // the steps that cross warps (6 of the 55 for 1,024) go through shared
+    // memory and a barrier.
     __shared__ int s_slot[kAppendMaxTokens];
     __shared__ unsigned s_warp[kAppWarps];
     int n2 = 2;
     while (n2 < a.n_new) n2 <<= 1;
+    int v[kPer];
+    const int e0 = warp * (32 * kPer) + lane;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      const int u = tid + k * kAppThreads;
-      if (u >= n2) break;
-      int sl = INT_MAX;
-      if (u < a.n_new) {
-        int ib = 0;
-        const int x = token_slot(a, mine[k], s_off, &ib, err, false);
-        sl = x < 0 ? INT_MAX : x;
-      }
-      s_slot[u] = sl;
+      int ib = 0;
+      const int x = e0 + 32 * k < a.n_new ? token_slot(a, mine[k], s_off, &ib, err, false) : -1;
+      v[k] = x < 0 ? INT_MAX : x;
     }
-    __syncthreads();
+    auto keep = [](int x, int y, bool smaller) { return smaller ? min(x, y) : max(x, y); };
     for (int k = 2; k <= n2; k <<= 1) {
       for (int j = k >> 1; j > 0; j >>= 1) {
-        for (int i = tid; i < n2; i += kAppThreads) {
-          const int l = i ^ j;
-          if (l > i) {
-            const int x = s_slot[i], y = s_slot[l];
-            if ((x > y) == ((i & k) == 0)) {
-              s_slot[i] = y;
-              s_slot[l] = x;
-            }
+        if (j >= 32 * kPer) {
+#pragma unroll
+          for (int q = 0; q < kPer; ++q) s_slot[e0 + 32 * q] = v[q];
+          __syncthreads();
+#pragma unroll
+          for (int q = 0; q < kPer; ++q) {
+            const int e = e0 + 32 * q;
+            v[q] = keep(v[q], s_slot[e ^ j], ((e & j) == 0) == ((e & k) == 0));
+          }
+          __syncthreads();
+        } else if (j >= 32) {
+          int y[kPer];
+#pragma unroll
+          for (int q = 0; q < kPer; ++q) y[q] = j == 32 ? v[q ^ 1] : v[q ^ 2];
+#pragma unroll
+          for (int q = 0; q < kPer; ++q) {
+            const int e = e0 + 32 * q;
+            v[q] = keep(v[q], y[q], ((e & j) == 0) == ((e & k) == 0));
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < kPer; ++q) {
+            const int e = e0 + 32 * q;
+            v[q] = keep(v[q], __shfl_xor_sync(kFull, v[q], j), ((e & j) == 0) == ((e & k) == 0));
           }
         }
-        __syncthreads();
       }
     }
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) s_slot[e0 + 32 * q] = v[q];
+    __syncthreads();
     // thread tid takes the contiguous run [tid * per, tid * per + per)
     const int per = (n2 + kAppThreads - 1) / kAppThreads;   // <= 4
     const int i0 = min(n2, tid * per), i1 = min(n2, i0 + per);

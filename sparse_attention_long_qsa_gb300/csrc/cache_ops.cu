@@ -11,6 +11,8 @@
 // sweep: what they write (rows, block lists, free cells) may be an input that
 // the next call reads before its dependency wait, so the next kernel may start
 // only after the last CTA, and every CTA ends with a fence.
+#include <atomic>
+
 #include "qsa_internal.cuh"
 
 namespace qsa {
@@ -118,17 +120,22 @@ k_cells_copy(const CopyArgs a, unsigned* err) {
 }
 
 // ------------------------------------------------------------- qsa_seq_fork
-// grid.y: the forks; grid.x: 256 list entries each; CTA x = 0 also writes the
-// private tail block.
+// grid.y: the forks; grid.x: kForkPer list entries a thread; CTA x = 0 also
+// writes the private tail block.  Every CTA checks the whole fork (a bad one
+// changes nothing) and loads its entries before the checks that need the
+// tables have come back.
+constexpr int kForkPer = 4;
+
 __global__ void __launch_bounds__(kThreads)
 k_seq_fork(const ForkArgs a, unsigned* err) {
   grid_dep_wait();
   const int tid = threadIdx.x, f = blockIdx.y, r = a.r;
-  const int64_t j = (int64_t)blockIdx.x * kThreads + tid;
-  const int s = a.src_seq[f], d = a.dst_seq[f], p = a.n_pos[f];
+  const int64_t j0 = (int64_t)blockIdx.x * (kThreads * kForkPer) + tid;
+  const int s = a.src_seq[f], d = a.dst_seq[f], p = a.n_pos[f], ts = a.tail_slot[f];
   unsigned bad = 0u;
   int64_t so = 0, to = 0;
-  int nb = 0, tail = 0, slot = -1, ts = -1;
+  int nb = 0, tail = 0, slot = -1;
+  int v[kForkPer];
   if (s < 0 || s >= a.n_seq || d < 0 || d >= a.n_seq || p < 0) {
     bad = kErrToken;
   } else {
@@ -139,217 +146,319 @@ k_seq_fork(const ForkArgs a, unsigned* err) {
     const int64_t need = nb + (tail > 0 ? 1 : 0), sl = a.seq_blk_off[s + 1], tl = a.seq_blk_off[d + 1];
     if (nb > a.max_blocks) bad |= kErrMaxBlocks;
     if (so < 0 || to < 0 || sl > a.n_list || tl > a.n_list || so + need > sl || to + need > tl) bad |= kErrBlockList;
+    if (!bad) {
+#pragma unroll
+      for (int i = 0; i < kForkPer; ++i)
+        if (j0 + i * kThreads < nb) v[i] = a.seq_blk_slots[so + j0 + i * kThreads];
+    }
     if (!bad && tail > 0) {
       slot = a.seq_blk_slots[so + nb];
-      ts = a.tail_slot[f];
       if (slot < 0 || slot >= a.n_slots || ts < 0 || ts >= a.n_slots || slot == ts) bad |= kErrSlot;
-      for (int x = 0; x < tail && !bad; ++x) {
+      for (int x = 0; x < tail && !(bad & kErrSlot); ++x) {
         const int c = a.tail_cells[(int64_t)f * r + x], o = a.blk_cells[(int64_t)slot * r + x];
         if (c < 0 || c >= a.n_cells || o < 0 || o >= a.n_cells) bad |= kErrCell;
       }
     }
   }
-  // A sequence forked onto itself gets a tail of its own: the tail's list entry
-  // is both read above and written below.  This CTA's threads have all read it
-  // at the barrier; in the other CTAs either value leads to the same whole
-  // blocks (copied onto themselves).
-  __syncthreads();
-  if (bad && blockIdx.x == 0 && tid == 0) atomicOr(err, bad);
-  if (blockIdx.x == 0 && tid < r) {
-    const bool has = !bad && tid < tail;
-    const int from = has ? a.blk_cells[(int64_t)slot * r + tid] : -1;
-    const int cell = has ? a.tail_cells[(int64_t)f * r + tid] : -1;
-    a.copy_src[(int64_t)f * r + tid] = from;
-    a.copy_dst[(int64_t)f * r + tid] = cell;
-    if (!bad && tail > 0) {
-      a.blk_cells[(int64_t)ts * r + tid] = cell;
-      if (tid == 0) a.slot_block_idx[ts] = nb;
+  if (blockIdx.x == 0) {
+    // A sequence forked onto itself gets a tail of its own: the tail's list
+    // entry is both read above and written below.  This CTA's threads have all
+    // read it at the barrier; in the other CTAs either value leads to the same
+    // whole blocks (copied onto themselves).
+    __syncthreads();
+    if (bad && tid == 0) atomicOr(err, bad);
+    if (tid < r) {
+      const bool has = !bad && tid < tail;
+      const int from = has ? a.blk_cells[(int64_t)slot * r + tid] : -1;
+      const int cell = has ? a.tail_cells[(int64_t)f * r + tid] : -1;
+      a.copy_src[(int64_t)f * r + tid] = from;
+      a.copy_dst[(int64_t)f * r + tid] = cell;
+      if (!bad && tail > 0) {
+        a.blk_cells[(int64_t)ts * r + tid] = cell;
+        if (tid == 0) {
+          a.slot_block_idx[ts] = nb;
+          a.seq_blk_slots[to + nb] = ts;
+        }
+      }
     }
   }
-  if (bad) return;
-  if (j < nb) a.seq_blk_slots[to + j] = a.seq_blk_slots[so + j];
-  if (tail > 0 && blockIdx.x == 0 && tid == 0) a.seq_blk_slots[to + nb] = ts;
+  if (!bad) {
+#pragma unroll
+    for (int i = 0; i < kForkPer; ++i)
+      if (j0 + i * kThreads < nb) a.seq_blk_slots[to + j0 + i * kThreads] = v[i];
+  }
   __threadfence();
 }
 
 // ---------------------------------------------------------- qsa_cache_sweep
-constexpr int kTileWords = 256;              // bitmap words of one CTA: 8,192 cells or slots
+// Five phases, each a loop over all threads (or, by tiles of 4,096 cells or
+// slots, over all CTAs) of whatever runs it:
+//   clear   a byte of every cell and slot
+//   mark    a thread per list entry: the slot it names is held while the
+//           sequence's positions reach its block, and with it the cells of
+//           those positions (plain byte stores; atomics on bits took longer)
+//   count   held cells and slots of each tile
+//   apply   ranks: free lists, moves, cell_map
+//   table   the block table under the new places
+// A small cache is swept by one cluster with its hardware barrier between the
+// phases, one launch in all; a large one by five kernels over the whole GPU.
+constexpr int kSweepThreads = 1024, kSweepWarps = kSweepThreads / 32;
+constexpr int kTile = 4 * kSweepThreads;        // a thread's four flags of a tile
+constexpr int kSweepCluster = 16;
+// A cluster sweeps caches of up to so many cells, list entries and slots: the
+// device time is then that of the five kernels (9 us at 1,000 cells, 17 and 16
+// us at 50,000) and the host makes one launch instead of five (some 8 us); at
+// 100,000 cells the cluster's 16 SMs take 24 us, the five kernels 16 us.
+constexpr int64_t kSweepClusterCells = 65536;
+constexpr int kSweepSeqs = 256;                 // sequences whose lists a CTA keeps in shared memory
 
-__global__ void __launch_bounds__(kThreads) k_sweep_clear(uint4* bits, int64_t n16) {
-  grid_dep_wait();
-  grid_dep_launch();
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i < n16) bits[i] = make_uint4(0u, 0u, 0u, 0u);
+struct SweepSmem {
+  unsigned tmp[2][kSweepWarps];
+  int64_t off[kSweepSeqs + 1];
+  int len[kSweepSeqs];
+};
+
+__device__ __forceinline__ void sweep_clear(const SweepArgs& a, int64_t i0, int64_t n) {
+  uint4* p = reinterpret_cast<uint4*>(a.cell_flags);   // the slots' flags follow
+  const int64_t all = (a.cell_tiles + a.slot_tiles) * (kTile / 16);
+  for (int64_t i = i0; i < all; i += n) p[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// One thread per list entry: the slot it names is held while the sequence's
-// positions reach its block, and with it the cells of those positions.
-__global__ void __launch_bounds__(kThreads) k_sweep_mark(const SweepArgs a, unsigned* err) {
-  grid_dep_wait();
-  grid_dep_launch();
-  const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (e < a.n_seq) {   // a length that its list cannot hold
-    const int64_t cap = a.seq_blk_off[e + 1] - a.seq_blk_off[e];
-    if (a.seq_len[e] > 0 && (a.seq_len[e] + (int64_t)a.r - 1) / a.r > cap) atomicOr(err, kErrBlockList);
-  }
-  if (e >= a.n_list || e < a.seq_blk_off[0] || e >= a.seq_blk_off[a.n_seq]) return;
-  int lo = 0, hi = a.n_seq;                   // the last sequence whose list starts at or before e
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.seq_blk_off[mid] <= e) lo = mid;
-    else hi = mid;
-  }
-  const int64_t first = (e - a.seq_blk_off[lo]) * a.r;
-  const int64_t held = min((int64_t)a.seq_len[lo] - first, (int64_t)a.r);
-  if (held <= 0) return;
-  const int slot = a.seq_blk_slots[e];
-  if (slot < 0 || slot >= a.n_slots) {
-    atomicOr(err, kErrSlot);
-    return;
-  }
-  atomicOr(&a.slot_bits[slot >> 5], 1u << (slot & 31));
-  for (int i = 0; i < (int)held; ++i) {
-    const int c = a.blk_cells[(int64_t)slot * a.r + i];
-    if (c >= a.n_cells) atomicOr(err, kErrCell);
-    else if (c >= 0) atomicOr(&a.cell_bits[c >> 5], 1u << (c & 31));
-  }
-}
-
-__device__ __forceinline__ unsigned block_sum(unsigned v, unsigned* s_tmp) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-  __syncthreads();
-  if (lane == 0) s_tmp[warp] = v;
-  __syncthreads();
-  unsigned t = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) t += s_tmp[w];
-  return t;
-}
-
-// Live cells (then slots) of each tile.
-__global__ void __launch_bounds__(kThreads) k_sweep_count(const SweepArgs a) {
-  __shared__ unsigned s_tmp[kWarps];
-  grid_dep_wait();
-  grid_dep_launch();
-  const bool cells = blockIdx.x < (unsigned)a.cell_tiles;
-  const int64_t tile = cells ? blockIdx.x : blockIdx.x - a.cell_tiles;
-  const unsigned* bits = (cells ? a.cell_bits : a.slot_bits) + tile * kTileWords;
-  const unsigned sum = block_sum(__popc(bits[threadIdx.x]), s_tmp);
-  if (threadIdx.x == 0) (cells ? a.cell_sums : a.slot_sums)[tile] = sum;
-}
-
-// Ranks, free lists and moves of one tile's cells or slots.  In a compaction
-// a live cell at or past n_live is written to cell_map as -2 - (its move's
-// number); k_sweep_table resolves it.
-__global__ void __launch_bounds__(kThreads) k_sweep_apply(const SweepArgs a) {
-  __shared__ unsigned s_tmp[kWarps];
-  __shared__ unsigned s_bits[kTileWords], s_rank[kTileWords];
-  grid_dep_wait();
-  grid_dep_launch();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool cells = blockIdx.x < (unsigned)a.cell_tiles;
-  const int64_t tile = cells ? blockIdx.x : blockIdx.x - a.cell_tiles;
-  const unsigned* sums = cells ? a.cell_sums : a.slot_sums;
-  const int64_t n_tiles = cells ? a.cell_tiles : a.slot_tiles;
-  unsigned before = 0, all = 0;
-  for (int64_t k = tid; k < n_tiles; k += kThreads) {
-    const unsigned v = sums[k];
-    all += v;
-    if (k < tile) before += v;
-  }
-  before = block_sum(before, s_tmp);
-  all = block_sum(all, s_tmp);
-  const unsigned w = ((cells ? a.cell_bits : a.slot_bits) + tile * kTileWords)[tid];
-  unsigned incl = __popc(w);
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned y = __shfl_up_sync(kFull, incl, o);
-    if (lane >= o) incl += y;
-  }
-  __syncthreads();
-  if (lane == 31) s_tmp[warp] = incl;
-  s_bits[tid] = w;
-  __syncthreads();
-  unsigned rank = before + incl - __popc(w);
-  for (int k = 0; k < warp; ++k) rank += s_tmp[k];
-  s_rank[tid] = rank;
-  __syncthreads();
-  // live cells below n_live: the movers' ranks start there
-  unsigned below = 0;
-  const int64_t n_live = all;
-  if (cells && a.compact) {
-    const int64_t cut = n_live / (32 * kTileWords);
-    for (int64_t k = tid; k < cut; k += kThreads) below += sums[k];
-    const int64_t cw = n_live >> 5;
-    if (cut < n_tiles) {
-      const int64_t word = cut * kTileWords + tid;
-      const unsigned v = a.cell_bits[word];
-      if (word < cw) below += __popc(v);
-      if (word == cw) below += __popc(v & ((1u << (n_live & 31)) - 1u));
+__device__ __forceinline__ void sweep_mark(const SweepArgs& a, int64_t i0, int64_t n, SweepSmem& sm, unsigned* err) {
+  const bool near = a.n_seq <= kSweepSeqs;
+  if (near) {
+    for (int i = threadIdx.x; i <= a.n_seq; i += kSweepThreads) {
+      sm.off[i] = a.seq_blk_off[i];
+      if (i < a.n_seq) sm.len[i] = a.seq_len[i];
     }
-    below = block_sum(below, s_tmp);
+    __syncthreads();
   }
-  if (tid == 0 && tile == 0) {
-    if (cells) {
-      a.counts[0] = (int)all;
-      a.counts[1] = (int)(a.n_cells - n_live);
-      a.counts[3] = a.compact ? (int)(all - below) : 0;
-    } else {
-      a.counts[2] = (int)(a.n_slots - (int64_t)all);
+  const int64_t* off = near ? sm.off : a.seq_blk_off;
+  const int32_t* len = near ? sm.len : a.seq_len;
+  const int64_t lists = off[a.n_seq] < a.n_list ? off[a.n_seq] : a.n_list;
+  const int64_t end = lists > a.n_seq ? lists : a.n_seq;
+  for (int64_t e = i0; e < end; e += n) {
+    if (e < a.n_seq) {   // a length that its list cannot hold
+      if (len[e] > 0 && (len[e] + (int64_t)a.r - 1) / a.r > off[e + 1] - off[e]) atomicOr(err, kErrBlockList);
     }
-  }
-  const int64_t n = cells ? a.n_cells : a.n_slots;
-  for (int i = tid; i < 32 * kTileWords; i += kThreads) {
-    const int64_t c = tile * (32 * kTileWords) + i;
-    if (c >= n) break;
-    const unsigned word = s_bits[i >> 5];
-    const bool live = (word >> (i & 31)) & 1u;
-    const int64_t rk = (int64_t)s_rank[i >> 5] + __popc(word & ((1u << (i & 31)) - 1u));
-    if (!cells) {
-      if (!live && a.free_slots) a.free_slots[c - rk] = (int)c;
+    if (e >= lists || e < off[0]) continue;
+    const int slot = a.seq_blk_slots[e];
+    int lo = 0, hi = a.n_seq;                   // the last sequence whose list starts at or before e
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (off[mid] <= e) lo = mid;
+      else hi = mid;
+    }
+    const int64_t held = len[lo] - (e - off[lo]) * a.r;
+    if (held <= 0) continue;
+    if (slot < 0 || slot >= a.n_slots) {
+      atomicOr(err, kErrSlot);
       continue;
     }
-    int map = live ? (int)c : -1;
-    if (a.compact) {
-      if (live && c >= n_live) {
-        const int64_t k = rk - below;
-        a.move_src[k] = (int)c;
-        map = (int)(-2 - k);
-      }
-      if (!live && c < n_live) a.move_dst[c - rk] = (int)c;
-      if (c >= n_live && a.free_cells) a.free_cells[c - n_live] = (int)c;
-    } else if (!live && a.free_cells) {
-      a.free_cells[c - rk] = (int)c;
+    a.slot_flags[slot] = 1;
+    const int32_t* row = a.blk_cells + (int64_t)slot * a.r;
+    int c[8];   // compress_ratio is at most 8
+    if (a.r == 4 && a.rows16) {
+      const int4 v = *reinterpret_cast<const int4*>(row);
+      c[0] = v.x, c[1] = v.y, c[2] = v.z, c[3] = v.w;
+#pragma unroll
+      for (int i = 4; i < 8; ++i) c[i] = -1;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = i < a.r ? row[i] : -1;
     }
-    if (a.cell_map) a.cell_map[c] = map;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i >= held || c[i] < 0) continue;
+      if (c[i] >= a.n_cells) atomicOr(err, kErrCell);
+      else a.cell_flags[c[i]] = 1;
+    }
+  }
+}
+
+// This thread's four flags of a tile, a byte each.
+__device__ __forceinline__ unsigned sweep_flags(const SweepArgs& a, int64_t tile) {
+  return __ldcg(reinterpret_cast<const unsigned*>(a.cell_flags + tile * kTile) + threadIdx.x);
+}
+
+// Sums of x and of y over the CTA, in every thread.
+__device__ __forceinline__ uint2 block_sums(unsigned x, unsigned y, SweepSmem& sm) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  x = __reduce_add_sync(kFull, x);
+  y = __reduce_add_sync(kFull, y);
+  __syncthreads();
+  if (lane == 0) sm.tmp[0][warp] = x, sm.tmp[1][warp] = y;
+  __syncthreads();
+  static_assert(kSweepWarps == 32, "one partial per lane");
+  return make_uint2(__reduce_add_sync(kFull, sm.tmp[0][lane]), __reduce_add_sync(kFull, sm.tmp[1][lane]));
+}
+
+// Tiles [0, cell_tiles) are cells', the others slots' (whose flags follow).
+__device__ __forceinline__ void sweep_count(const SweepArgs& a, int64_t t0, int64_t n, SweepSmem& sm) {
+  for (int64_t t = t0; t < a.cell_tiles + a.slot_tiles; t += n) {
+    const uint2 sum = block_sums(__popc(sweep_flags(a, t)), 0u, sm);
+    if (threadIdx.x == 0) a.sums[t] = sum.x;
+  }
+}
+
+// In a compaction a held cell at or past n_held is written to cell_map as
+// -2 - (its move's number); sweep_table resolves it.
+__device__ __forceinline__ void sweep_apply(const SweepArgs& a, int64_t t0, int64_t n, SweepSmem& sm) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int64_t t = t0; t < a.cell_tiles + a.slot_tiles; t += n) {
+    const bool cells = t < a.cell_tiles;
+    const int64_t tile = cells ? t : t - a.cell_tiles, tiles = cells ? a.cell_tiles : a.slot_tiles;
+    const unsigned* sums = a.sums + (cells ? 0 : a.cell_tiles);
+    const unsigned w = sweep_flags(a, t);
+    unsigned before = 0, all = 0;
+    for (int64_t k = tid; k < tiles; k += kSweepThreads) {
+      const unsigned v = __ldcg(sums + k);
+      all += v;
+      if (k < tile) before += v;
+    }
+    const uint2 s2 = block_sums(before, all, sm);
+    const int64_t n_held = s2.y;
+    // held cells below n_held: the movers' ranks start there
+    unsigned below = 0;
+    if (cells && a.compact) {
+      const int64_t cut = n_held / kTile;
+      for (int64_t k = tid; k < cut; k += kSweepThreads) below += __ldcg(sums + k);
+      if (cut < tiles) {
+        const unsigned v = sweep_flags(a, cut);
+        const int in = (int)(n_held - cut * kTile) - 4 * tid;   // of this thread's four cells
+        if (in > 0) below += __popc(in >= 4 ? v : v & ((1u << (8 * in)) - 1u));
+      }
+    }
+    // this thread's rank: the tiles before, the warps before, the lanes before
+    unsigned incl = __popc(w);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned y = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += y;
+    }
+    below = __reduce_add_sync(kFull, below);
+    __syncthreads();
+    if (lane == 31) sm.tmp[0][warp] = incl;
+    if (lane == 0) sm.tmp[1][warp] = below;
+    __syncthreads();
+    below = __reduce_add_sync(kFull, sm.tmp[1][lane]);
+    int64_t rk = s2.x + __reduce_add_sync(kFull, lane < warp ? sm.tmp[0][lane] : 0u) + incl - __popc(w);
+    if (tid == 0 && tile == 0) {
+      if (cells) {
+        a.counts[0] = (int)n_held;
+        a.counts[1] = (int)(a.n_cells - n_held);
+        a.counts[3] = a.compact ? (int)(n_held - below) : 0;
+      } else {
+        a.counts[2] = (int)(a.n_slots - n_held);
+      }
+    }
+    const int64_t c0 = tile * kTile + 4 * tid, n_of = cells ? a.n_cells : a.n_slots;
+    int map[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t c = c0 + i;
+      const bool held = (w >> (8 * i)) & 1u;
+      map[i] = held ? (int)c : -1;
+      if (c >= n_of) continue;
+      if (!cells) {
+        if (!held && a.free_slots) a.free_slots[c - rk] = (int)c;
+      } else if (a.compact) {
+        if (held && c >= n_held) {
+          const int64_t k = rk - below;
+          a.move_src[k] = (int)c;
+          map[i] = (int)(-2 - k);
+        }
+        if (!held && c < n_held) a.move_dst[c - rk] = (int)c;
+        if (c >= n_held && a.free_cells) a.free_cells[c - n_held] = (int)c;
+      } else if (!held && a.free_cells) {
+        a.free_cells[c - rk] = (int)c;
+      }
+      rk += held;
+    }
+    if (cells && a.cell_map) {
+      if (a.map16 && c0 + 4 <= n_of) {
+        *reinterpret_cast<int4*>(a.cell_map + c0) = make_int4(map[0], map[1], map[2], map[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (c0 + i < n_of) a.cell_map[c0 + i] = map[i];
+      }
+    }
   }
 }
 
 // The block table without what nobody holds, under the cells' new places; and
-// the movers' entries of cell_map.
-__global__ void __launch_bounds__(kThreads) k_sweep_table(const SweepArgs a) {
-  grid_dep_wait();
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i < a.n_slots * a.r) {
-    const int64_t slot = i / a.r;
-    const int c = a.blk_cells[i];
-    int v = -1;
-    if (c >= 0 && c < a.n_cells && ((a.slot_bits[slot >> 5] >> (slot & 31)) & 1u)) {
-      if (a.compact) {
-        // the entry of a mover may already be resolved by its own thread
-        v = *reinterpret_cast<volatile const int32_t*>(a.cell_map + c);
-        if (v < -1) v = a.move_dst[-2 - v];
-      } else {
-        v = ((a.cell_bits[c >> 5] >> (c & 31)) & 1u) ? c : -1;
-      }
+// the movers' entries of cell_map (either form of an entry gives its place, so
+// the two may meet).
+__device__ __forceinline__ void sweep_table(const SweepArgs& a, int64_t i0, int64_t n) {
+  const int64_t moves = a.compact ? __ldcg(a.counts + 3) : 0;
+  auto place = [&](int c) -> int {
+    if (c < 0 || c >= a.n_cells) return -1;
+    if (!a.compact) return __ldcg(a.cell_flags + c) ? c : -1;
+    const int v = *reinterpret_cast<volatile const int32_t*>(a.cell_map + c);
+    return v < -1 ? __ldcg(a.move_dst + (-2 - v)) : v;
+  };
+  for (int64_t slot = i0; slot < a.n_slots; slot += n) {
+    const bool held = __ldcg(a.slot_flags + slot) != 0;
+    const int32_t* row = a.blk_cells + slot * a.r;
+    int32_t* out = a.blk_cells_out + slot * a.r;
+    if (a.r == 4 && a.rows16) {
+      const int4 v = *reinterpret_cast<const int4*>(row);
+      int4 o = make_int4(-1, -1, -1, -1);
+      if (held) o = make_int4(place(v.x), place(v.y), place(v.z), place(v.w));
+      *reinterpret_cast<int4*>(out) = o;
+    } else {
+      for (int i = 0; i < a.r; ++i) out[i] = held ? place(row[i]) : -1;
     }
-    a.blk_cells_out[i] = v;
   }
-  if (a.compact && i < a.counts[3]) {
-    *reinterpret_cast<volatile int32_t*>(a.cell_map + a.move_src[i]) = a.move_dst[i];
-  }
+  for (int64_t k = i0; k < moves; k += n)
+    *reinterpret_cast<volatile int32_t*>(a.cell_map + __ldcg(a.move_src + k)) = __ldcg(a.move_dst + k);
+}
+
+__device__ __forceinline__ int64_t grid_thread() { return (int64_t)blockIdx.x * kSweepThreads + threadIdx.x; }
+__device__ __forceinline__ int64_t grid_threads() { return (int64_t)gridDim.x * kSweepThreads; }
+
+__global__ void __launch_bounds__(kSweepThreads) k_sweep_clear(const SweepArgs a) {
+  grid_dep_wait();
+  grid_dep_launch();
+  sweep_clear(a, grid_thread(), grid_threads());
+}
+__global__ void __launch_bounds__(kSweepThreads) k_sweep_mark(const SweepArgs a, unsigned* err) {
+  __shared__ SweepSmem sm;
+  grid_dep_wait();
+  grid_dep_launch();
+  sweep_mark(a, grid_thread(), grid_threads(), sm, err);
+}
+__global__ void __launch_bounds__(kSweepThreads) k_sweep_count(const SweepArgs a) {
+  __shared__ SweepSmem sm;
+  grid_dep_wait();
+  grid_dep_launch();
+  sweep_count(a, blockIdx.x, gridDim.x, sm);
+}
+__global__ void __launch_bounds__(kSweepThreads) k_sweep_apply(const SweepArgs a) {
+  __shared__ SweepSmem sm;
+  grid_dep_wait();
+  grid_dep_launch();
+  sweep_apply(a, blockIdx.x, gridDim.x, sm);
+}
+__global__ void __launch_bounds__(kSweepThreads) k_sweep_table(const SweepArgs a) {
+  grid_dep_wait();
+  sweep_table(a, grid_thread(), grid_threads());
+  __threadfence();
+}
+// All of it by one cluster; its barrier orders the phases' global writes.
+__global__ void __launch_bounds__(kSweepThreads) k_sweep_cluster(const SweepArgs a, unsigned* err) {
+  __shared__ SweepSmem sm;
+  grid_dep_wait();
+  sweep_clear(a, grid_thread(), grid_threads());
+  cluster_sync();
+  sweep_mark(a, grid_thread(), grid_threads(), sm, err);
+  cluster_sync();
+  sweep_count(a, blockIdx.x, gridDim.x, sm);
+  cluster_sync();
+  sweep_apply(a, blockIdx.x, gridDim.x, sm);
+  cluster_sync();
+  sweep_table(a, grid_thread(), grid_threads());
   __threadfence();
 }
 
@@ -379,7 +488,7 @@ cudaError_t launch_cells_copy(const CopyArgs& a, unsigned* err, cudaStream_t str
 
 cudaError_t launch_seq_fork(const ForkArgs& a, unsigned* err, cudaStream_t stream) {
   if (a.n <= 0) return cudaSuccess;
-  const int64_t x = ceil_div(a.max_blocks > 0 ? a.max_blocks : 1, kThreads);
+  const int64_t x = ceil_div(a.max_blocks > 0 ? a.max_blocks : 1, kThreads * kForkPer);
   prof_before(kKFork, stream);
   cudaError_t e = launch_pdl(k_seq_fork, dim3((unsigned)x, (unsigned)a.n), dim3(kThreads), 0, stream, 1, a, err);
   prof_after(kKFork, stream);
@@ -387,34 +496,74 @@ cudaError_t launch_seq_fork(const ForkArgs& a, unsigned* err, cudaStream_t strea
   return cudaGetLastError();
 }
 
-// Workspace: the two bitmaps in whole tiles, then the tiles' sums.
-static int64_t sweep_tiles(int64_t n) { return ceil_div(n > 0 ? n : 1, 32 * kTileWords); }
+// Workspace: the cells' flags and the slots', in whole tiles, then the tiles' sums.
+static int64_t sweep_tiles(int64_t n) { return ceil_div(n > 0 ? n : 1, kTile); }
 size_t sweep_workspace_bytes(int64_t n_cells, int64_t n_slots) {
-  const int64_t tc = sweep_tiles(n_cells), ts = sweep_tiles(n_slots);
-  return (size_t)round_up((tc + ts) * kTileWords * 4 + (tc + ts) * 4, 256);
+  const int64_t tiles = sweep_tiles(n_cells) + sweep_tiles(n_slots);
+  return (size_t)round_up(tiles * kTile + tiles * 4, 256);
+}
+
+// Clusters of kSweepCluster CTAs can run on the current device (asked once per device).
+static cudaError_t sweep_cluster_ok(bool* ok) {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> known[kMaxDevices];   // 0: not asked, 1: no, 2: yes
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  int k = known[dev].load(std::memory_order_acquire);
+  if (k == 0) {
+    k = 1;
+    if (cudaFuncSetAttribute(k_sweep_cluster, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(kSweepCluster);
+      cfg.blockDim = dim3(kSweepThreads);
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = kSweepCluster;
+      attr.val.clusterDim.y = 1;
+      attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, k_sweep_cluster, &cfg) == cudaSuccess && n > 0) k = 2;
+    }
+    (void)cudaGetLastError();
+    known[dev].store(k, std::memory_order_release);
+  }
+  *ok = k == 2;
+  return cudaSuccess;
 }
 
 cudaError_t launch_cache_sweep(const SweepArgs& args, void* ws, unsigned* err, cudaStream_t stream) {
   SweepArgs a = args;
   a.cell_tiles = sweep_tiles(a.n_cells);
   a.slot_tiles = sweep_tiles(a.n_slots);
+  a.cell_flags = static_cast<unsigned char*>(ws);
+  a.slot_flags = a.cell_flags + a.cell_tiles * kTile;
   const int64_t tiles = a.cell_tiles + a.slot_tiles;
-  a.cell_bits = static_cast<unsigned*>(ws);
-  a.slot_bits = a.cell_bits + a.cell_tiles * kTileWords;
-  a.cell_sums = a.slot_bits + a.slot_tiles * kTileWords;
-  a.slot_sums = a.cell_sums + a.cell_tiles;
-  const int64_t n16 = tiles * kTileWords / 4;
+  a.sums = reinterpret_cast<unsigned*>(a.cell_flags + tiles * kTile);
+  a.rows16 = ((reinterpret_cast<uintptr_t>(a.blk_cells) | reinterpret_cast<uintptr_t>(a.blk_cells_out)) & 15u) == 0u;
+  a.map16 = (reinterpret_cast<uintptr_t>(a.cell_map) & 15u) == 0u;
+  const dim3 block(kSweepThreads);
+  auto grid = [](int64_t n) { return dim3((unsigned)ceil_div(n > 0 ? n : 1, kSweepThreads)); };
+  bool cluster = false;
+  if (a.n_cells <= kSweepClusterCells && a.n_list <= kSweepClusterCells && a.n_slots <= kSweepClusterCells) {
+    const cudaError_t e = sweep_cluster_ok(&cluster);
+    if (e != cudaSuccess) return e;
+  }
   const int64_t entries = a.n_list > a.n_seq ? a.n_list : a.n_seq;
-  int64_t table = a.n_slots * a.r;
-  if (a.compact && a.n_cells / 2 > table) table = a.n_cells / 2;
-  const dim3 block(kThreads);
-  auto grid = [](int64_t n) { return dim3((unsigned)ceil_div(n > 0 ? n : 1, kThreads)); };
   prof_before(kKSweep, stream);
-  cudaError_t e = launch_pdl(k_sweep_clear, grid(n16), block, 0, stream, 1, reinterpret_cast<uint4*>(ws), n16);
-  if (e == cudaSuccess) e = launch_pdl(k_sweep_mark, grid(entries), block, 0, stream, 1, a, err);
-  if (e == cudaSuccess) e = launch_pdl(k_sweep_count, dim3((unsigned)tiles), block, 0, stream, 1, a);
-  if (e == cudaSuccess) e = launch_pdl(k_sweep_apply, dim3((unsigned)tiles), block, 0, stream, 1, a);
-  if (e == cudaSuccess) e = launch_pdl(k_sweep_table, grid(table), block, 0, stream, 1, a);
+  cudaError_t e;
+  if (cluster) {
+    e = launch_pdl(k_sweep_cluster, dim3(kSweepCluster), block, 0, stream, kSweepCluster, a, err);
+  } else {
+    e = launch_pdl(k_sweep_clear, grid(tiles * (kTile / 16)), block, 0, stream, 1, a);
+    if (e == cudaSuccess) e = launch_pdl(k_sweep_mark, grid(entries), block, 0, stream, 1, a, err);
+    if (e == cudaSuccess) e = launch_pdl(k_sweep_count, dim3((unsigned)tiles), block, 0, stream, 1, a);
+    if (e == cudaSuccess) e = launch_pdl(k_sweep_apply, dim3((unsigned)tiles), block, 0, stream, 1, a);
+    if (e == cudaSuccess) e = launch_pdl(k_sweep_table, grid(a.n_slots), block, 0, stream, 1, a);
+  }
   prof_after(kKSweep, stream);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();

@@ -175,16 +175,11 @@ def _check(st: int, what: str):
 
 def _stream(stream):
     import torch
-    if stream is None:   # current_stream() would build a Stream object for it
+    if stream is None:   # (current_stream() would build a Stream object for it)
         return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
-
-
-def _elem_types():
-    import torch
-    return {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 
 
 def _ptr(t, dtype, name, allow_none=False, host_ok=False, strided=False):
@@ -193,7 +188,7 @@ def _ptr(t, dtype, name, allow_none=False, host_ok=False, strided=False):
     tensors, which the kernels read and write in place over the host link."""
     import torch
     if t.__class__ is torch.Tensor and (dtype is None or t.dtype is dtype) and (strided or t.is_contiguous()) \
-            and t.get_device() == torch._C._cuda_getDevice():   # -1 for host memory
+            and t.is_cuda and t.get_device() == torch._C._cuda_getDevice():
         return t.data_ptr()
     if t is None:
         if allow_none:
@@ -219,6 +214,33 @@ def _ptr(t, dtype, name, allow_none=False, host_ok=False, strided=False):
 def _io(t, dtype, name):
     """A step input or output: device memory or pinned host memory."""
     return _ptr(t, dtype, name, host_ok=True)
+
+
+def _at(t, dtype, dev, name, host_ok=False):
+    """_ptr of a contiguous tensor with the current device looked up by the
+    caller, once for all its tensors (the calls here take up to 13, and each
+    look at a tensor costs a tenth of a microsecond)."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _ptr(t, dtype, name, host_ok=host_ok)
+
+
+def _bytes_at(t, dev, name):
+    """_at of a cache, whose element type is the caller's business."""
+    if t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    return _ptr(t, None, name)
+
+
+def _torch_dev():
+    import torch
+    try:
+        return torch, torch._C._cuda_getDevice(), torch.int32
+    except RuntimeError:   # no GPU: no tensor is on device -2, and _ptr says what is wrong
+        return torch, -2, torch.int32
 
 
 def cells_per_token(cfg: Config) -> int:
@@ -336,15 +358,17 @@ def sparse_attn(cfg, q, k_cache, v_cache, n_cells: int, cells, count, out, works
                 union: bool = False):
     """qsa_sparse_attn (union: qsa_sparse_attn_union, token pairs over the
     union of their lists)."""
-    import torch
-    T = int(count.numel())
-    ws_ptr = _ptr(workspace, torch.uint8, "workspace") if workspace is not None and workspace.numel() else None
-    ws_len = int(workspace.numel()) if workspace is not None else 0
-    name = "qsa_sparse_attn_union" if union else "qsa_sparse_attn"
-    st = getattr(lib(), name)(
-        ctypes.byref(cfg), T, _io(q, torch.float16, "q"), _ptr(k_cache, None, "k_cache"),
-        _ptr(v_cache, None, "v_cache"), int(n_cells), _ptr(cells, torch.int32, "cells"),
-        _ptr(count, torch.int32, "count"), _io(out, torch.float32, "out"),
+    torch, dev, i32 = _torch_dev()
+    T = count.numel()
+    ws_ptr, ws_len = None, 0
+    if workspace is not None and workspace.numel():
+        ws_ptr, ws_len = _ptr(workspace, torch.uint8, "workspace"), int(workspace.numel())
+    L = lib()
+    name, call = ("qsa_sparse_attn_union", L.qsa_sparse_attn_union) if union else ("qsa_sparse_attn", L.qsa_sparse_attn)
+    st = call(
+        ctypes.byref(cfg), T, _at(q, torch.float16, dev, "q", True), _bytes_at(k_cache, dev, "k_cache"),
+        _bytes_at(v_cache, dev, "v_cache"), int(n_cells), _at(cells, i32, dev, "cells"),
+        _at(count, i32, dev, "count"), _at(out, torch.float32, dev, "out", True),
         ws_ptr, ws_len, _stream(stream))
     _check(st, name)
 
@@ -354,21 +378,21 @@ def kv_append(cfg, tok_seq, tok_pos, cells, k_new, v_new, idx_new, k_cache, v_ca
     """Write the step's new cells (K/V rows, indexer keys, block-table
     entries) and fill `dirty` with the slots of the blocks they change; with
     `pooled` (and slot_block_idx, norm_w) also re-pool those blocks."""
-    import torch
+    torch, dev, i32 = _torch_dev()
+    f16 = torch.float16
     pool_args = (None, None, None)
     if pooled is not None:
-        pool_args = (_ptr(slot_block_idx, torch.int32, "slot_block_idx"), _ptr(norm_w, torch.float32, "norm_w"),
-                     _ptr(pooled, torch.float32, "pooled"))
-    n_cells = int(idx_k.shape[0])
+        pool_args = (_at(slot_block_idx, i32, dev, "slot_block_idx"), _at(norm_w, torch.float32, dev, "norm_w"),
+                     _at(pooled, torch.float32, dev, "pooled"))
     st = lib().qsa_kv_append(
-        ctypes.byref(cfg), int(tok_pos.numel()), _io(tok_seq, torch.int32, "tok_seq"),
-        _io(tok_pos, torch.int32, "tok_pos"), _io(cells, torch.int32, "cells"),
-        _io(k_new, torch.float16, "k_new"), _io(v_new, torch.float16, "v_new"),
-        _io(idx_new, torch.float16, "idx_new"), _ptr(k_cache, None, "k_cache"), _ptr(v_cache, None, "v_cache"),
-        _ptr(idx_k, torch.float16, "idx_k"), n_cells, _ptr(blk_cells, torch.int32, "blk_cells"),
-        int(blk_cells.shape[0]), _ptr(seq_blk_off, torch.int64, "seq_blk_off"),
-        _ptr(seq_blk_slots, torch.int32, "seq_blk_slots"), int(seq_blk_off.numel()) - 1,
-        _ptr(dirty, torch.int32, "dirty"), int(dirty.numel()), *pool_args, _stream(stream))
+        ctypes.byref(cfg), tok_pos.numel(), _at(tok_seq, i32, dev, "tok_seq", True),
+        _at(tok_pos, i32, dev, "tok_pos", True), _at(cells, i32, dev, "cells", True),
+        _at(k_new, f16, dev, "k_new", True), _at(v_new, f16, dev, "v_new", True),
+        _at(idx_new, f16, dev, "idx_new", True), _bytes_at(k_cache, dev, "k_cache"), _bytes_at(v_cache, dev, "v_cache"),
+        _at(idx_k, f16, dev, "idx_k"), idx_k.shape[0], _at(blk_cells, i32, dev, "blk_cells"),
+        blk_cells.shape[0], _at(seq_blk_off, torch.int64, dev, "seq_blk_off"),
+        _at(seq_blk_slots, i32, dev, "seq_blk_slots"), seq_blk_off.numel() - 1,
+        _at(dirty, i32, dev, "dirty"), dirty.numel(), *pool_args, _stream(stream))
     _check(st, "qsa_kv_append")
 
 
@@ -385,15 +409,25 @@ def rope_config(sections, interleaved: bool = False, cfg: Optional[Config] = Non
     return r
 
 
-def _head_rows(t, heads: int, dim: int, name: str):
-    """Address, tokens and token stride of a [T][heads][dim] tensor whose
-    heads are contiguous within a token (a slice of a fused projection)."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} must be [T][{heads}][{dim}], got {list(t.shape)}")
-    s = t.stride()
-    if s[2] != 1 or (heads > 1 and s[1] != dim):
-        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {list(s)}")
-    return s[0]
+def _head_rows(x, w, out, T, heads, dim, dtype, out_dtype, torch, dev, name):
+    """(address, token stride, weight, output) of a [T][heads][dim] input
+    whose heads are contiguous within a token (a slice of a fused
+    projection), checked with its weight and output."""
+    if x is None:
+        if out is not None:
+            raise ValueError(f"the output of {name} is given without it")
+        return None, 0, None, None
+    if x.shape != (T, heads, dim):
+        raise ValueError(f"{name} must be [{T}][{heads}][{dim}], got {list(x.shape)}")
+    s0, s1, s2 = x.stride()
+    if s2 != 1 or (heads > 1 and s1 != dim):
+        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {[s0, s1, s2]}")
+    if out is None or out.numel() != T * heads * dim:
+        raise ValueError(f"{name}'s output must hold {T} tokens")
+    if w is None or w.numel() != dim:
+        raise ValueError(f"the norm weight of {name} must hold {dim} values")
+    at = x.data_ptr() if x.dtype is dtype and x.get_device() == dev else _ptr(x, dtype, name, host_ok=True, strided=True)
+    return at, s0, _at(w, torch.float32, dev, "norm weight"), _at(out, out_dtype, dev, "output", True)
 
 
 def qk_norm_rope(cfg, rope: Rope, pos, q_in, k_in, q_norm_w, k_norm_w, q, k_new, q_idx_in=None, idx_pos=None,
@@ -404,55 +438,45 @@ def qk_norm_rope(cfg, rope: Rope, pos, q_in, k_in, q_norm_w, k_norm_w, q, k_new,
     (fp16, bf16 or fp32, one type; tokens may be strided).  pos: int32
     [n_axes][T]; idx_pos: int32 [T].  q_in or k_in may be None (with its
     output)."""
-    import torch
-    L = lib()
-    given = [x for x in (q_in, k_in, q_idx_in) if x is not None]
-    if not given:
+    torch, dev, i32 = _torch_dev()
+    first = q_in if q_in is not None else k_in if k_in is not None else q_idx_in
+    if first is None:
         raise ValueError("one of q_in, k_in and q_idx_in is required")
-    T, dt = int(given[0].shape[0]), given[0].dtype
-    elem = _elem_types().get(dt)
-    if elem is None:
+    T, dt = first.shape[0], first.dtype
+    elem = 0 if dt is torch.float16 else 1 if dt is torch.bfloat16 else 2 if dt is torch.float32 else -1
+    if elem < 0:
         raise TypeError(f"inputs must be fp16, bf16 or fp32, got {dt}")
-
-    def part(x, w, out, heads, dim, name, out_dtype):
-        if x is None:
-            if out is not None:
-                raise ValueError(f"the output of {name} is given without it")
-            return None, 0, None, None
-        stride = _head_rows(x, heads, dim, name)
-        if x.shape[0] != T or out is None or out.numel() != T * heads * dim:
-            raise ValueError(f"{name} and its output must hold {T} tokens")
-        if w is None or w.numel() != dim:
-            raise ValueError(f"the norm weight of {name} must hold {dim} values")
-        return (_ptr(x, dt, name, host_ok=True, strided=True), stride, _ptr(w, torch.float32, "norm weight"),
-                _io(out, out_dtype, "output"))
-
-    qp, qs, qw, qo = part(q_in, q_norm_w, q, cfg.n_q_heads, cfg.head_dim, "q_in", torch.float16)
-    kp, ks, kw, ko = part(k_in, k_norm_w, k_new, cfg.n_kv_heads, cfg.head_dim, "k_in", torch.float16)
-    ip, is_, iw, io = part(q_idx_in, q_idx_norm_w, q_idx, cfg.n_idx_heads, cfg.idx_dim, "q_idx_in", torch.float32)
-    if (qp or kp) and pos.numel() != rope.n_axes * T:
-        raise ValueError(f"pos must hold {rope.n_axes} x {T} positions")
-    if ip and idx_pos.numel() != T:
-        raise ValueError(f"idx_pos must hold {T} positions")
-    st = L.qsa_qk_norm_rope(
-        ctypes.byref(cfg), ctypes.byref(rope), T, elem, _io(pos, torch.int32, "pos") if pos is not None else None,
-        qp, qs, kp, ks, qw, kw, qo, ko, _io(idx_pos, torch.int32, "idx_pos") if idx_pos is not None else None,
-        ip, is_, iw, io, _stream(stream))
+    qp, qs, qw, qo = _head_rows(q_in, q_norm_w, q, T, cfg.n_q_heads, cfg.head_dim, dt, torch.float16, torch, dev, "q_in")
+    kp, ks, kw, ko = _head_rows(k_in, k_norm_w, k_new, T, cfg.n_kv_heads, cfg.head_dim, dt, torch.float16, torch, dev,
+                                "k_in")
+    ip, is_, iw, io = _head_rows(q_idx_in, q_idx_norm_w, q_idx, T, cfg.n_idx_heads, cfg.idx_dim, dt, torch.float32,
+                                 torch, dev, "q_idx_in")
+    at, iat = None, None
+    if qp or kp:
+        if pos.numel() != rope.n_axes * T:
+            raise ValueError(f"pos must hold {rope.n_axes} x {T} positions")
+        at = _at(pos, i32, dev, "pos", True)
+    if ip:
+        if idx_pos.numel() != T:
+            raise ValueError(f"idx_pos must hold {T} positions")
+        iat = _at(idx_pos, i32, dev, "idx_pos", True)
+    st = lib().qsa_qk_norm_rope(ctypes.byref(cfg), ctypes.byref(rope), T, elem, at, qp, qs, kp, ks, qw, kw, qo, ko, iat,
+                                ip, is_, iw, io, _stream(stream))
     _check(st, "qsa_qk_norm_rope")
 
 
 def kv_read(cfg, cells, k_cache, v_cache, n_cells: int, k_out, v_out, stream=None):
     """K and V rows of the listed cells as fp16 values, [n][n_kv_heads][head_dim]
     each (entries < 0 are skipped)."""
-    import torch
-    n = int(cells.numel())
+    torch, dev, i32 = _torch_dev()
+    n = cells.numel()
     want = n * cfg.n_kv_heads * cfg.head_dim
     if k_out.numel() != want or v_out.numel() != want:
         raise ValueError(f"k_out and v_out must hold {n} rows")
     _check_cache(cfg, k_cache, v_cache, n_cells)
-    st = lib().qsa_kv_read(ctypes.byref(cfg), n, _ptr(cells, torch.int32, "cells"), _ptr(k_cache, None, "k_cache"),
-                           _ptr(v_cache, None, "v_cache"), int(n_cells), _ptr(k_out, torch.float16, "k_out"),
-                           _ptr(v_out, torch.float16, "v_out"), _stream(stream))
+    st = lib().qsa_kv_read(ctypes.byref(cfg), n, _at(cells, i32, dev, "cells"), _bytes_at(k_cache, dev, "k_cache"),
+                           _bytes_at(v_cache, dev, "v_cache"), int(n_cells), _at(k_out, torch.float16, dev, "k_out"),
+                           _at(v_out, torch.float16, dev, "v_out"), _stream(stream))
     _check(st, "qsa_kv_read")
 
 
@@ -465,26 +489,26 @@ def cache_bytes(cfg, n_cells: int) -> int:
 
 def _check_cache(cfg, k_cache, v_cache, n_cells: int):
     need = cache_bytes(cfg, n_cells)
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.numel() * t.element_size() < need:
-            raise ValueError(f"{name} holds {t.numel() * t.element_size()} bytes, {n_cells} cells need {need}")
+    if k_cache.nbytes < need or v_cache.nbytes < need:
+        raise ValueError(f"k_cache and v_cache hold {k_cache.nbytes} and {v_cache.nbytes} bytes, {n_cells} cells need "
+                         f"{need} each")
 
 
 def cells_copy(cfg, src, dst, k_cache, v_cache, idx_k, n_cells: int, n_pairs=None, stream=None):
     """Copy the K and V rows (as stored) and, unless idx_k is None, the
     indexer key of cell src[i] to cell dst[i].  n_pairs: optional int32 CUDA
     tensor of one element, how many of the pairs count."""
-    import torch
-    n = int(src.numel())
+    torch, dev, i32 = _torch_dev()
+    n = src.numel()
     if dst.numel() != n:
         raise ValueError("src and dst must have the same length")
     _check_cache(cfg, k_cache, v_cache, n_cells)
     if idx_k is not None and idx_k.numel() < int(n_cells) * cfg.idx_dim:
         raise ValueError(f"idx_k must hold {n_cells} rows")
     st = lib().qsa_cells_copy(
-        ctypes.byref(cfg), n, _ptr(n_pairs, torch.int32, "n_pairs", allow_none=True), _ptr(src, torch.int32, "src"),
-        _ptr(dst, torch.int32, "dst"), _ptr(k_cache, None, "k_cache"), _ptr(v_cache, None, "v_cache"),
-        _ptr(idx_k, torch.float16, "idx_k", allow_none=True), int(n_cells), _stream(stream))
+        ctypes.byref(cfg), n, None if n_pairs is None else _at(n_pairs, i32, dev, "n_pairs"), _at(src, i32, dev, "src"),
+        _at(dst, i32, dev, "dst"), _bytes_at(k_cache, dev, "k_cache"), _bytes_at(v_cache, dev, "v_cache"),
+        None if idx_k is None else _at(idx_k, torch.float16, dev, "idx_k"), int(n_cells), _stream(stream))
     _check(st, "qsa_cells_copy")
 
 
@@ -494,24 +518,21 @@ def seq_fork(cfg, src_seq, dst_seq, n_pos, tail_slot, tail_cells, seq_blk_off, s
     whole blocks shared, a partial last block private (tail_slot[f],
     tail_cells[f]); copy_src / copy_dst [n_fork][r] get the pairs for
     cells_copy."""
-    import torch
-    n, r = int(src_seq.numel()), cfg.compress_ratio
-    for t, name, want in ((dst_seq, "dst_seq", n), (n_pos, "n_pos", n), (tail_slot, "tail_slot", n),
-                          (tail_cells, "tail_cells", n * r), (copy_src, "copy_src", n * r),
-                          (copy_dst, "copy_dst", n * r)):
-        if t.numel() != want:
-            raise ValueError(f"{name} must hold {want} values")
-    n_slots = int(blk_cells.shape[0])
+    torch, dev, i32 = _torch_dev()
+    n, r, n_slots = src_seq.numel(), cfg.compress_ratio, blk_cells.shape[0]
+    if not (dst_seq.numel() == n_pos.numel() == tail_slot.numel() == n
+            and tail_cells.numel() == copy_src.numel() == copy_dst.numel() == n * r):
+        raise ValueError(f"dst_seq, n_pos and tail_slot must hold {n} values, tail_cells, copy_src and copy_dst {n * r}")
     if blk_cells.numel() != n_slots * r or slot_block_idx.numel() < n_slots:
         raise ValueError("blk_cells must be [n_slots][r] and slot_block_idx hold n_slots values")
     st = lib().qsa_seq_fork(
-        ctypes.byref(cfg), n, _ptr(src_seq, torch.int32, "src_seq"), _ptr(dst_seq, torch.int32, "dst_seq"),
-        _ptr(n_pos, torch.int32, "n_pos"), _ptr(tail_slot, torch.int32, "tail_slot"),
-        _ptr(tail_cells, torch.int32, "tail_cells"), _ptr(seq_blk_off, torch.int64, "seq_blk_off"),
-        _ptr(seq_blk_slots, torch.int32, "seq_blk_slots"), int(seq_blk_off.numel()) - 1, int(seq_blk_slots.numel()),
-        _ptr(blk_cells, torch.int32, "blk_cells"), _ptr(slot_block_idx, torch.int32, "slot_block_idx"),
+        ctypes.byref(cfg), n, _at(src_seq, i32, dev, "src_seq"), _at(dst_seq, i32, dev, "dst_seq"),
+        _at(n_pos, i32, dev, "n_pos"), _at(tail_slot, i32, dev, "tail_slot"),
+        _at(tail_cells, i32, dev, "tail_cells"), _at(seq_blk_off, torch.int64, dev, "seq_blk_off"),
+        _at(seq_blk_slots, i32, dev, "seq_blk_slots"), seq_blk_off.numel() - 1, seq_blk_slots.numel(),
+        _at(blk_cells, i32, dev, "blk_cells"), _at(slot_block_idx, i32, dev, "slot_block_idx"),
         n_slots, int(n_cells), int(max_blocks),
-        _ptr(copy_src, torch.int32, "copy_src"), _ptr(copy_dst, torch.int32, "copy_dst"), _stream(stream))
+        _at(copy_src, i32, dev, "copy_src"), _at(copy_dst, i32, dev, "copy_dst"), _stream(stream))
     _check(st, "qsa_seq_fork")
 
 
@@ -525,25 +546,26 @@ def cache_sweep(cfg, seq_len, seq_blk_off, seq_blk_slots, blk_cells, blk_cells_o
     """Free what the sequences no longer hold (seq_len[s] positions each), and
     with compact=True plan the moves that bring the held cells together:
     counts[4] = held cells, free cells, free slots, moves; see qsa.h."""
-    import torch
-    n_slots, n = int(blk_cells.shape[0]), int(n_cells)
-    n_seq = int(seq_blk_off.numel()) - 1
-    for t, name, want in ((seq_len, "seq_len", n_seq), (counts, "counts", 4), (cell_map, "cell_map", n),
-                          (free_cells, "free_cells", n), (free_slots, "free_slots", n_slots),
-                          (move_src, "move_src", n // 2), (move_dst, "move_dst", n // 2),
-                          (blk_cells, "blk_cells", n_slots * cfg.compress_ratio),
-                          (blk_cells_out, "blk_cells_out", n_slots * cfg.compress_ratio)):
-        if t is not None and t.numel() < want:
+    torch, dev, i32 = _torch_dev()
+    n_slots, n = blk_cells.shape[0], int(n_cells)
+    n_seq, table = seq_blk_off.numel() - 1, n_slots * cfg.compress_ratio
+
+    def some(t, want, name):   # an int32 buffer of at least `want` values, or None
+        if t is None:
+            return None
+        if t.numel() < want:
             raise ValueError(f"{name} must hold {want} values, got {t.numel()}")
-    i32 = torch.int32
+        return _at(t, i32, dev, name)
+
+    if seq_len is None or counts is None or blk_cells_out is None:
+        raise ValueError("seq_len, counts and blk_cells_out are required")
     st = lib().qsa_cache_sweep(
-        ctypes.byref(cfg), QSA_SWEEP_COMPACT if compact else 0, _ptr(seq_len, i32, "seq_len"),
-        _ptr(seq_blk_off, torch.int64, "seq_blk_off"), _ptr(seq_blk_slots, i32, "seq_blk_slots"), n_seq,
-        int(seq_blk_slots.numel()), _ptr(blk_cells, i32, "blk_cells"), _ptr(blk_cells_out, i32, "blk_cells_out"),
-        n_slots, n, _ptr(counts, i32, "counts"), _ptr(cell_map, i32, "cell_map", allow_none=True),
-        _ptr(free_cells, i32, "free_cells", allow_none=True), _ptr(free_slots, i32, "free_slots", allow_none=True),
-        _ptr(move_src, i32, "move_src", allow_none=True), _ptr(move_dst, i32, "move_dst", allow_none=True),
-        _ptr(workspace, torch.uint8, "workspace"), int(workspace.numel()), _stream(stream))
+        ctypes.byref(cfg), QSA_SWEEP_COMPACT if compact else 0, some(seq_len, n_seq, "seq_len"),
+        _at(seq_blk_off, torch.int64, dev, "seq_blk_off"), _at(seq_blk_slots, i32, dev, "seq_blk_slots"), n_seq,
+        seq_blk_slots.numel(), some(blk_cells, table, "blk_cells"), some(blk_cells_out, table, "blk_cells_out"),
+        n_slots, n, some(counts, 4, "counts"), some(cell_map, n, "cell_map"), some(free_cells, n, "free_cells"),
+        some(free_slots, n_slots, "free_slots"), some(move_src, n // 2, "move_src"), some(move_dst, n // 2, "move_dst"),
+        _at(workspace, torch.uint8, dev, "workspace"), workspace.numel(), _stream(stream))
     _check(st, "qsa_cache_sweep")
 
 
