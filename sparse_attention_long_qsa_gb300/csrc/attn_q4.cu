@@ -49,7 +49,6 @@ constexpr int kMaxCluster = 16;
 // of them, stays a normal half for all that count; s may pass the running
 // maximum m by kLazy before m follows.  2^(kUp + kLazy) <= 2^15.
 constexpr float kUp = 7.f, kLazy = 8.f;
-constexpr int kFixed = 4;                        // a CTA's prologue and merge, in chunks
 constexpr int kNoExp = 32;                       // no scale of V seen yet
 constexpr float kNoMax = -3.0e38f;               // no cell seen yet (below every score, and finite)
 constexpr int kBlocks = kHeadDim / 32;           // q4_0 blocks of a row
@@ -534,10 +533,10 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
 constexpr int kMaxDevices = 64;
 
 // Clusters of 16, 8, 4, 2, 1 CTAs of k_attn_q4<kWarps> that fit the current
-// device at once, measured once per device under a lock.
+// device at once, then its SMs, measured once per device under a lock.
 template <int kWarps>
 cudaError_t max_clusters(const int** out) {
-  static int active[kMaxDevices][5];
+  static int active[kMaxDevices][6];
   static std::atomic<bool> configured[kMaxDevices];
   static std::mutex mu;
   int dev = 0;
@@ -571,6 +570,8 @@ cudaError_t max_clusters(const int** out) {
         }
         active[dev][i] = n;
       }
+      e = cudaDeviceGetAttribute(&active[dev][5], cudaDevAttrMultiProcessorCount, dev);
+      if (e != cudaSuccess) return e;
       configured[dev].store(true, std::memory_order_release);
     }
   }
@@ -584,9 +585,12 @@ cudaError_t launch(const AttnArgs& a, int nc, unsigned* err, cudaStream_t stream
                     dim3(kWarps * 32), sizeof(Smem<kWarps>), stream, (unsigned)nc, a, err);
 }
 
-// Cluster size for kWarps warps a CTA, and the time it is reckoned to take in
-// units of a warp's chunk: the CTAs' waves, each as long as a warp's chunks
-// and a fixed part (prologue, merge).
+// Cluster size for kWarps warps a CTA, and the time the call then takes by this
+// reckoning, in units of 0.05 us.  Measured at 1 to 512 tokens (250k cells, 129
+// chunks, every size and both warp counts): 6 us for launch, prologue and
+// merge, and for each chunk that a warp takes 0.9 us with 4 warps on the SM, 1.3
+// with 8 and 2.3 with 16 (where the SM's throughput decides).  16 tokens: 17 us
+// with as many warps as fit, 12.6 us with half of them and twice the chunks.
 template <int kWarps>
 cudaError_t plan(int64_t clusters, int chunks, int* nc, int64_t* cost) {
   const int* active = nullptr;
@@ -594,11 +598,20 @@ cudaError_t plan(int64_t clusters, int chunks, int* nc, int64_t* cost) {
   if (e != cudaSuccess) return e;
   *nc = 1;
   *cost = -1;
+  const int64_t sms = active[5], slots = active[4] > sms ? active[4] / sms : 1;   // CTAs that share an SM
   for (int i = 0; i < 5; ++i) {
     const int c = 16 >> i;
     if (active[i] <= 0 || (c > 1 && (c - 1) * kWarps >= chunks)) continue;
-    const int64_t waves = ceil_div(clusters, (int64_t)active[i]);
-    const int64_t w = waves * (kFixed + ceil_div((int64_t)chunks, (int64_t)c * kWarps));
+    const int64_t per_sm = ceil_div(clusters * c, sms), steps = ceil_div((int64_t)chunks, (int64_t)c * kWarps);
+    auto chunk = [](int64_t ctas) -> int64_t {   // with so many CTAs on the SM
+      const int64_t t = 5 * ctas * kWarps / 2 + 6;
+      return t > 18 ? t : 18;
+    };
+    // past what fits: single CTAs follow one another on an SM, clusters come in waves
+    int64_t w;
+    if (clusters <= active[i]) w = 120 + steps * chunk(per_sm < slots ? per_sm : slots);
+    else if (c > 1) w = ceil_div(clusters, (int64_t)active[i]) * (120 + steps * chunk(slots));
+    else w = 120 * ceil_div(per_sm, slots) + steps * (per_sm / slots * chunk(slots) + (per_sm % slots ? chunk(per_sm % slots) : 0));
     if (*cost < 0 || w < *cost) {
       *cost = w;
       *nc = c;
