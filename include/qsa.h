@@ -308,9 +308,10 @@ qsa_status qsa_index_topk_noalloc(const qsa_config* cfg, int32_t n_tokens,
  * share an SM; the result is the same within the stated tolerance.
  * For q4_0 K/V the codes are multiplied as integers (exactly) and only the
  * scales' products are rounded, in fp32 (probabilities in two fp16 parts): no
- * K, V or probability is rounded to fp16, and the output is within 2e-5
- * max-relative of the exact result.  An infinite or NaN scale among the
- * attended cells gives NaN.
+ * K, V or probability is rounded to fp16, and the output is as close to the
+ * exact result as fp32 arithmetic on the decoded rows (2e-7 of the output's norm
+ * for N(0,1) rows).  An infinite or NaN scale of an attended K block gives NaN,
+ * one of a V block NaN in that block's dims.
  * count[t] == 0 gives zeros.  A cell outside [0, n_cells) is masked and
  * flagged.  The call needs no workspace (qsa_sparse_attn_workspace_size
  * returns 0; `workspace` may be NULL). */
@@ -516,7 +517,7 @@ qsa_status qsa_seq_fork(const qsa_config* cfg, int32_t n_fork, const int32_t* sr
  * carried out by qsa_cells_copy with n_pairs = counts + 3 on every layer before
  * the cells are used (sources and destinations are disjoint); the table and
  * cell_map name the new places, free_cells the cells from n_held on.  cell_map,
- * move_src and move_dst are then required.  Entries of the lists past their
+ * move_src and move_dst are then required (where they have any entries).  Entries of the lists past their
  * counts are left as they were.
  * Indices out of range are skipped and flagged.  workspace:
  * qsa_cache_sweep_workspace_size bytes, 256-byte aligned, any contents. */

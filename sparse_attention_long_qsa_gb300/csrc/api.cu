@@ -574,7 +574,7 @@ qsa_status qsa_cache_sweep(const qsa_config* cfg, uint32_t flags, const int32_t*
   const bool compact = (flags & QSA_SWEEP_COMPACT) != 0u;
   if (!seq_len || !seq_blk_off || !seq_blk_slots || n_seq == 0 || !blk_cells || !blk_cells_out || !counts)
     return QSA_ERR_INVALID_ARG;
-  if (compact && (!cell_map || !move_src || !move_dst)) return QSA_ERR_INVALID_ARG;
+  if (compact && ((n_cells > 0 && !cell_map) || (n_cells > 1 && (!move_src || !move_dst)))) return QSA_ERR_INVALID_ARG;
   if (!aligned(seq_blk_off, 8)) return QSA_ERR_INVALID_ARG;
   if (workspace == nullptr || !aligned(workspace, 256) || ws_bytes < sweep_workspace_bytes(n_cells, n_slots))
     return QSA_ERR_WORKSPACE;

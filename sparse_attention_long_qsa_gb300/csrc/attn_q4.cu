@@ -326,10 +326,14 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
     // the largest scale of V sets the weights' exponent: d_max * 2^wexp lies in
     // [2^-2, 2^-1) (below, for subnormal scales) when it is set, and stays below 1
     const uint32_t dm = bits(__hmax2(__habs2(dv[0]), __habs2(dv[1])));
-    const uint32_t db = __reduce_max_sync(kFull, max(dm >> 16, dm & 0xffffu));
+    uint32_t db = __reduce_max_sync(kFull, max(dm >> 16, dm & 0xffffu));
     int nexp = wexp;
+    // (an infinite scale spoils its own block's dims, not the others' weights)
+    if (db >= 0x7c00u)
+      db = __reduce_max_sync(kFull, max((dm >> 16) >= 0x7c00u ? 0u : dm >> 16,
+                                        (dm & 0xffffu) >= 0x7c00u ? 0u : dm & 0xffffu));
     if (db > dlim) {
-      nexp = 13 - (int)(db >> 10);   // -18 .. 13
+      nexp = 13 - (int)(db >> 10);   // -17 .. 13
       dlim = ((uint32_t)(15 - nexp) << 10) - 1u;
       up = pow2h(nexp);
     }

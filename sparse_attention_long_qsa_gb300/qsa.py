@@ -453,11 +453,11 @@ def qk_norm_rope(cfg, rope: Rope, pos, q_in, k_in, q_norm_w, k_norm_w, q, k_new,
                                  torch, dev, "q_idx_in")
     at, iat = None, None
     if qp or kp:
-        if pos.numel() != rope.n_axes * T:
+        if pos is None or pos.numel() != rope.n_axes * T:
             raise ValueError(f"pos must hold {rope.n_axes} x {T} positions")
         at = _at(pos, i32, dev, "pos", True)
     if ip:
-        if idx_pos.numel() != T:
+        if idx_pos is None or idx_pos.numel() != T:
             raise ValueError(f"idx_pos must hold {T} positions")
         iat = _at(idx_pos, i32, dev, "idx_pos", True)
     st = lib().qsa_qk_norm_rope(ctypes.byref(cfg), ctypes.byref(rope), T, elem, at, qp, qs, kp, ks, qw, kw, qo, ko, iat,

@@ -286,6 +286,48 @@ def test_sweep_flags_bad_indices():
         assert st == -6 and flags == (1 | 2 | 4)
 
 
+def test_sweep_of_one_cell_and_of_a_cache_at_the_cluster_limit():
+    for n_cells in (1, 2, 65_536, 65_537):
+        off = np.array([0, n_cells], np.int64)
+        lists = np.arange(n_cells)[::-1].copy()
+        table = np.random.default_rng(n_cells).permutation(n_cells).reshape(n_cells, 1).astype(np.int32)
+        cfg = qsa.config(compress_ratio=1, top_k=512)
+        for keep in (0, 1, n_cells // 2, n_cells):
+            for compact in (False, True):
+                _check_sweep(cfg, [keep], off, lists, table, n_cells, compact)
+
+
+def test_sweep_captured_and_replayed_on_a_used_workspace():
+    """One workspace, dirty from a call of other sizes, shared by two captured
+    sweeps replayed in turn."""
+    rng = np.random.default_rng(14)
+    cfg = qsa.config()
+    ws = torch.full((qsa.cache_sweep_workspace_size(cfg, 200_000, 60_000),), 0xEE, dtype=torch.uint8, device="cuda")
+    runs = []
+    for lens, keep in (([5000, 90_000], [0, 70_000]), ([3000, 40], [2999, 0])):
+        cap = [-(-x // 4) + 1 for x in lens]
+        off, lists, table, _, _, _, n_cells = _tables(rng, lens, cap, 4, 3, 20)
+        want = _sweep_ref(keep, off, lists, table, n_cells, True)
+        bufs = dict(cell_map=_i32(np.zeros(n_cells)), move_src=_i32(np.zeros(n_cells // 2)),
+                    move_dst=_i32(np.zeros(n_cells // 2)))
+        out, counts = _i32(np.zeros(table.shape)), _i32(np.zeros(4))
+        args = (_i32(keep), torch.from_numpy(off).cuda(), _i32(lists), _i32(table), out, n_cells, counts, ws)
+        qsa.cache_sweep(cfg, *args, compact=True, **bufs)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            qsa.cache_sweep(cfg, *args, compact=True, **bufs)
+        runs.append((g, args, bufs, want, out, counts))
+    for _ in range(2):
+        for g, _, bufs, want, out, counts in runs:
+            out.fill_(5), counts.fill_(5), bufs["cell_map"].fill_(5)
+            g.replay()
+            torch.cuda.synchronize()
+            np.testing.assert_array_equal(to_np(out), want[0])
+            np.testing.assert_array_equal(to_np(counts), want[1])
+            np.testing.assert_array_equal(to_np(bufs["cell_map"]), want[2])
+
+
 def test_sweep_large_cache():
     """Many tiles of cells; compaction of a random half, checked as sets."""
     rng = np.random.default_rng(12)

@@ -182,6 +182,24 @@ def test_infinities_and_nan_outside_the_list_do_not_reach_it():
     assert np.all(np.isnan(C.run([np.arange(495, 510)], q[:1])))
 
 
+def test_an_infinite_value_scale_spoils_its_own_dims_only():
+    C = _Case(n=1000, seed=43)
+    nq = C.n * 2 * 128
+    d = C.vc[nq:].view(np.float16).reshape(C.n, 2, 8)
+    keep = d[[100, 200], 0, [3, 5]].copy()
+    q = _q(1, 16, 44)
+    lists = [np.arange(900)]
+    ref = C.ref(lists, q)
+    d[100, 0, 3], d[200, 0, 5] = np.inf, np.nan
+    C.v = torch.from_numpy(C.vc).cuda()
+    out = C.run(lists, q)
+    assert np.all(np.isnan(out[0, :8, 96:128])) and np.all(np.isnan(out[0, :8, 160:192]))
+    assert np.all(np.isfinite(np.delete(out[0, :8], np.r_[96:128, 160:192], axis=1))) and np.all(np.isfinite(out[0, 8:]))
+    d[[100, 200], 0, [3, 5]] = keep
+    out[np.isnan(out)] = ref[np.isnan(out)]
+    assert max_rel(out, ref) <= TOL
+
+
 def test_append_and_read_match_the_oracle_bit_for_bit():
     for kw in (dict(n_seq=1, prompt_len=301, n_steps=3), dict(n_seq=3, prompt_len=[101, 202, 303], n_steps=2,
                tokens_per_step=5, shuffled=True), dict(n_seq=1, prompt_len=50, n_steps=1, tokens_per_step=96)):

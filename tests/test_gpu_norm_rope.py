@@ -148,3 +148,18 @@ def test_pinned_inputs_and_outputs():
     qsa.qk_norm_rope(cfg, rope, pin(pos), pin(q), None, w[0], None, po, None)
     torch.cuda.synchronize()
     assert torch.equal(po, qo.cpu())
+
+
+def test_binding_checks_positions():
+    q, k, qi, w, (qo, ko, io) = _make(3, torch.float16)
+    cfg, rope = qsa.config(), qsa.rope_config((64, 64))
+    pos = torch.zeros(3, dtype=torch.int32, device="cuda")
+    for bad in (None, pos):                       # two axes want six positions
+        with pytest.raises(ValueError, match="pos must hold"):
+            qsa.qk_norm_rope(cfg, rope, bad, q, None, w[0], None, qo, None)
+    with pytest.raises(ValueError, match="idx_pos must hold"):
+        qsa.qk_norm_rope(cfg, rope, None, None, None, None, None, None, None, qi, None, w[2], io)
+    with pytest.raises(TypeError):                # one element type for all inputs
+        qsa.qk_norm_rope(cfg, rope, pos.repeat(2), q, k.float(), w[0], w[1], qo, ko)
+    with pytest.raises(ValueError, match="contiguous"):
+        qsa.qk_norm_rope(cfg, rope, pos.repeat(2), q.transpose(0, 1).contiguous().transpose(0, 1), None, w[0], None, qo, None)
