@@ -154,7 +154,7 @@ __device__ __forceinline__ __half2 pow2h(int k) {
 }
 
 template <int kWarps>
-__global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
+__global__ void __launch_bounds__(kWarps * 32, kWarps == 4 ? 4 : 1)
 k_attn_q4(const AttnArgs a, unsigned* err) {
   extern __shared__ unsigned char smem_raw[];
   Smem<kWarps>& sm = *reinterpret_cast<Smem<kWarps>*>(smem_raw);
@@ -605,7 +605,7 @@ cudaError_t plan(int64_t clusters, int chunks, int* nc, int64_t* cost) {
   const int64_t sms = active[5], slots = active[4] > sms ? active[4] / sms : 1;   // CTAs that share an SM
   for (int i = 0; i < 5; ++i) {
     const int c = 16 >> i;
-    if (active[i] <= 0 || (c > 1 && (c - 1) * kWarps >= chunks)) continue;
+    if (active[i] <= 0 || c > (chunks > 1 ? chunks : 1)) continue;   // every CTA has a chunk
     const int64_t per_sm = ceil_div(clusters * c, sms), steps = ceil_div((int64_t)chunks, (int64_t)c * kWarps);
     auto chunk = [](int64_t ctas) -> int64_t {   // with so many CTAs on the SM
       const int64_t t = 5 * ctas * kWarps / 2 + 6;
@@ -616,7 +616,7 @@ cudaError_t plan(int64_t clusters, int chunks, int* nc, int64_t* cost) {
     if (clusters <= active[i]) w = 120 + steps * chunk(per_sm < slots ? per_sm : slots);
     else if (c > 1) w = ceil_div(clusters, (int64_t)active[i]) * (120 + steps * chunk(slots));
     else w = 120 * ceil_div(per_sm, slots) + steps * (per_sm / slots * chunk(slots) + (per_sm % slots ? chunk(per_sm % slots) : 0));
-    if (*cost < 0 || w < *cost) {
+    if (*cost < 0 || w <= *cost) {   // the smaller of two equals
       *cost = w;
       *nc = c;
     }
@@ -629,12 +629,12 @@ cudaError_t plan(int64_t clusters, int chunks, int* nc, int64_t* cost) {
 cudaError_t launch_attn_q4(const AttnArgs& a, unsigned* err, cudaStream_t stream) {
   const int chunks = (int)ceil_div(a.cells_pitch, kChunk);
   const int64_t clusters = (int64_t)a.n_tokens * a.n_kv_heads;
-  int nc4 = 1, nc8 = 1;
-  int64_t cost4 = 0, cost8 = 0;
+  int nc4 = 1, nc9 = 1;
+  int64_t cost4 = 0, cost9 = 0;
   cudaError_t e = plan<4>(clusters, chunks, &nc4, &cost4);
-  if (e == cudaSuccess) e = plan<8>(clusters, chunks, &nc8, &cost8);
+  if (e == cudaSuccess) e = plan<9>(clusters, chunks, &nc9, &cost9);
   if (e != cudaSuccess) return e;
-  if (cost8 < cost4) return launch<8>(a, nc8, err, stream);
+  if (cost9 < cost4) return launch<9>(a, nc9, err, stream);
   return launch<4>(a, nc4, err, stream);
 }
 
