@@ -16,7 +16,7 @@
 //
 // One warp per (token, row): rows 0..G-1 are the K heads, G..2G-1 the V
 // heads, 2G the indexer key together with the table entry; that warp of each
-// block's first new token then re-pools the block.  An extra first CTA builds
+// block's first new token then re-pools the block.  An extra CTA builds
 // the dirty list: the distinct slots, ascending, padded with -1.
 // Everything is read and encoded before the grid-dependency wait (the new
 // rows are inputs, not outputs of the preceding kernel); only the stores wait.
@@ -33,12 +33,13 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kAppThreads = 256;
 constexpr int kAppOffCache = 256;   // sequences whose block offsets a CTA preloads
 constexpr int kAppWarps = kAppThreads / 32;
+constexpr int kAppFew = 64;
 
 struct AppendArgs {
   int n_new;
   int G;
   int r;
-  int kv_type;
+  int kv_q8;
   const int32_t* tok_seq;
   const int32_t* tok_pos;
   const int32_t* cell;
@@ -98,6 +99,12 @@ __device__ __forceinline__ int token_slot(const AppendArgs& a, NewTok k, const i
   return slot;
 }
 
+// kMany: calls of more than kAppFew tokens, whose dirty list is the launch's
+// longest work: its CTA comes first and sorts in registers (1,024 tokens: 23 us
+// with the loop through shared memory, 9 us).  The few-token kernel is without
+// that code, and each cache type without the others', as a decode step runs it
+// from a cold instruction cache (one kernel for all cost the step 0.2 us).
+template <bool kQ4, bool kMany>
 __global__ void __launch_bounds__(kAppThreads)
 k_append(const AppendArgs a, const Turns turns, unsigned* err) {
   QSA_TS_SCOPE_LAST(append, 1);
@@ -108,17 +115,17 @@ k_append(const AppendArgs a, const Turns turns, unsigned* err) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kPer = kAppendMaxTokens / kAppThreads;   // tokens per thread in the dirty-list CTA
   static_assert(kPer == 4, "the dirty list sorts four registers a thread");
-  const bool dirty_cta = blockIdx.x == 0;   // first: its sort is the launch's longest work
+  const bool dirty_cta = blockIdx.x == (kMany ? 0 : gridDim.x - 1);
   // this thread's tokens' ids, loaded together with the sequences' block
   // offsets (one dependent load less on the way to the slots)
   const int rows = 2 * a.G + 1;
-  const int64_t w = ((int64_t)blockIdx.x - 1) * kAppWarps + warp;
+  const int64_t w = ((int64_t)blockIdx.x - (kMany ? 1 : 0)) * kAppWarps + warp;
   const bool active = !dirty_cta && w < (int64_t)a.n_new * rows;
   const int t = active ? (int)(w / rows) : 0;
   NewTok mine[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
-    const int u = dirty_cta ? warp * (32 * kPer) + 32 * k + lane : t;
+    const int u = !dirty_cta ? t : kMany ? warp * (32 * kPer) + 32 * k + lane : tid + k * kAppThreads;
     mine[k] = ((dirty_cta && u < a.n_new) || (!dirty_cta && k == 0 && active)) ? load_tok(a, u) : NewTok{-1, -1, -1};
   }
   __shared__ int64_t s_off_buf[kAppOffCache + 1];
@@ -139,56 +146,87 @@ k_append(const AppendArgs a, const Turns turns, unsigned* err) {
     // ---- the dirty list (n_new <= kAppendMaxTokens): every token's slot
     // (INT_MAX for an invalid token and past n_new), a bitonic sort of the
     // next power of two >= n_new, then the first of every run of equal slots
-    // compacted in order: the distinct slots, ascending.  Thread (warp, lane)
-    // holds elements 128 warp + 32 k + lane, k < 4, in registers, so that only
-    // the steps that cross warps (6 of the 55 for 1,024) go through shared
-    // memory and a barrier.
+    // compacted in order: the distinct slots, ascending.  With many tokens
+    // thread (warp, lane) holds elements 128 warp + 32 k + lane, k < 4, in
+    // registers, so that only the steps that cross warps (6 of the 55 for
+    // 1,024) go through shared memory and a barrier.
     __shared__ int s_slot[kAppendMaxTokens];
     __shared__ unsigned s_warp[kAppWarps];
     int n2 = 2;
     while (n2 < a.n_new) n2 <<= 1;
-    int v[kPer];
-    const int e0 = warp * (32 * kPer) + lane;
+    if constexpr (!kMany) {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      int ib = 0;
-      const int x = e0 + 32 * k < a.n_new ? token_slot(a, mine[k], s_off, &ib, err, false) : -1;
-      v[k] = x < 0 ? INT_MAX : x;
-    }
-    auto keep = [](int x, int y, bool smaller) { return smaller ? min(x, y) : max(x, y); };
-    for (int k = 2; k <= n2; k <<= 1) {
-      for (int j = k >> 1; j > 0; j >>= 1) {
-        if (j >= 32 * kPer) {
-#pragma unroll
-          for (int q = 0; q < kPer; ++q) s_slot[e0 + 32 * q] = v[q];
-          __syncthreads();
-#pragma unroll
-          for (int q = 0; q < kPer; ++q) {
-            const int e = e0 + 32 * q;
-            v[q] = keep(v[q], s_slot[e ^ j], ((e & j) == 0) == ((e & k) == 0));
+      for (int k = 0; k < kPer; ++k) {
+        const int u = tid + k * kAppThreads;
+        if (u >= n2) break;
+        int sl = INT_MAX;
+        if (u < a.n_new) {
+          int ib = 0;
+          const int x = token_slot(a, mine[k], s_off, &ib, err, false);
+          sl = x < 0 ? INT_MAX : x;
+        }
+        s_slot[u] = sl;
+      }
+      __syncthreads();
+      for (int k = 2; k <= n2; k <<= 1) {
+        for (int j = k >> 1; j > 0; j >>= 1) {
+          for (int i = tid; i < n2; i += kAppThreads) {
+            const int l = i ^ j;
+            if (l > i) {
+              const int x = s_slot[i], y = s_slot[l];
+              if ((x > y) == ((i & k) == 0)) {
+                s_slot[i] = y;
+                s_slot[l] = x;
+              }
+            }
           }
           __syncthreads();
-        } else if (j >= 32) {
-          int y[kPer];
+        }
+      }
+    } else {
+      int v[kPer];
+      const int e0 = warp * (32 * kPer) + lane;
 #pragma unroll
-          for (int q = 0; q < kPer; ++q) y[q] = j == 32 ? v[q ^ 1] : v[q ^ 2];
+      for (int k = 0; k < kPer; ++k) {
+        int ib = 0;
+        const int x = e0 + 32 * k < a.n_new ? token_slot(a, mine[k], s_off, &ib, err, false) : -1;
+        v[k] = x < 0 ? INT_MAX : x;
+      }
+      auto keep = [](int x, int y, bool smaller) { return smaller ? min(x, y) : max(x, y); };
+      for (int k = 2; k <= n2; k <<= 1) {
+        for (int j = k >> 1; j > 0; j >>= 1) {
+          if (j >= 32 * kPer) {
 #pragma unroll
-          for (int q = 0; q < kPer; ++q) {
-            const int e = e0 + 32 * q;
-            v[q] = keep(v[q], y[q], ((e & j) == 0) == ((e & k) == 0));
-          }
-        } else {
+            for (int q = 0; q < kPer; ++q) s_slot[e0 + 32 * q] = v[q];
+            __syncthreads();
 #pragma unroll
-          for (int q = 0; q < kPer; ++q) {
-            const int e = e0 + 32 * q;
-            v[q] = keep(v[q], __shfl_xor_sync(kFull, v[q], j), ((e & j) == 0) == ((e & k) == 0));
+            for (int q = 0; q < kPer; ++q) {
+              const int e = e0 + 32 * q;
+              v[q] = keep(v[q], s_slot[e ^ j], ((e & j) == 0) == ((e & k) == 0));
+            }
+            __syncthreads();
+          } else if (j >= 32) {
+            int y[kPer];
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) y[q] = j == 32 ? v[q ^ 1] : v[q ^ 2];
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) {
+              const int e = e0 + 32 * q;
+              v[q] = keep(v[q], y[q], ((e & j) == 0) == ((e & k) == 0));
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) {
+              const int e = e0 + 32 * q;
+              v[q] = keep(v[q], __shfl_xor_sync(kFull, v[q], j), ((e & j) == 0) == ((e & k) == 0));
+            }
           }
         }
       }
-    }
 #pragma unroll
-    for (int q = 0; q < kPer; ++q) s_slot[e0 + 32 * q] = v[q];
-    __syncthreads();
+      for (int q = 0; q < kPer; ++q) s_slot[e0 + 32 * q] = v[q];
+      __syncthreads();
+    }
     // thread tid takes the contiguous run [tid * per, tid * per + per)
     const int per = (n2 + kAppThreads - 1) / kAppThreads;   // <= 4
     const int i0 = min(n2, tid * per), i1 = min(n2, i0 + per);
@@ -233,7 +271,7 @@ k_append(const AppendArgs a, const Turns turns, unsigned* err) {
     const __half* src = (kind < a.G ? a.k_new : a.v_new) + ((int64_t)t * a.G + g) * kHeadDim;
     unsigned char* cache = kind < a.G ? a.k_cache : a.v_cache;
     const uint4 raw = ok ? __ldg(reinterpret_cast<const uint4*>(src) + lane) : make_uint4(0, 0, 0, 0);
-    if (a.kv_type == QSA_KV_F16) {
+    if (!kQ4 && !a.kv_q8) {
       grid_dep_wait();
       if (ok) reinterpret_cast<uint4*>(cache + (c * a.G + g) * kHeadDim * 2)[lane] = raw;
       return;
@@ -247,7 +285,7 @@ k_append(const AppendArgs a, const Turns turns, unsigned* err) {
       x[2 * i] = f.x;
       x[2 * i + 1] = f.y;
     }
-    if (a.kv_type == QSA_KV_Q4_0) {
+    if constexpr (kQ4) {
       float m = 0.f;
       bool nan = false;
 #pragma unroll
@@ -397,7 +435,7 @@ cudaError_t launch_append(const qsa_config& cfg, int n_new, const int32_t* tok_s
   a.n_new = n_new;
   a.G = cfg.n_kv_heads;
   a.r = cfg.compress_ratio;
-  a.kv_type = cfg.kv_type;
+  a.kv_q8 = cfg.kv_type == QSA_KV_Q8_0;
   a.tok_seq = tok_seq;
   a.tok_pos = tok_pos;
   a.cell = cell;
@@ -424,7 +462,10 @@ cudaError_t launch_append(const qsa_config& cfg, int n_new, const int32_t* tok_s
   const int64_t warps = (int64_t)n_new * (2 * cfg.n_kv_heads + 1);
   const unsigned blocks = (unsigned)ceil_div(warps, kAppWarps) + 1;   // + the dirty-list CTA
   prof_before(kKAppend, stream);
-  cudaError_t e = launch_pdl(k_append, dim3(blocks), dim3(kAppThreads), 0, stream, 1, a, turns, err);
+  const bool q4 = cfg.kv_type == QSA_KV_Q4_0, many = n_new > kAppFew;
+  void (*const kernel)(AppendArgs, Turns, unsigned*) = q4 ? (many ? k_append<true, true> : k_append<true, false>)
+                                                          : (many ? k_append<false, true> : k_append<false, false>);
+  cudaError_t e = launch_pdl(kernel, dim3(blocks), dim3(kAppThreads), 0, stream, 1, a, turns, err);
   prof_after(kKAppend, stream);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
