@@ -206,9 +206,9 @@ constexpr int kSweepThreads = 1024, kSweepWarps = kSweepThreads / 32;
 constexpr int kTile = 4 * kSweepThreads;        // a thread's four flags of a tile
 constexpr int kSweepCluster = 16;
 // A cluster sweeps caches of up to so many cells, list entries and slots: the
-// device time is then that of the five kernels (9 us at 1,000 cells, 17 and 16
-// us at 50,000) and the host makes one launch instead of five (some 8 us); at
-// 100,000 cells the cluster's 16 SMs take 24 us, the five kernels 16 us.
+// host makes one launch instead of five (some 8 us less) and the device time is
+// lower, too (us, cluster / five kernels: 8.3 / 9.3 at 1,000 cells, 12.5 / 15.9
+// at 50,000, 14.5 / 16 at 65,536; beyond, 17.5 / 16 at 80,000).
 constexpr int64_t kSweepClusterCells = 65536;
 constexpr int kSweepSeqs = 256;                 // sequences whose lists a CTA keeps in shared memory
 
@@ -224,7 +224,13 @@ __device__ __forceinline__ void sweep_clear(const SweepArgs& a, int64_t i0, int6
   for (int64_t i = i0; i < all; i += n) p[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-__device__ __forceinline__ void sweep_mark(const SweepArgs& a, int64_t i0, int64_t n, SweepSmem& sm, unsigned* err) {
+// The sequences' lists and lengths, from shared memory where they fit.
+struct SweepSeqs {
+  const int64_t* off;
+  const int32_t* len;
+  int64_t lists, end;   // list entries; the loop's end (every sequence is looked at, too)
+};
+__device__ __forceinline__ SweepSeqs sweep_seqs(const SweepArgs& a, SweepSmem& sm) {
   const bool near = a.n_seq <= kSweepSeqs;
   if (near) {
     for (int i = threadIdx.x; i <= a.n_seq; i += kSweepThreads) {
@@ -233,47 +239,67 @@ __device__ __forceinline__ void sweep_mark(const SweepArgs& a, int64_t i0, int64
     }
     __syncthreads();
   }
-  const int64_t* off = near ? sm.off : a.seq_blk_off;
-  const int32_t* len = near ? sm.len : a.seq_len;
-  const int64_t lists = off[a.n_seq] < a.n_list ? off[a.n_seq] : a.n_list;
-  const int64_t end = lists > a.n_seq ? lists : a.n_seq;
-  for (int64_t e = i0; e < end; e += n) {
-    if (e < a.n_seq) {   // a length that its list cannot hold
-      if (len[e] > 0 && (len[e] + (int64_t)a.r - 1) / a.r > off[e + 1] - off[e]) atomicOr(err, kErrBlockList);
-    }
-    if (e >= lists || e < off[0]) continue;
-    const int slot = a.seq_blk_slots[e];
-    int lo = 0, hi = a.n_seq;                   // the last sequence whose list starts at or before e
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (off[mid] <= e) lo = mid;
-      else hi = mid;
-    }
-    const int64_t held = len[lo] - (e - off[lo]) * a.r;
-    if (held <= 0) continue;
-    if (slot < 0 || slot >= a.n_slots) {
-      atomicOr(err, kErrSlot);
-      continue;
-    }
-    a.slot_flags[slot] = 1;
-    const int32_t* row = a.blk_cells + (int64_t)slot * a.r;
-    int c[8];   // compress_ratio is at most 8
-    if (a.r == 4 && a.rows16) {
-      const int4 v = *reinterpret_cast<const int4*>(row);
-      c[0] = v.x, c[1] = v.y, c[2] = v.z, c[3] = v.w;
-#pragma unroll
-      for (int i = 4; i < 8; ++i) c[i] = -1;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) c[i] = i < a.r ? row[i] : -1;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (i >= held || c[i] < 0) continue;
-      if (c[i] >= a.n_cells) atomicOr(err, kErrCell);
-      else a.cell_flags[c[i]] = 1;
-    }
+  SweepSeqs q;
+  q.off = near ? sm.off : a.seq_blk_off;
+  q.len = near ? sm.len : a.seq_len;
+  q.lists = q.off[a.n_seq] < a.n_list ? q.off[a.n_seq] : a.n_list;
+  q.end = q.lists > a.n_seq ? q.lists : a.n_seq;
+  return q;
+}
+
+// What list entry e marks: its slot (-1: nothing) and the first `held` cells of
+// the slot's row.  `slot` is the entry's, loaded by the caller.
+struct SweepEntry {
+  int slot;
+  int64_t held;
+  int c[8];   // compress_ratio is at most 8
+};
+__device__ __forceinline__ SweepEntry sweep_entry(const SweepArgs& a, const SweepSeqs& q, int64_t e, int slot, unsigned* err) {
+  SweepEntry r;
+  r.slot = -1;
+  r.held = 0;
+  if (e < a.n_seq) {   // a length that its list cannot hold
+    if (q.len[e] > 0 && (q.len[e] + (int64_t)a.r - 1) / a.r > q.off[e + 1] - q.off[e]) atomicOr(err, kErrBlockList);
   }
+  if (e >= q.lists || e < q.off[0]) return r;
+  int lo = 0, hi = a.n_seq;                   // the last sequence whose list starts at or before e
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (q.off[mid] <= e) lo = mid;
+    else hi = mid;
+  }
+  r.held = q.len[lo] - (e - q.off[lo]) * a.r;
+  if (r.held <= 0) return r;
+  if (slot < 0 || slot >= a.n_slots) {
+    atomicOr(err, kErrSlot);
+    return r;
+  }
+  r.slot = slot;
+  const int32_t* row = a.blk_cells + (int64_t)slot * a.r;
+  if (a.r == 4 && a.rows16) {
+    const int4 v = *reinterpret_cast<const int4*>(row);
+    r.c[0] = v.x, r.c[1] = v.y, r.c[2] = v.z, r.c[3] = v.w;
+#pragma unroll
+    for (int i = 4; i < 8; ++i) r.c[i] = -1;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.c[i] = i < a.r ? row[i] : -1;
+  }
+  return r;
+}
+__device__ __forceinline__ void sweep_flag(const SweepArgs& a, const SweepEntry& r, unsigned* err) {
+  if (r.slot < 0) return;
+  a.slot_flags[r.slot] = 1;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (i >= r.held || r.c[i] < 0) continue;
+    if (r.c[i] >= a.n_cells) atomicOr(err, kErrCell);
+    else a.cell_flags[r.c[i]] = 1;
+  }
+}
+__device__ __forceinline__ void sweep_mark(const SweepArgs& a, const SweepSeqs& q, int64_t i0, int64_t n, unsigned* err) {
+  for (int64_t e = i0; e < q.end; e += n)
+    sweep_flag(a, sweep_entry(a, q, e, e < q.lists ? a.seq_blk_slots[e] : -1, err), err);
 }
 
 // This thread's four flags of a tile, a byte each.
@@ -294,25 +320,21 @@ __device__ __forceinline__ uint2 block_sums(unsigned x, unsigned y, SweepSmem& s
 }
 
 // Tiles [0, cell_tiles) are cells', the others slots' (whose flags follow).
-__device__ __forceinline__ void sweep_count(const SweepArgs& a, int64_t t0, int64_t n, SweepSmem& sm) {
-  for (int64_t t = t0; t < a.cell_tiles + a.slot_tiles; t += n) {
-    const uint2 sum = block_sums(__popc(sweep_flags(a, t)), 0u, sm);
-    if (threadIdx.x == 0) a.sums[t] = sum.x;
-  }
-}
-
-// In a compaction a held cell at or past n_held is written to cell_map as
-// -2 - (its move's number); sweep_table resolves it.
-__device__ __forceinline__ void sweep_apply(const SweepArgs& a, int64_t t0, int64_t n, SweepSmem& sm) {
+// Ranks of tile t, whose flags are w; all_sums: every tile's sum, in global
+// memory or (kNear) shared.  In a compaction a held cell at or past n_held is
+// written to cell_map as -2 - (its move's number); sweep_table resolves it.
+template <bool kNear>
+__device__ __forceinline__ void sweep_apply(const SweepArgs& a, int64_t t, unsigned w, const unsigned* all_sums,
+                                            SweepSmem& sm) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int64_t t = t0; t < a.cell_tiles + a.slot_tiles; t += n) {
+  auto sum_of = [&](const unsigned* p) { return kNear ? *p : __ldcg(p); };
+  {
     const bool cells = t < a.cell_tiles;
     const int64_t tile = cells ? t : t - a.cell_tiles, tiles = cells ? a.cell_tiles : a.slot_tiles;
-    const unsigned* sums = a.sums + (cells ? 0 : a.cell_tiles);
-    const unsigned w = sweep_flags(a, t);
+    const unsigned* sums = all_sums + (cells ? 0 : a.cell_tiles);
     unsigned before = 0, all = 0;
     for (int64_t k = tid; k < tiles; k += kSweepThreads) {
-      const unsigned v = __ldcg(sums + k);
+      const unsigned v = sum_of(sums + k);
       all += v;
       if (k < tile) before += v;
     }
@@ -322,7 +344,7 @@ __device__ __forceinline__ void sweep_apply(const SweepArgs& a, int64_t t0, int6
     unsigned below = 0;
     if (cells && a.compact) {
       const int64_t cut = n_held / kTile;
-      for (int64_t k = tid; k < cut; k += kSweepThreads) below += __ldcg(sums + k);
+      for (int64_t k = tid; k < cut; k += kSweepThreads) below += sum_of(sums + k);
       if (cut < tiles) {
         const unsigned v = sweep_flags(a, cut);
         const int in = (int)(n_held - cut * kTile) - 4 * tid;   // of this thread's four cells
@@ -427,38 +449,70 @@ __global__ void __launch_bounds__(kSweepThreads) k_sweep_mark(const SweepArgs a,
   __shared__ SweepSmem sm;
   grid_dep_wait();
   grid_dep_launch();
-  sweep_mark(a, grid_thread(), grid_threads(), sm, err);
+  sweep_mark(a, sweep_seqs(a, sm), grid_thread(), grid_threads(), err);
 }
 __global__ void __launch_bounds__(kSweepThreads) k_sweep_count(const SweepArgs a) {
   __shared__ SweepSmem sm;
   grid_dep_wait();
   grid_dep_launch();
-  sweep_count(a, blockIdx.x, gridDim.x, sm);
+  const uint2 sum = block_sums(__popc(sweep_flags(a, blockIdx.x)), 0u, sm);
+  if (threadIdx.x == 0) a.sums[blockIdx.x] = sum.x;
 }
 __global__ void __launch_bounds__(kSweepThreads) k_sweep_apply(const SweepArgs a) {
   __shared__ SweepSmem sm;
   grid_dep_wait();
   grid_dep_launch();
-  sweep_apply(a, blockIdx.x, gridDim.x, sm);
+  sweep_apply<false>(a, blockIdx.x, sweep_flags(a, blockIdx.x), a.sums, sm);
 }
 __global__ void __launch_bounds__(kSweepThreads) k_sweep_table(const SweepArgs a) {
   grid_dep_wait();
   sweep_table(a, grid_thread(), grid_threads());
   __threadfence();
 }
-// All of it by one cluster; its barrier orders the phases' global writes.
+// All of it by one cluster; its barrier orders the phases' global writes.  What
+// the first phases read of the inputs is loaded before the flags are clear, a
+// CTA's (at most kNearTiles) tiles stay in registers, and the tiles' sums go
+// straight into every CTA's shared memory.
+constexpr int kNearTiles = (int)(2 * (kSweepClusterCells / kTile) / kSweepCluster);
 __global__ void __launch_bounds__(kSweepThreads) k_sweep_cluster(const SweepArgs a, unsigned* err) {
   __shared__ SweepSmem sm;
+  __shared__ unsigned s_sums[kNearTiles * kSweepCluster];
+  static_assert(kNearTiles * kSweepCluster * (int64_t)kTile >= 2 * kSweepClusterCells, "every tile has a CTA");
   grid_dep_wait();
-  sweep_clear(a, grid_thread(), grid_threads());
+  // warps dealt to the CTAs in turn: a small cache keeps all 16 SMs busy
+  const int64_t n = grid_threads();
+  const int64_t i0 = ((int64_t)(threadIdx.x >> 5) * kSweepCluster + blockIdx.x) * 32 + (threadIdx.x & 31);
+  const int slot0 = i0 < a.n_list ? a.seq_blk_slots[i0] : -1;
+  sweep_clear(a, i0, n);
+  const SweepSeqs q = sweep_seqs(a, sm);
+  SweepEntry first;
+  first.slot = -1;
+  if (i0 < q.end) first = sweep_entry(a, q, i0, slot0, err);
   cluster_sync();
-  sweep_mark(a, grid_thread(), grid_threads(), sm, err);
+  sweep_flag(a, first, err);
+  sweep_mark(a, q, i0 + n, n, err);
   cluster_sync();
-  sweep_count(a, blockIdx.x, gridDim.x, sm);
+  unsigned w[kNearTiles];
+  const int tiles = (int)(a.cell_tiles + a.slot_tiles);
+#pragma unroll
+  for (int k = 0; k < kNearTiles; ++k) {
+    const int t = (int)blockIdx.x + k * kSweepCluster;
+    w[k] = t < tiles ? sweep_flags(a, t) : 0u;
+  }
+#pragma unroll
+  for (int k = 0; k < kNearTiles; ++k) {
+    const int t = (int)blockIdx.x + k * kSweepCluster;
+    const uint2 sum = block_sums(__popc(w[k]), 0u, sm);
+    if (t < tiles && threadIdx.x < kSweepCluster) st_dsmem_u32(dsmem_addr(&s_sums[t], threadIdx.x), sum.x);
+  }
   cluster_sync();
-  sweep_apply(a, blockIdx.x, gridDim.x, sm);
+#pragma unroll
+  for (int k = 0; k < kNearTiles; ++k) {
+    const int t = (int)blockIdx.x + k * kSweepCluster;
+    if (t < tiles) sweep_apply<true>(a, t, w[k], s_sums, sm);
+  }
   cluster_sync();
-  sweep_table(a, grid_thread(), grid_threads());
+  sweep_table(a, i0, n);
   __threadfence();
 }
 

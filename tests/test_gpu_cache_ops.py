@@ -287,7 +287,7 @@ def test_sweep_flags_bad_indices():
 
 
 def test_sweep_of_one_cell_and_of_a_cache_at_the_cluster_limit():
-    for n_cells in (1, 2, 65_536, 65_537):
+    for n_cells in (1, 2, 4_097, 65_536, 65_537):
         off = np.array([0, n_cells], np.int64)
         lists = np.arange(n_cells)[::-1].copy()
         table = np.random.default_rng(n_cells).permutation(n_cells).reshape(n_cells, 1).astype(np.int32)
