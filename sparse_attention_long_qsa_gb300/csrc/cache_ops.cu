@@ -193,22 +193,23 @@ k_seq_fork(const ForkArgs a, unsigned* err) {
 // ---------------------------------------------------------- qsa_cache_sweep
 // Five phases, each a loop over all threads (or, by tiles of 4,096 cells or
 // slots, over all CTAs) of whatever runs it:
-//   clear   a byte of every cell and slot
+//   clear   a bit of every cell and slot
 //   mark    a thread per list entry: the slot it names is held while the
 //           sequence's positions reach its block, and with it the cells of
-//           those positions (plain byte stores; atomics on bits took longer)
+//           those positions
 //   count   held cells and slots of each tile
 //   apply   ranks: free lists, moves, cell_map
 //   table   the block table under the new places
 // A small cache is swept by one cluster with its hardware barrier between the
 // phases, one launch in all; a large one by five kernels over the whole GPU.
 constexpr int kSweepThreads = 1024, kSweepWarps = kSweepThreads / 32;
-constexpr int kTile = 4 * kSweepThreads;        // a thread's four flags of a tile
+constexpr int kTile = 4 * kSweepThreads;        // a thread's four cells or slots of a tile
+constexpr int kTileWords = kTile / 32;
 constexpr int kSweepCluster = 16;
 // A cluster sweeps caches of up to so many cells, list entries and slots: the
-// host makes one launch instead of five (some 8 us less) and the device time is
-// lower, too (us, cluster / five kernels: 8.3 / 9.3 at 1,000 cells, 12.5 / 15.9
-// at 50,000, 14.5 / 16 at 65,536; beyond, 17.5 / 16 at 80,000).
+// host makes one launch instead of five (some 8 us less) and the device takes as
+// long or less (us, cluster / five kernels, compacting: 10.3 / 11.3 at 5,000
+// cells, 14.0 / 15.4 at 50,000, 16.5 / 15.6 at 65,536).
 constexpr int64_t kSweepClusterCells = 65536;
 constexpr int kSweepSeqs = 256;                 // sequences whose lists a CTA keeps in shared memory
 
@@ -219,8 +220,8 @@ struct SweepSmem {
 };
 
 __device__ __forceinline__ void sweep_clear(const SweepArgs& a, int64_t i0, int64_t n) {
-  uint4* p = reinterpret_cast<uint4*>(a.cell_flags);   // the slots' flags follow
-  const int64_t all = (a.cell_tiles + a.slot_tiles) * (kTile / 16);
+  uint4* p = reinterpret_cast<uint4*>(a.cell_bits);   // the slots' bits follow
+  const int64_t all = (a.cell_tiles + a.slot_tiles) * (kTileWords / 4);
   for (int64_t i = i0; i < all; i += n) p[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
@@ -289,12 +290,12 @@ __device__ __forceinline__ SweepEntry sweep_entry(const SweepArgs& a, const Swee
 }
 __device__ __forceinline__ void sweep_flag(const SweepArgs& a, const SweepEntry& r, unsigned* err) {
   if (r.slot < 0) return;
-  a.slot_flags[r.slot] = 1;
+  atomicOr(&a.slot_bits[r.slot >> 5], 1u << (r.slot & 31));
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if (i >= r.held || r.c[i] < 0) continue;
     if (r.c[i] >= a.n_cells) atomicOr(err, kErrCell);
-    else a.cell_flags[r.c[i]] = 1;
+    else atomicOr(&a.cell_bits[r.c[i] >> 5], 1u << (r.c[i] & 31));
   }
 }
 __device__ __forceinline__ void sweep_mark(const SweepArgs& a, const SweepSeqs& q, int64_t i0, int64_t n, unsigned* err) {
@@ -302,9 +303,9 @@ __device__ __forceinline__ void sweep_mark(const SweepArgs& a, const SweepSeqs& 
     sweep_flag(a, sweep_entry(a, q, e, e < q.lists ? a.seq_blk_slots[e] : -1, err), err);
 }
 
-// This thread's four flags of a tile, a byte each.
-__device__ __forceinline__ unsigned sweep_flags(const SweepArgs& a, int64_t tile) {
-  return __ldcg(reinterpret_cast<const unsigned*>(a.cell_flags + tile * kTile) + threadIdx.x);
+// This thread's four bits of a tile.
+__device__ __forceinline__ unsigned sweep_bits(const SweepArgs& a, int64_t tile) {
+  return (__ldcg(a.cell_bits + tile * kTileWords + (threadIdx.x >> 3)) >> (4 * (threadIdx.x & 7))) & 15u;
 }
 
 // Sums of x and of y over the CTA, in every thread.
@@ -319,8 +320,8 @@ __device__ __forceinline__ uint2 block_sums(unsigned x, unsigned y, SweepSmem& s
   return make_uint2(__reduce_add_sync(kFull, sm.tmp[0][lane]), __reduce_add_sync(kFull, sm.tmp[1][lane]));
 }
 
-// Tiles [0, cell_tiles) are cells', the others slots' (whose flags follow).
-// Ranks of tile t, whose flags are w; all_sums: every tile's sum, in global
+// Tiles [0, cell_tiles) are cells', the others slots' (whose bits follow).
+// Ranks of tile t, of which this thread's bits are w; all_sums: every tile's sum, in global
 // memory or (kNear) shared.  In a compaction a held cell at or past n_held is
 // written to cell_map as -2 - (its move's number); sweep_table resolves it.
 template <bool kNear>
@@ -346,9 +347,9 @@ __device__ __forceinline__ void sweep_apply(const SweepArgs& a, int64_t t, unsig
       const int64_t cut = n_held / kTile;
       for (int64_t k = tid; k < cut; k += kSweepThreads) below += sum_of(sums + k);
       if (cut < tiles) {
-        const unsigned v = sweep_flags(a, cut);
+        const unsigned v = sweep_bits(a, cut);
         const int in = (int)(n_held - cut * kTile) - 4 * tid;   // of this thread's four cells
-        if (in > 0) below += __popc(in >= 4 ? v : v & ((1u << (8 * in)) - 1u));
+        if (in > 0) below += __popc(in >= 4 ? v : v & ((1u << in) - 1u));
       }
     }
     // this thread's rank: the tiles before, the warps before, the lanes before
@@ -379,7 +380,7 @@ __device__ __forceinline__ void sweep_apply(const SweepArgs& a, int64_t t, unsig
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t c = c0 + i;
-      const bool held = (w >> (8 * i)) & 1u;
+      const bool held = (w >> i) & 1u;
       map[i] = held ? (int)c : -1;
       if (c >= n_of) continue;
       if (!cells) {
@@ -416,12 +417,12 @@ __device__ __forceinline__ void sweep_table(const SweepArgs& a, int64_t i0, int6
   const int64_t moves = a.compact ? __ldcg(a.counts + 3) : 0;
   auto place = [&](int c) -> int {
     if (c < 0 || c >= a.n_cells) return -1;
-    if (!a.compact) return __ldcg(a.cell_flags + c) ? c : -1;
+    if (!a.compact) return (__ldcg(a.cell_bits + (c >> 5)) >> (c & 31)) & 1u ? c : -1;
     const int v = *reinterpret_cast<volatile const int32_t*>(a.cell_map + c);
     return v < -1 ? __ldcg(a.move_dst + (-2 - v)) : v;
   };
   for (int64_t slot = i0; slot < a.n_slots; slot += n) {
-    const bool held = __ldcg(a.slot_flags + slot) != 0;
+    const bool held = (__ldcg(a.slot_bits + (slot >> 5)) >> (slot & 31)) & 1u;
     const int32_t* row = a.blk_cells + slot * a.r;
     int32_t* out = a.blk_cells_out + slot * a.r;
     if (a.r == 4 && a.rows16) {
@@ -455,14 +456,14 @@ __global__ void __launch_bounds__(kSweepThreads) k_sweep_count(const SweepArgs a
   __shared__ SweepSmem sm;
   grid_dep_wait();
   grid_dep_launch();
-  const uint2 sum = block_sums(__popc(sweep_flags(a, blockIdx.x)), 0u, sm);
+  const uint2 sum = block_sums(__popc(sweep_bits(a, blockIdx.x)), 0u, sm);
   if (threadIdx.x == 0) a.sums[blockIdx.x] = sum.x;
 }
 __global__ void __launch_bounds__(kSweepThreads) k_sweep_apply(const SweepArgs a) {
   __shared__ SweepSmem sm;
   grid_dep_wait();
   grid_dep_launch();
-  sweep_apply<false>(a, blockIdx.x, sweep_flags(a, blockIdx.x), a.sums, sm);
+  sweep_apply<false>(a, blockIdx.x, sweep_bits(a, blockIdx.x), a.sums, sm);
 }
 __global__ void __launch_bounds__(kSweepThreads) k_sweep_table(const SweepArgs a) {
   grid_dep_wait();
@@ -470,7 +471,7 @@ __global__ void __launch_bounds__(kSweepThreads) k_sweep_table(const SweepArgs a
   __threadfence();
 }
 // All of it by one cluster; its barrier orders the phases' global writes.  What
-// the first phases read of the inputs is loaded before the flags are clear, a
+// the first phases read of the inputs is loaded before the bits are clear, a
 // CTA's (at most kNearTiles) tiles stay in registers, and the tiles' sums go
 // straight into every CTA's shared memory.
 constexpr int kNearTiles = (int)(2 * (kSweepClusterCells / kTile) / kSweepCluster);
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(kSweepThreads) k_sweep_cluster(const SweepArgs
 #pragma unroll
   for (int k = 0; k < kNearTiles; ++k) {
     const int t = (int)blockIdx.x + k * kSweepCluster;
-    w[k] = t < tiles ? sweep_flags(a, t) : 0u;
+    w[k] = t < tiles ? sweep_bits(a, t) : 0u;
   }
 #pragma unroll
   for (int k = 0; k < kNearTiles; ++k) {
@@ -550,11 +551,11 @@ cudaError_t launch_seq_fork(const ForkArgs& a, unsigned* err, cudaStream_t strea
   return cudaGetLastError();
 }
 
-// Workspace: the cells' flags and the slots', in whole tiles, then the tiles' sums.
+// Workspace: the cells' bits and the slots', in whole tiles, then the tiles' sums.
 static int64_t sweep_tiles(int64_t n) { return ceil_div(n > 0 ? n : 1, kTile); }
 size_t sweep_workspace_bytes(int64_t n_cells, int64_t n_slots) {
   const int64_t tiles = sweep_tiles(n_cells) + sweep_tiles(n_slots);
-  return (size_t)round_up(tiles * kTile + tiles * 4, 256);
+  return (size_t)round_up(tiles * (kTileWords * 4) + tiles * 4, 256);
 }
 
 // Clusters of kSweepCluster CTAs can run on the current device (asked once per device).
@@ -593,10 +594,10 @@ cudaError_t launch_cache_sweep(const SweepArgs& args, void* ws, unsigned* err, c
   SweepArgs a = args;
   a.cell_tiles = sweep_tiles(a.n_cells);
   a.slot_tiles = sweep_tiles(a.n_slots);
-  a.cell_flags = static_cast<unsigned char*>(ws);
-  a.slot_flags = a.cell_flags + a.cell_tiles * kTile;
+  a.cell_bits = static_cast<unsigned*>(ws);
+  a.slot_bits = a.cell_bits + a.cell_tiles * kTileWords;
   const int64_t tiles = a.cell_tiles + a.slot_tiles;
-  a.sums = reinterpret_cast<unsigned*>(a.cell_flags + tiles * kTile);
+  a.sums = a.cell_bits + tiles * kTileWords;
   a.rows16 = ((reinterpret_cast<uintptr_t>(a.blk_cells) | reinterpret_cast<uintptr_t>(a.blk_cells_out)) & 15u) == 0u;
   a.map16 = (reinterpret_cast<uintptr_t>(a.cell_map) & 15u) == 0u;
   const dim3 block(kSweepThreads);
@@ -612,7 +613,7 @@ cudaError_t launch_cache_sweep(const SweepArgs& args, void* ws, unsigned* err, c
   if (cluster) {
     e = launch_pdl(k_sweep_cluster, dim3(kSweepCluster), block, 0, stream, kSweepCluster, a, err);
   } else {
-    e = launch_pdl(k_sweep_clear, grid(tiles * (kTile / 16)), block, 0, stream, 1, a);
+    e = launch_pdl(k_sweep_clear, grid(tiles * (kTileWords / 4)), block, 0, stream, 1, a);
     if (e == cudaSuccess) e = launch_pdl(k_sweep_mark, grid(entries), block, 0, stream, 1, a, err);
     if (e == cudaSuccess) e = launch_pdl(k_sweep_count, dim3((unsigned)tiles), block, 0, stream, 1, a);
     if (e == cudaSuccess) e = launch_pdl(k_sweep_apply, dim3((unsigned)tiles), block, 0, stream, 1, a);

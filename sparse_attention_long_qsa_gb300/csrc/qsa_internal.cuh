@@ -409,8 +409,8 @@ struct SweepArgs {
   int32_t* move_src;
   int32_t* move_dst;
   // workspace (launch_cache_sweep fills these)
-  unsigned char* cell_flags;
-  unsigned char* slot_flags;
+  unsigned* cell_bits;
+  unsigned* slot_bits;
   unsigned* sums;
   int rows16, map16;     // the tables' rows of four, and cell_map, can be moved 16 bytes at a time
   int64_t cell_tiles;
