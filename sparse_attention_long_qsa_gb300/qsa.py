@@ -230,8 +230,11 @@ def _at(t, dtype, dev, name, host_ok=False):
 
 def _bytes_at(t, dev, name):
     """_at of a cache, whose element type is the caller's business."""
-    if t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     return _ptr(t, None, name)
 
 
@@ -489,6 +492,8 @@ def cache_bytes(cfg, n_cells: int) -> int:
 
 def _check_cache(cfg, k_cache, v_cache, n_cells: int):
     need = cache_bytes(cfg, n_cells)
+    if k_cache is None or v_cache is None:
+        raise ValueError("k_cache and v_cache are required")
     if k_cache.nbytes < need or v_cache.nbytes < need:
         raise ValueError(f"k_cache and v_cache hold {k_cache.nbytes} and {v_cache.nbytes} bytes, {n_cells} cells need "
                          f"{need} each")

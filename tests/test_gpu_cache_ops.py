@@ -445,3 +445,46 @@ def test_a_served_run(kv_type):
     fcells = to_np(s["free_cells"])
     step([1, 2], [803, 2605], fcells[:2])
     assert_no_device_errors()
+
+
+def test_outputs_that_the_next_call_reads_early():
+    """The step's kernels read their inputs (queries, new rows, block lists,
+    cells) before they wait for their predecessor.  Calls that write such inputs
+    are followed at once by the calls that read them, 40 times with new data;
+    every result is that of the same calls with a synchronisation between."""
+    wl = make_workload(n_seq=2, prompt_len=[3000, 900], n_steps=1, seed=95, kv_type="q4_0")
+    A, B = QSALayer.from_workload(wl, 0, max_tokens=8), QSALayer.from_workload(wl, 0, max_tokens=8)
+    rope, cfg = qsa.rope_config((128,)), A.cfg
+    g = torch.Generator(device="cuda").manual_seed(6)
+    w = [torch.ones(n, device="cuda") for n in (256, 256, 128)]
+    st = step_inputs(wl.steps[0], new_cells=True)
+    for it in range(40):
+        T = 2
+        q_in = torch.randn((T, 16, 256), generator=g, device="cuda").bfloat16()
+        k_in = torch.randn((T, 2, 256), generator=g, device="cuda").bfloat16()
+        qi = torch.randn((T, 4, 128), generator=g, device="cuda").bfloat16()
+        w_idx, idx_new = torch.rand((T, 4), generator=g, device="cuda"), torch.randn((T, 128), generator=g, device="cuda").half()
+        v = torch.randn((T, 2, 256), generator=g, device="cuda").half()
+        pos = st["tok_pos"]
+        outs = []
+        for L, sync in ((A, False), (B, True)):
+            wait = torch.cuda.synchronize if sync else (lambda: None)
+            torch.cuda.synchronize()
+            q, k, q_idx = L.norm_rope(rope, pos, q_in, k_in, w[0], w[1], qi, pos, w[2])
+            wait()
+            out = L.full_step(st["tok_seq"], pos, q, q_idx, w_idx, st["cells"], k, v, idx_new).clone()
+            wait()
+            q2, _, _ = L.norm_rope(rope, pos, q_in * 2, k_in, w[1], w[1], qi, pos, w[2])
+            wait()
+            L.sparse_attn(q2, T)               # reads the queries first thing
+            out2 = L.out[:T].clone()
+            wait()
+            kr, vr = L.kv_read(st["cells"])    # and an append of rows just read back
+            wait()
+            L.kv_append(st["tok_seq"], pos, st["cells"], kr, vr, idx_new)
+            wait()
+            torch.cuda.synchronize()
+            outs.append((out, out2, kr, vr, L.k_cache.clone(), L.v_cache.clone(), L.cells.clone()))
+        for a, b in zip(*outs):
+            assert torch.equal(a, b), it
+    assert_no_device_errors()
