@@ -63,6 +63,7 @@ struct Smem {
                                                  // (blocks 144 B apart: their stores do not conflict)
   uint2 vd[kWarps][kBlocks][4];                  // its V scales times 2^wexp: block, l4 -> cells 2 l4 + {0, 1, 8, 9}
   float m[kWarps][kGqa], l[kWarps][kGqa];
+  float cta[2 * kGqa];                           // the CTA's (max, sum)
   alignas(16) float po[kGqa * kHeadDim];         // the cluster's partials of this CTA's dims: [NC][8][256 / NC]
   alignas(16) float pm[kMaxCluster][2 * kGqa];   // their (max, sum)
   float w[kMaxCluster][kGqa];
@@ -210,11 +211,14 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
   grid_dep_wait();
   grid_dep_launch();
   const int32_t* crow = a.cells + (int64_t)t * a.cells_pitch;
+  // chunks go round the cluster's CTAs first, so a short list uses all of them
+  const int first = warp * (int)NC + (int)rank, step = kWarps * (int)NC;
+  // the first chunk's ids and the count load together
+  const int i_first = first * kChunk + (lane & 15);
+  const int id_first = i_first < a.cells_pitch ? crow[i_first] : 0;
   int cnt = a.count[t];
   cnt = cnt < 0 ? 0 : (cnt > a.cells_pitch ? a.cells_pitch : cnt);
   const int n_chunks = (cnt + kChunk - 1) / kChunk;
-  // chunks go round the cluster's CTAs first, so a short list uses all of them
-  const int first = warp * (int)NC + (int)rank, step = kWarps * (int)NC;
 
   const uint32_t ring = smem_u32(sm.stage[warp]);
   const unsigned char* kc = static_cast<const unsigned char*>(a.k_cache);
@@ -276,7 +280,7 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
   __half2 up = pow2h(0);                  // 2^wexp
   unsigned valid[kStages - 1] = {};       // of the chunks in flight, oldest first: which of the 16 cells exist
 
-  int ahead = listed(first);
+  int ahead = i_first < cnt ? id_first : kPast;
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) {
     const int chunk = first + s * step;
@@ -469,15 +473,20 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
             make_float2(acc[b][0][2 + e] * (f[e] * 0.0625f), acc[b][1][2 + e] * (f[e] * 0.0625f));
       }
   }
-  // the CTA's (max, sum) of head h in threads h < 8
-  float cta_m = kNoMax, cta_l = 0.f;
-  if (tid < kGqa) {
+  // the CTA's (max, sum) of each head: four lanes of warp 0 a head
+  if (warp == 0) {
+    float m = kNoMax, l = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) cta_m = fmaxf(cta_m, sm.m[w][tid]);
+    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm.m[w][gid]);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-      cta_l += sm.l[w][tid] * exp2f(sm.m[w][tid] - cta_m);
-    if (NC == 1) sm.w[0][tid] = cta_l != 0.f ? 1.0f / cta_l : 0.f;
+    for (int w = 0; w < kWarps; w += 4)
+      if (w + l4 < kWarps) l += sm.l[w + l4][gid] * exp2f(sm.m[w + l4][gid] - m);
+    l += __shfl_xor_sync(kFull, l, 1);
+    l += __shfl_xor_sync(kFull, l, 2);
+    if (l4 == 0) {
+      sm.cta[gid] = m;
+      sm.cta[kGqa + gid] = l;
+    }
   }
   __syncthreads();
   // four dims of a head, summed over the warps
@@ -495,18 +504,15 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
   if (NC == 1) {
     for (int i = tid; i < kGqa * kHeadDim / 4; i += kThreads) {
       const float4 o = sum4(i);
-      const float w = sm.w[0][i >> 6];
+      const float l = sm.cta[kGqa + (i >> 6)], w = l != 0.f ? 1.0f / l : 0.f;
       reinterpret_cast<float4*>(out)[i] = make_float4(o.x * w, o.y * w, o.z * w, o.w * w);
     }
     cluster_wait();
     return;
   }
   cluster_wait();   // every CTA of the cluster runs
-  if (tid < kGqa)
-    for (uint32_t r = 0; r < NC; ++r) {
-      st_dsmem_f32(dsmem_addr(&sm.pm[rank][tid], r), cta_m);
-      st_dsmem_f32(dsmem_addr(&sm.pm[rank][kGqa + tid], r), cta_l);
-    }
+  for (int i = tid; i < 2 * kGqa * (int)NC; i += kThreads)
+    st_dsmem_f32(dsmem_addr(&sm.pm[rank][i % (2 * kGqa)], (uint32_t)(i / (2 * kGqa))), sm.cta[i % (2 * kGqa)]);
   // partial o: dims [r * 256 / NC, ...) go to CTA r
   const int dpc = kHeadDim / (int)NC;
   for (int i = tid; i < kGqa * kHeadDim / 4; i += kThreads) {
@@ -515,15 +521,17 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
     st_dsmem_f32x4(dsmem_addr(&sm.po[((int)rank * kGqa + h) * dpc + d % dpc], (uint32_t)(d / dpc)), o);
   }
   cluster_sync();   // all pushes have landed; nobody touches a peer after this
-  if (tid < kGqa) {
-    float m = kNoMax, l = 0.f;
-    for (int r = 0; r < (int)NC; ++r) m = fmaxf(m, sm.pm[r][tid]);
-    for (int r = 0; r < (int)NC; ++r) {
-      const float w = exp2f(sm.pm[r][tid] - m);
-      sm.w[r][tid] = w;
-      l += w * sm.pm[r][kGqa + tid];
-    }
-    for (int r = 0; r < (int)NC; ++r) sm.w[r][tid] = l != 0.f ? sm.w[r][tid] / l : 0.f;
+  if (tid < kMaxCluster * kGqa) {   // the partials' weights, a head's in 16 neighbouring lanes
+    const int h = tid >> 4, r = tid & 15;
+    const float m = r < (int)NC ? sm.pm[r][h] : kNoMax, l = r < (int)NC ? sm.pm[r][kGqa + h] : 0.f;
+    float top = m;
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+    const float w = exp2f(m - top);
+    float sum = w * l;
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    sm.w[r][h] = sum != 0.f ? w / sum : 0.f;
   }
   __syncthreads();
   for (int i = tid; i < kGqa * dpc; i += kThreads) {
@@ -590,11 +598,11 @@ cudaError_t launch(const AttnArgs& a, int nc, unsigned* err, cudaStream_t stream
 }
 
 // Cluster size for kWarps warps a CTA, and the time the call then takes by this
-// reckoning, in units of 0.05 us.  Measured at 1 to 512 tokens (250k cells, 129
-// chunks, every size and both warp counts): 6 us for launch, prologue and
-// merge, and for each chunk that a warp takes 0.9 us with 4 warps on the SM, 1.3
-// with 8 and 2.3 with 16 (where the SM's throughput decides).  16 tokens: 17 us
-// with as many warps as fit, 12.6 us with half of them and twice the chunks.
+// reckoning, in units of 0.05 us.  Fitted to every size and both warp counts at 1
+// to 512 tokens (250k cells, 129 chunks): 4.5 us for launch, prologue and merge,
+// and for each chunk that a warp takes 0.9 us with 4 warps on the SM, 1.3 with 8
+// and 2.3 with 16 (where the SM's throughput decides).  16 tokens: 17 us with as
+// many warps as fit, 12 us with half of them and twice the chunks.
 template <int kWarps>
 cudaError_t plan(int64_t clusters, int chunks, int* nc, int64_t* cost) {
   const int* active = nullptr;
@@ -613,9 +621,9 @@ cudaError_t plan(int64_t clusters, int chunks, int* nc, int64_t* cost) {
     };
     // past what fits: single CTAs follow one another on an SM, clusters come in waves
     int64_t w;
-    if (clusters <= active[i]) w = 120 + steps * chunk(per_sm < slots ? per_sm : slots);
-    else if (c > 1) w = ceil_div(clusters, (int64_t)active[i]) * (120 + steps * chunk(slots));
-    else w = 120 * ceil_div(per_sm, slots) + steps * (per_sm / slots * chunk(slots) + (per_sm % slots ? chunk(per_sm % slots) : 0));
+    if (clusters <= active[i]) w = 90 + steps * chunk(per_sm < slots ? per_sm : slots);
+    else if (c > 1) w = ceil_div(clusters, (int64_t)active[i]) * (90 + steps * chunk(slots));
+    else w = 90 * ceil_div(per_sm, slots) + steps * (per_sm / slots * chunk(slots) + (per_sm % slots ? chunk(per_sm % slots) : 0));
     if (*cost < 0 || w <= *cost) {   // the smaller of two equals
       *cost = w;
       *nc = c;
