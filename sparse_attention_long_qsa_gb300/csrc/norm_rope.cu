@@ -329,12 +329,14 @@ cudaError_t launch_norm_rope(const NormRopeArgs& a, const qsa_rope& rope, int el
   return cudaGetLastError();
 }
 
-// turns[i] = theta^(-i/m) / (2 pi) of a turn, scaled to 2^64 and rounded: the
-// frequency in double, its fraction of a turn in long double.
+// theta^exponent / (2 pi) of a turn, less whole turns (a theta below one gives
+// frequencies above one radian), scaled to 2^64 and rounded: the frequency in
+// double, its fraction of a turn in long double.
 unsigned long long turn_of(double theta, double exponent) {
   const long double two_pi = 6.28318530717958647692528676655900577L;
   const double f = std::pow(theta, exponent);
-  const long double x = ((long double)f / two_pi) * 18446744073709551616.0L;
+  const long double turns = (long double)f / two_pi;
+  const long double x = (turns - std::floor(turns)) * 18446744073709551616.0L;
   return x >= 18446744073709551615.0L ? ~0ull : (unsigned long long)(x + 0.5L);
 }
 

@@ -60,6 +60,20 @@ def test_rope_init(L):
     assert L.qsa_rope_init(ctypes.byref(c), 1, (ctypes.c_int32 * 1)(8), 0, None) == -1
 
 
+@pytest.mark.parametrize("theta", [0.5, 0.1, 1e-3])
+def test_rope_frequencies_of_several_turns(theta):
+    """Whole turns of a frequency above 2 pi do not count.  The frequency is a double (the power to an ulp or two:
+    2^-51 of it), so its turns are off by at most 2^-51 of them; the rounding to a whole unit adds half of one."""
+    r = qsa.rope_config((64,), cfg=qsa.config(rope_theta=theta))
+    th = float(np.float32(theta))
+    for table, m in ((r.turns, 64), (r.idx_turns, 64)):
+        for i in (0, 1, 31, 63):
+            turns = th ** (-i / m) / (2 * np.pi)
+            got = table[i] / 2.0 ** 64
+            err = abs(got - turns % 1.0)
+            assert min(err, 1.0 - err) <= 2.0 ** -50 * (1.0 + turns)
+
+
 def test_norm_rope_host_checks(L):
     c, r = qsa.config(), qsa.rope_config((64,))
     #       0                1                2  3  4  5  6     7  8    9  10 11 12 13 14 15   16 17 18
