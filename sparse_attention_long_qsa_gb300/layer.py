@@ -32,6 +32,15 @@ def _dev(x, dtype=None, device="cuda"):
     return t.to(device)
 
 
+def _on(stream):
+    """Tensors made within belong to `stream` (a torch stream, its handle, or
+    None for the current one): filled before what is launched there, and on
+    memory that no other stream still uses."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
 class QSALayer:
     def __init__(self, cfg: dict, idx_k, k_cache, v_cache, n_cells: int, blk_cells, slot_block_idx,
                  seq_blk_off, seq_blk_slots, norm_w, max_blocks: int, max_tokens: int,
@@ -147,15 +156,20 @@ class QSALayer:
 
     def norm_rope(self, rope, pos, q_in, k_in, q_norm_w, k_norm_w, q_idx_in, idx_pos, q_idx_norm_w, stream=None):
         """Head norms and rotation of T tokens' projections into the layer's
-        buffers; returns (q, k_new, q_idx) as full_step takes them."""
+        buffers (more than max_tokens: into new ones, the layer's stay where
+        they are); returns (q, k_new, q_idx) as full_step takes them."""
         T, c = int(q_in.shape[0]), self.cfgd
-        if self._heads is None or self._heads[0].shape[0] < T:
-            n = max(T, self.max_tokens)
-            new = lambda h, d, t: torch.empty((n, h, d), dtype=t, device=self.device)  # noqa: E731
-            self._heads = (new(c["n_q_heads"], c["head_dim"], torch.float16),
-                           new(c["n_kv_heads"], c["head_dim"], torch.float16),
-                           new(c["n_idx_heads"], c["idx_dim"], torch.float32))
-        q, k, qi = (x[:T] for x in self._heads)
+        heads = self._heads
+        if heads is None or T > self.max_tokens:
+            def new(h, d, t):
+                return torch.empty((max(T, self.max_tokens), h, d), dtype=t, device=self.device)
+            with _on(stream):
+                heads = (new(c["n_q_heads"], c["head_dim"], torch.float16),
+                         new(c["n_kv_heads"], c["head_dim"], torch.float16),
+                         new(c["n_idx_heads"], c["idx_dim"], torch.float32))
+            if T <= self.max_tokens:
+                self._heads = heads
+        q, k, qi = (x[:T] for x in heads)
         qsa.qk_norm_rope(self.cfg, rope, pos, q_in, k_in, q_norm_w, k_norm_w, q, k, q_idx_in, idx_pos,
                          q_idx_norm_w, qi, stream)
         return q, k, qi
@@ -163,7 +177,8 @@ class QSALayer:
     def kv_read(self, cells, stream=None):
         """K and V rows of the listed cells as fp16 [n][n_kv_heads][head_dim]."""
         shape = (int(cells.numel()), self.cfgd["n_kv_heads"], self.cfgd["head_dim"])
-        k, v = (torch.zeros(shape, dtype=torch.float16, device=self.device) for _ in range(2))
+        with _on(stream):
+            k, v = (torch.zeros(shape, dtype=torch.float16, device=self.device) for _ in range(2))
         qsa.kv_read(self.cfg, cells, self.k_cache, self.v_cache, self.n_cells, k, v, stream)
         return k, v
 
@@ -173,7 +188,8 @@ class QSALayer:
         lists and tables, and this layer's rows of the private tail cells.
         Returns the (source, destination) cell pairs, for other layers."""
         n, r = int(src_seq.numel()), self.cfgd["compress_ratio"]
-        pairs = torch.empty((2, n, r), dtype=torch.int32, device=self.device)
+        with _on(stream):
+            pairs = torch.empty((2, n, r), dtype=torch.int32, device=self.device)
         # the lists bound every sequence's blocks
         qsa.seq_fork(self.cfg, src_seq, dst_seq, n_pos, tail_slot, tail_cells, self.seq_blk_off, self.seq_blk_slots,
                      self.blk_cells, self.slot_block_idx, int(self.seq_blk_slots.numel()), pairs[0], pairs[1],
@@ -186,14 +202,17 @@ class QSALayer:
         """Free what the sequences no longer hold (seq_len: int32 CUDA tensor,
         positions each one keeps); compact: also move the held cells to the
         front, this layer's rows with them.  Returns a dict of the sweep's
-        outputs (counts, cell_map, free_cells, free_slots, move_src, move_dst)."""
+        outputs (counts, cell_map, free_cells, free_slots, move_src, move_dst):
+        the layer's own tensors, which the next call writes again."""
         n, dev = self.n_cells, self.device
         if self._sweep is None:
-            i32 = lambda m: torch.full((m,), -1, dtype=torch.int32, device=dev)  # noqa: E731
-            self._sweep = dict(counts=i32(4), cell_map=i32(n), free_cells=i32(n), free_slots=i32(self.n_slots),
-                               move_src=i32(n // 2), move_dst=i32(n // 2))
-            self._ws_sweep = torch.empty(qsa.cache_sweep_workspace_size(self.cfg, n, self.n_slots),
-                                         dtype=torch.uint8, device=dev)
+            def i32(m):
+                return torch.full((m,), -1, dtype=torch.int32, device=dev)
+            with _on(stream):
+                self._sweep = dict(counts=i32(4), cell_map=i32(n), free_cells=i32(n), free_slots=i32(self.n_slots),
+                                   move_src=i32(n // 2), move_dst=i32(n // 2))
+                self._ws_sweep = torch.empty(qsa.cache_sweep_workspace_size(self.cfg, n, self.n_slots),
+                                             dtype=torch.uint8, device=dev)
         s = self._sweep
         qsa.cache_sweep(self.cfg, seq_len, self.seq_blk_off, self.seq_blk_slots, self.blk_cells, self.blk_cells, n,
                         s["counts"], self._ws_sweep, compact, s["cell_map"], s["free_cells"], s["free_slots"],

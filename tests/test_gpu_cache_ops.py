@@ -488,3 +488,58 @@ def test_outputs_that_the_next_call_reads_early():
         for a, b in zip(*outs):
             assert torch.equal(a, b), it
     assert_no_device_errors()
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_layer_calls_on_a_stream_that_is_ahead(handle):
+    """A layer's calls on another stream than the current one, which is busy: what they allocate and fill must be
+    ordered on their own stream."""
+    wl = make_workload(n_seq=2, prompt_len=[3000, 902], n_steps=1, seed=97, kv_type="q4_0")
+    cells, length = _i32(wl.seq_cells[0][:500]), _i32([3000, 900])
+    # sequence 1's block 225 (positions 900, 901) is freed first; then it is forked from sequence 0 with that block
+    tail = [int(c) for c in wl.seq_cells[1][900:902]] + [-1, -1]
+    slot = int(wl.seq_blk_slots[wl.seq_blk_off[1] + 225])
+    fork = [_i32(x) for x in ([0], [1], [802], [slot], [tail])]
+    got = []
+    for ahead in (False, True):
+        L = QSALayer.from_workload(wl, 0)
+        other = torch.cuda.Stream()
+        stream = None if not ahead else other.cuda_stream if handle else other
+        torch.cuda.synchronize()
+        if ahead:
+            torch.cuda._sleep(40_000_000)          # some 20 ms on the current stream
+        k, v = L.kv_read(cells, stream=stream)
+        swept = L.release(length, stream=stream)
+        swept = {n: t for n, t in swept.items() if not n.startswith("move")}
+        pairs = L.fork(*fork, stream=stream)
+        torch.cuda.synchronize()
+        got.append([k, v, *swept.values(), *pairs, L.blk_cells, L.k_cache])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert_no_device_errors()
+
+
+def test_norm_rope_of_more_tokens_leaves_the_layers_buffers():
+    """A captured call writes the layer's buffers; a larger eager call in between does not move them."""
+    wl = make_workload(n_seq=1, prompt_len=[400], n_steps=1, seed=98)
+    L, rope = QSALayer.from_workload(wl, 0, max_tokens=4), qsa.rope_config((64,))
+    g = torch.Generator(device="cuda").manual_seed(3)
+    w = [torch.ones(n, device="cuda") for n in (256, 256, 128)]
+
+    def rows(T):
+        return [torch.randn((T, h, d), generator=g, device="cuda") for h, d in ((16, 256), (2, 256), (4, 128))]
+
+    small, large = rows(2), rows(9)
+    pos = torch.arange(9, dtype=torch.int32, device="cuda")
+    call = lambda x: L.norm_rope(rope, pos[:len(x[0])], x[0], x[1], w[0], w[1], x[2], pos[:len(x[0])], w[2])  # noqa: E731
+    first = call(small)
+    want = [t.clone() for t in first]
+    at = [t.data_ptr() for t in first]
+    big = [t.clone() for t in call(large)]
+    again = call(small)
+    assert [t.data_ptr() for t in again] == at
+    for a, b in zip(again, want):
+        assert torch.equal(a, b)
+    for a, b in zip(call(large), big):
+        assert torch.equal(a, b)
+    assert_no_device_errors()
