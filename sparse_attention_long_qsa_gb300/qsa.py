@@ -510,6 +510,8 @@ def cells_copy(cfg, src, dst, k_cache, v_cache, idx_k, n_cells: int, n_pairs=Non
     _check_cache(cfg, k_cache, v_cache, n_cells)
     if idx_k is not None and idx_k.numel() < int(n_cells) * cfg.idx_dim:
         raise ValueError(f"idx_k must hold {n_cells} rows")
+    if n_pairs is not None and n_pairs.numel() < 1:
+        raise ValueError("n_pairs must hold one value")
     st = lib().qsa_cells_copy(
         ctypes.byref(cfg), n, None if n_pairs is None else _at(n_pairs, i32, dev, "n_pairs"), _at(src, i32, dev, "src"),
         _at(dst, i32, dev, "dst"), _bytes_at(k_cache, dev, "k_cache"), _bytes_at(v_cache, dev, "v_cache"),

@@ -176,6 +176,14 @@ def test_binding_refusals(L):
         qsa.seq_fork(c, i, i, i, i, i, i.long(), i, i.view(3, 1), i, 4, i, i)
 
 
+def test_an_empty_pair_count_is_refused(L):
+    """(an empty tensor has no address, and no address would mean that all pairs count)"""
+    i, c = torch.zeros(3, dtype=torch.int32), qsa.config()
+    rows = torch.zeros((1, 2, 256), dtype=torch.float16)
+    with pytest.raises(ValueError, match="n_pairs must hold one value"):
+        qsa.cells_copy(c, i, i, rows, rows, None, 1, n_pairs=i[:0])
+
+
 # ------------------------------------------------------------------ q4_0
 def test_q4_0_block_closed_forms():
     x = np.zeros(32, dtype=np.float32)
