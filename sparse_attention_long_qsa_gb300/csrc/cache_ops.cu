@@ -199,7 +199,8 @@ k_seq_fork(const ForkArgs a, unsigned* err) {
 //           those positions
 //   count   held cells and slots of each tile
 //   apply   ranks: free lists, moves, cell_map
-//   table   the block table under the new places
+//   table   the block table under the new places (without compaction the bits
+//           say all it needs, so it does not wait for the counts)
 // A small cache is swept by one cluster with its hardware barrier between the
 // phases, one launch in all; a large one by five kernels over the whole GPU.
 constexpr int kSweepThreads = 1024, kSweepWarps = kSweepThreads / 32;
@@ -462,8 +463,10 @@ __global__ void __launch_bounds__(kSweepThreads) k_sweep_count(const SweepArgs a
 __global__ void __launch_bounds__(kSweepThreads) k_sweep_apply(const SweepArgs a) {
   __shared__ SweepSmem sm;
   grid_dep_wait();
-  grid_dep_launch();
+  if (a.compact) grid_dep_launch();   // else this is the last kernel
+  else sweep_table(a, grid_thread(), grid_threads());
   sweep_apply<false>(a, blockIdx.x, sweep_bits(a, blockIdx.x), a.sums, sm);
+  __threadfence();
 }
 __global__ void __launch_bounds__(kSweepThreads) k_sweep_table(const SweepArgs a) {
   grid_dep_wait();
@@ -506,14 +509,19 @@ __global__ void __launch_bounds__(kSweepThreads) k_sweep_cluster(const SweepArgs
     const uint2 sum = block_sums(__popc(w[k]), 0u, sm);
     if (t < tiles && threadIdx.x < kSweepCluster) st_dsmem_u32(dsmem_addr(&s_sums[t], threadIdx.x), sum.x);
   }
-  cluster_sync();
+  cluster_arrive();
+  if (!a.compact) sweep_table(a, i0, n);
+  __syncwarp();
+  cluster_wait();
 #pragma unroll
   for (int k = 0; k < kNearTiles; ++k) {
     const int t = (int)blockIdx.x + k * kSweepCluster;
     if (t < tiles) sweep_apply<true>(a, t, w[k], s_sums, sm);
   }
-  cluster_sync();
-  sweep_table(a, i0, n);
+  if (a.compact) {
+    cluster_sync();
+    sweep_table(a, i0, n);
+  }
   __threadfence();
 }
 
@@ -617,7 +625,7 @@ cudaError_t launch_cache_sweep(const SweepArgs& args, void* ws, unsigned* err, c
     if (e == cudaSuccess) e = launch_pdl(k_sweep_mark, grid(entries), block, 0, stream, 1, a, err);
     if (e == cudaSuccess) e = launch_pdl(k_sweep_count, dim3((unsigned)tiles), block, 0, stream, 1, a);
     if (e == cudaSuccess) e = launch_pdl(k_sweep_apply, dim3((unsigned)tiles), block, 0, stream, 1, a);
-    if (e == cudaSuccess) e = launch_pdl(k_sweep_table, grid(a.n_slots), block, 0, stream, 1, a);
+    if (e == cudaSuccess && a.compact) e = launch_pdl(k_sweep_table, grid(a.n_slots), block, 0, stream, 1, a);
   }
   prof_after(kKSweep, stream);
   if (e != cudaSuccess) return e;
