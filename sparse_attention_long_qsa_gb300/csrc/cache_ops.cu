@@ -202,15 +202,16 @@ k_seq_fork(const ForkArgs a, unsigned* err) {
 //   table   the block table under the new places (without compaction the bits
 //           say all it needs, so it does not wait for the counts)
 // A small cache is swept by one cluster with its hardware barrier between the
-// phases, one launch in all; a large one by five kernels over the whole GPU.
+// phases, one launch in all; a large one by kernels of their own over the whole GPU.
 constexpr int kSweepThreads = 1024, kSweepWarps = kSweepThreads / 32;
 constexpr int kTile = 4 * kSweepThreads;        // a thread's four cells or slots of a tile
 constexpr int kTileWords = kTile / 32;
 constexpr int kSweepCluster = 16;
 // A cluster sweeps caches of up to so many cells, list entries and slots: the
-// host makes one launch instead of five (some 8 us less) and the device takes as
-// long or less (us, cluster / five kernels, compacting: 10.3 / 11.3 at 5,000
-// cells, 14.0 / 15.4 at 50,000, 16.5 / 15.6 at 65,536).
+// host makes one launch instead of four or five (some 8 us less) and the device takes as
+// long or less (us, cluster / kernels of their own, compacting: 10.0 / 11.3 at
+// 5,000 cells, 12.4 / 15.4 at 50,000, 14.7 / 15.6 at 65,536; past it an entry
+// loop of two rounds or more costs the cluster 2 us each).
 constexpr int64_t kSweepClusterCells = 65536;
 constexpr int kSweepSeqs = 256;                 // sequences whose lists a CTA keeps in shared memory
 
@@ -289,19 +290,21 @@ __device__ __forceinline__ SweepEntry sweep_entry(const SweepArgs& a, const Swee
   }
   return r;
 }
-__device__ __forceinline__ void sweep_flag(const SweepArgs& a, const SweepEntry& r, unsigned* err) {
+__device__ __forceinline__ void sweep_flag(const SweepArgs& a, const SweepEntry& r, unsigned* cell_bits,
+                                           unsigned* slot_bits, unsigned* err) {
   if (r.slot < 0) return;
-  atomicOr(&a.slot_bits[r.slot >> 5], 1u << (r.slot & 31));
+  atomicOr(&slot_bits[r.slot >> 5], 1u << (r.slot & 31));
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if (i >= r.held || r.c[i] < 0) continue;
     if (r.c[i] >= a.n_cells) atomicOr(err, kErrCell);
-    else atomicOr(&a.cell_bits[r.c[i] >> 5], 1u << (r.c[i] & 31));
+    else atomicOr(&cell_bits[r.c[i] >> 5], 1u << (r.c[i] & 31));
   }
 }
-__device__ __forceinline__ void sweep_mark(const SweepArgs& a, const SweepSeqs& q, int64_t i0, int64_t n, unsigned* err) {
+__device__ __forceinline__ void sweep_mark(const SweepArgs& a, const SweepSeqs& q, int64_t i0, int64_t n,
+                                           unsigned* cell_bits, unsigned* slot_bits, unsigned* err) {
   for (int64_t e = i0; e < q.end; e += n)
-    sweep_flag(a, sweep_entry(a, q, e, e < q.lists ? a.seq_blk_slots[e] : -1, err), err);
+    sweep_flag(a, sweep_entry(a, q, e, e < q.lists ? a.seq_blk_slots[e] : -1, err), cell_bits, slot_bits, err);
 }
 
 // This thread's four bits of a tile.
@@ -451,7 +454,7 @@ __global__ void __launch_bounds__(kSweepThreads) k_sweep_mark(const SweepArgs a,
   __shared__ SweepSmem sm;
   grid_dep_wait();
   grid_dep_launch();
-  sweep_mark(a, sweep_seqs(a, sm), grid_thread(), grid_threads(), err);
+  sweep_mark(a, sweep_seqs(a, sm), grid_thread(), grid_threads(), a.cell_bits, a.slot_bits, err);
 }
 __global__ void __launch_bounds__(kSweepThreads) k_sweep_count(const SweepArgs a) {
   __shared__ SweepSmem sm;
@@ -473,52 +476,62 @@ __global__ void __launch_bounds__(kSweepThreads) k_sweep_table(const SweepArgs a
   sweep_table(a, grid_thread(), grid_threads());
   __threadfence();
 }
-// All of it by one cluster; its barrier orders the phases' global writes.  What
-// the first phases read of the inputs is loaded before the bits are clear, a
-// CTA's (at most kNearTiles) tiles stay in registers, and the tiles' sums go
-// straight into every CTA's shared memory.
+// All of it by one cluster.  Every CTA marks its entries in bits of its own, in
+// shared memory (50,000 cells: 62,500 atomics that cross no network); the CTA of
+// a tile (each has at most kNearTiles) joins the 16 CTAs' bits of it, keeps them
+// in registers, writes them out for the table, and puts the tile's sum straight
+// into every CTA's shared memory.
 constexpr int kNearTiles = (int)(2 * (kSweepClusterCells / kTile) / kSweepCluster);
 __global__ void __launch_bounds__(kSweepThreads) k_sweep_cluster(const SweepArgs a, unsigned* err) {
   __shared__ SweepSmem sm;
   __shared__ unsigned s_sums[kNearTiles * kSweepCluster];
+  __shared__ alignas(16) unsigned s_bits[kNearTiles * kSweepCluster * kTileWords];   // cells, then slots, as in the workspace
   static_assert(kNearTiles * kSweepCluster * (int64_t)kTile >= 2 * kSweepClusterCells, "every tile has a CTA");
+  static_assert(sizeof(s_bits) == 16 * kSweepThreads, "a thread clears 16 bytes");
+  static_assert(kSweepCluster == 16 && kTileWords * 8 == kSweepThreads, "eight threads a word join two CTAs' each");
   grid_dep_wait();
   // warps dealt to the CTAs in turn: a small cache keeps all 16 SMs busy
   const int64_t n = grid_threads();
   const int64_t i0 = ((int64_t)(threadIdx.x >> 5) * kSweepCluster + blockIdx.x) * 32 + (threadIdx.x & 31);
   const int slot0 = i0 < a.n_list ? a.seq_blk_slots[i0] : -1;
-  sweep_clear(a, i0, n);
+  reinterpret_cast<uint4*>(s_bits)[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
   const SweepSeqs q = sweep_seqs(a, sm);
   SweepEntry first;
   first.slot = -1;
   if (i0 < q.end) first = sweep_entry(a, q, i0, slot0, err);
-  cluster_sync();
-  sweep_flag(a, first, err);
-  sweep_mark(a, q, i0 + n, n, err);
+  __syncthreads();
+  unsigned* slot_bits = s_bits + a.cell_tiles * kTileWords;
+  sweep_flag(a, first, s_bits, slot_bits, err);
+  sweep_mark(a, q, i0 + n, n, s_bits, slot_bits, err);
+  __syncwarp();
   cluster_sync();
   unsigned w[kNearTiles];
-  const int tiles = (int)(a.cell_tiles + a.slot_tiles);
+  const int tiles = (int)(a.cell_tiles + a.slot_tiles), part = threadIdx.x & 7;
 #pragma unroll
   for (int k = 0; k < kNearTiles; ++k) {
     const int t = (int)blockIdx.x + k * kSweepCluster;
-    w[k] = t < tiles ? sweep_bits(a, t) : 0u;
+    const unsigned* word = s_bits + t * kTileWords + (threadIdx.x >> 3);
+    w[k] = t < tiles ? ld_dsmem_u32v(dsmem_addr(word, 2 * part)) | ld_dsmem_u32v(dsmem_addr(word, 2 * part + 1)) : 0u;
   }
 #pragma unroll
   for (int k = 0; k < kNearTiles; ++k) {
     const int t = (int)blockIdx.x + k * kSweepCluster;
+#pragma unroll
+    for (int o = 1; o <= 4; o <<= 1) w[k] |= __shfl_xor_sync(kFull, w[k], o);
+    if (t < tiles && part == 0) a.cell_bits[t * kTileWords + (threadIdx.x >> 3)] = w[k];
+    w[k] = (w[k] >> (4 * part)) & 15u;
     const uint2 sum = block_sums(__popc(w[k]), 0u, sm);
     if (t < tiles && threadIdx.x < kSweepCluster) st_dsmem_u32(dsmem_addr(&s_sums[t], threadIdx.x), sum.x);
   }
-  cluster_arrive();
+  cluster_sync();   // also: nobody touches a peer after this
   if (!a.compact) sweep_table(a, i0, n);
-  __syncwarp();
-  cluster_wait();
 #pragma unroll
   for (int k = 0; k < kNearTiles; ++k) {
     const int t = (int)blockIdx.x + k * kSweepCluster;
     if (t < tiles) sweep_apply<true>(a, t, w[k], s_sums, sm);
   }
   if (a.compact) {
+    __syncwarp();
     cluster_sync();
     sweep_table(a, i0, n);
   }

@@ -95,6 +95,12 @@ __device__ __forceinline__ unsigned ld_dsmem_u32(uint32_t addr) {
   asm("ld.shared::cluster.u32 %0, [%1];\n" : "=r"(v) : "r"(addr));
   return v;
 }
+// The same of words that peers write at other times: kept between the barriers around it.
+__device__ __forceinline__ unsigned ld_dsmem_u32v(uint32_t addr) {
+  unsigned v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];\n" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
 
 __device__ __forceinline__ void st_dsmem_u32(uint32_t addr, unsigned v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(addr), "r"(v) : "memory");
