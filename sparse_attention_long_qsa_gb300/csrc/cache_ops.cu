@@ -206,12 +206,18 @@ k_seq_fork(const ForkArgs a, unsigned* err) {
 constexpr int kSweepThreads = 1024, kSweepWarps = kSweepThreads / 32;
 constexpr int kTile = 4 * kSweepThreads;        // a thread's four cells or slots of a tile
 constexpr int kTileWords = kTile / 32;
+// Threads of a CTA that walks list entries or table rows by itself: these wait on
+// scattered accesses, and small CTAs leave no SM with a second wave of them
+// (1.25M cells, 1,024 threads: 23.0 us, compacting 30.9; 256: 22.0 and 29.5).
+// The ranks are faster with 1,024 (512: 22.9 and 32.4, as a thread's stores of
+// eight cells spread over more lines).
+constexpr int kSweepRows = 256;
 constexpr int kSweepCluster = 16;
-// A cluster sweeps caches of up to so many cells, list entries and slots: the
-// host makes one launch instead of four or five (some 8 us less) and the device takes as
-// long or less (us, cluster / kernels of their own, compacting: 10.0 / 11.3 at
-// 5,000 cells, 12.4 / 15.4 at 50,000, 14.7 / 15.6 at 65,536; past it an entry
-// loop of two rounds or more costs the cluster 2 us each).
+// A cluster sweeps caches of up to so many cells, list entries and slots.  The
+// host makes one launch instead of four or five, which is what such a call waits
+// for (us a call, cluster / kernels of their own, compacting: 11.1 / 21.1 at 5,000
+// cells, 12.6 / 20.4 at 50,000, 14.9 / 20.1 at 65,536); in a graph the device
+// takes 9.9 / 10.5, 12.3 / 13.8 and 14.7 / 13.9.
 constexpr int64_t kSweepClusterCells = 65536;
 constexpr int kSweepSeqs = 256;                 // sequences whose lists a CTA keeps in shared memory
 
@@ -236,7 +242,7 @@ struct SweepSeqs {
 __device__ __forceinline__ SweepSeqs sweep_seqs(const SweepArgs& a, SweepSmem& sm) {
   const bool near = a.n_seq <= kSweepSeqs;
   if (near) {
-    for (int i = threadIdx.x; i <= a.n_seq; i += kSweepThreads) {
+    for (int i = threadIdx.x; i <= a.n_seq; i += blockDim.x) {
       sm.off[i] = a.seq_blk_off[i];
       if (i < a.n_seq) sm.len[i] = a.seq_len[i];
     }
@@ -442,15 +448,15 @@ __device__ __forceinline__ void sweep_table(const SweepArgs& a, int64_t i0, int6
     *reinterpret_cast<volatile int32_t*>(a.cell_map + __ldcg(a.move_src + k)) = __ldcg(a.move_dst + k);
 }
 
-__device__ __forceinline__ int64_t grid_thread() { return (int64_t)blockIdx.x * kSweepThreads + threadIdx.x; }
-__device__ __forceinline__ int64_t grid_threads() { return (int64_t)gridDim.x * kSweepThreads; }
+__device__ __forceinline__ int64_t grid_thread() { return (int64_t)blockIdx.x * blockDim.x + threadIdx.x; }
+__device__ __forceinline__ int64_t grid_threads() { return (int64_t)gridDim.x * blockDim.x; }
 
 __global__ void __launch_bounds__(kSweepThreads) k_sweep_clear(const SweepArgs a) {
   grid_dep_wait();
   grid_dep_launch();
   sweep_clear(a, grid_thread(), grid_threads());
 }
-__global__ void __launch_bounds__(kSweepThreads) k_sweep_mark(const SweepArgs a, unsigned* err) {
+__global__ void __launch_bounds__(kSweepRows) k_sweep_mark(const SweepArgs a, unsigned* err) {
   __shared__ SweepSmem sm;
   grid_dep_wait();
   grid_dep_launch();
@@ -471,7 +477,7 @@ __global__ void __launch_bounds__(kSweepThreads) k_sweep_apply(const SweepArgs a
   sweep_apply<false>(a, blockIdx.x, sweep_bits(a, blockIdx.x), a.sums, sm);
   __threadfence();
 }
-__global__ void __launch_bounds__(kSweepThreads) k_sweep_table(const SweepArgs a) {
+__global__ void __launch_bounds__(kSweepRows) k_sweep_table(const SweepArgs a) {
   grid_dep_wait();
   sweep_table(a, grid_thread(), grid_threads());
   __threadfence();
@@ -622,7 +628,8 @@ cudaError_t launch_cache_sweep(const SweepArgs& args, void* ws, unsigned* err, c
   a.rows16 = ((reinterpret_cast<uintptr_t>(a.blk_cells) | reinterpret_cast<uintptr_t>(a.blk_cells_out)) & 15u) == 0u;
   a.map16 = (reinterpret_cast<uintptr_t>(a.cell_map) & 15u) == 0u;
   const dim3 block(kSweepThreads);
-  auto grid = [](int64_t n) { return dim3((unsigned)ceil_div(n > 0 ? n : 1, kSweepThreads)); };
+  const dim3 rows(kSweepRows);
+  auto grid = [](int64_t n, int threads) { return dim3((unsigned)ceil_div(n > 0 ? n : 1, threads)); };
   bool cluster = false;
   if (a.n_cells <= kSweepClusterCells && a.n_list <= kSweepClusterCells && a.n_slots <= kSweepClusterCells) {
     const cudaError_t e = sweep_cluster_ok(&cluster);
@@ -634,11 +641,11 @@ cudaError_t launch_cache_sweep(const SweepArgs& args, void* ws, unsigned* err, c
   if (cluster) {
     e = launch_pdl(k_sweep_cluster, dim3(kSweepCluster), block, 0, stream, kSweepCluster, a, err);
   } else {
-    e = launch_pdl(k_sweep_clear, grid(tiles * (kTileWords / 4)), block, 0, stream, 1, a);
-    if (e == cudaSuccess) e = launch_pdl(k_sweep_mark, grid(entries), block, 0, stream, 1, a, err);
+    e = launch_pdl(k_sweep_clear, grid(tiles * (kTileWords / 4), kSweepThreads), block, 0, stream, 1, a);
+    if (e == cudaSuccess) e = launch_pdl(k_sweep_mark, grid(entries, kSweepRows), rows, 0, stream, 1, a, err);
     if (e == cudaSuccess) e = launch_pdl(k_sweep_count, dim3((unsigned)tiles), block, 0, stream, 1, a);
     if (e == cudaSuccess) e = launch_pdl(k_sweep_apply, dim3((unsigned)tiles), block, 0, stream, 1, a);
-    if (e == cudaSuccess && a.compact) e = launch_pdl(k_sweep_table, grid(a.n_slots), block, 0, stream, 1, a);
+    if (e == cudaSuccess && a.compact) e = launch_pdl(k_sweep_table, grid(a.n_slots, kSweepRows), rows, 0, stream, 1, a);
   }
   prof_after(kKSweep, stream);
   if (e != cudaSuccess) return e;
