@@ -502,10 +502,16 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
   };
   float* out = a.out + ((int64_t)t * Hq + g * kGqa) * kHeadDim;
   if (NC == 1) {
+    const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0u;   // the call takes any float address
     for (int i = tid; i < kGqa * kHeadDim / 4; i += kThreads) {
       const float4 o = sum4(i);
       const float l = sm.cta[kGqa + (i >> 6)], w = l != 0.f ? 1.0f / l : 0.f;
-      reinterpret_cast<float4*>(out)[i] = make_float4(o.x * w, o.y * w, o.z * w, o.w * w);
+      const float4 y = make_float4(o.x * w, o.y * w, o.z * w, o.w * w);
+      if (wide) {
+        reinterpret_cast<float4*>(out)[i] = y;
+      } else {
+        out[4 * i] = y.x, out[4 * i + 1] = y.y, out[4 * i + 2] = y.z, out[4 * i + 3] = y.w;
+      }
     }
     cluster_wait();
     return;
