@@ -148,6 +148,8 @@ __device__ __forceinline__ uint32_t low_codes(uint32_t x) {
 __device__ __forceinline__ uint32_t high_codes(uint32_t x) {
   return bits(__hsub2(half2_of(and_or(x, 0x00f000f0u, 0x64006400u)), half2_of(0x64806480u)));
 }
+// x, infinities as NaN
+__device__ __forceinline__ __half2 nan_of_inf(__half2 x) { return __hfma2(x, half2_of(0u), x); }
 // 2^k as a half, k in [-24, 15]
 __device__ __forceinline__ __half2 pow2h(int k) {
   const uint32_t e = k >= -14 ? (uint32_t)(k + 15) << 10 : 1u << (k + 24);
@@ -321,7 +323,9 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
     {
       uint32_t d[2];
       ldmatrix2_trans(sk + (lane & 15) * kRow + 128, d);
-      const float2 d0 = __half22float2(half2_of(d[0])), d1 = __half22float2(half2_of(d[1]));
+      // an infinite scale of K becomes NaN (a block of such values holds infinities of both signs and NaN):
+      // times a block's sum it would be an infinity of either sign, and -inf a cell of probability zero
+      const float2 d0 = __half22float2(nan_of_inf(half2_of(d[0]))), d1 = __half22float2(nan_of_inf(half2_of(d[1])));
       sm.kd[warp][gid][2 * l4] = make_float4(d0.x, d0.x, d1.x, d1.x);
       sm.kd[warp][gid][2 * l4 + 1] = make_float4(d0.y, d0.y, d1.y, d1.y);
       ldmatrix2_trans(sv + (lane & 15) * kRow + 128, d);
