@@ -308,10 +308,12 @@ qsa_status qsa_index_topk_noalloc(const qsa_config* cfg, int32_t n_tokens,
  * share an SM; the result is the same within the stated tolerance.
  * For q4_0 K/V the codes are multiplied as integers (exactly) and only the
  * scales' products are rounded, in fp32 (probabilities in two fp16 parts): no
- * K, V or probability is rounded to fp16, and the output is as close to the
- * exact result as fp32 arithmetic on the decoded rows (2e-7 of the output's norm
- * for N(0,1) rows).  An infinite or NaN scale of an attended K block gives NaN,
- * one of a V block NaN in that block's dims.
+ * K, V or probability is rounded to fp16, and the output, block of 32 dims by
+ * block, is as close to the exact result as fp32 arithmetic on the decoded rows,
+ * however far apart the scales of V lie (N(0,1) rows, 2,051 cells: 3e-7 of the
+ * output's norm for one token, 8e-7 for 512; fp32 5e-7 and 9e-7).  An infinite or
+ * NaN scale of an attended K block gives NaN, one of a V block NaN in that
+ * block's dims.
  * count[t] == 0 gives zeros.  A cell outside [0, n_cells) is masked and
  * flagged.  The call needs no workspace (qsa_sparse_attn_workspace_size
  * returns 0; `workspace` may be NULL). */

@@ -20,18 +20,34 @@
 //        subnormals, n * 2^-24, and would save the subtraction, but the tensor
 //        core then drops low bits of the queries: scores off by 1e-6.)
 //   P.V  d_V is folded into the probabilities: w = p * d_V, split into two
-//        fp16 parts (22 bits), two products into one fp32 accumulator.  A
-//        common power of two keeps w off the fp16 range's ends.
+//        fp16 parts (22 bits), two products into fp32.  A half keeps its bits
+//        only 30 binary places below the largest, so three forms, chosen by what
+//        a chunk of 16 cells holds, keep what is lost small beside what the chunk
+//        itself adds to a block of dims, however little that is beside other
+//        chunks and other blocks:
+//          near   the chunk's probabilities and scales lie close to the warp's
+//                 largest: weights relative to those, summed in place (2^-18 of
+//                 the chunk's part lost at most, with all 16 cells at the edges)
+//          apart  weights relative to the chunk's own largest, summed in an
+//                 accumulator of its own, which is added with the chunk's factor
+//                 in fp32 (2^-22)
+//          wild   scales of V in the chunk more than 2^10 apart, zero, subnormal
+//                 or infinite: products in fp32, cell by cell
+//        512 tokens at 250k cells take 146 us so; 151 with every chunk apart; 140
+//        with weights relative to the warp's largest throughout, but then one
+//        cell or block of large values, however unlikely, cost all others their
+//        bits (5e-4 of a block's norm at a ratio of 3,000, a tenth of it at 1e6).
 //
 // Work split.  A warp takes 16 cells at a time: it copies their rows with
 // cp.async into its own ring of stages (kStages - 1 chunks in flight), forms
-// the scores of 8 heads x 16 cells, updates its running maximum (lazily: the
-// accumulator is rescaled only when a score exceeds the maximum in use by
-// 2^kLazy), and adds P.V.  Warps of a CTA and CTAs of a cluster share nothing
-// until the end, when their (max, sum, o) are merged in a fixed order through
-// shared and distributed shared memory.
+// the scores of 8 heads x 16 cells and adds P.V relative to a reference score a
+// head, which is raised, and the accumulator rescaled, when a chunk exceeds it.
+// Warps of a CTA and CTAs of a cluster share nothing until the end, when their
+// (reference, sum, o) are merged in a fixed order through shared and distributed
+// shared memory.
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 
 #include "qsa_internal.cuh"
 #include "tc_util.cuh"
@@ -45,11 +61,13 @@ constexpr int kRow = 144;                        // 128 B codes + 16 B scales: l
 constexpr int kStageBytes = 2 * kChunk * kRow;   // K rows, then V rows
 constexpr int kStages = 2;
 constexpr int kMaxCluster = 16;
-// Probabilities are held as 2^(s - m + kUp) so that their low fp16 part, 2^-11
-// of them, stays a normal half for all that count; s may pass the running
-// maximum m by kLazy before m follows.  2^(kUp + kLazy) <= 2^15.
-constexpr float kUp = 7.f, kLazy = 8.f;
-constexpr int kNoExp = 32;                       // no scale of V seen yet
+constexpr float kUp = 15.f;                      // probabilities are held as 2^(s - m + kUp), m a whole number, at least s
+constexpr float kSlack = 2.f;                    // a raised reference lies so far above the chunk's largest score
+constexpr float kNear = 7.f;                     // "near": the chunk's largest scores at most so far below the reference,
+constexpr int kNearExp = 2;                      // its largest scale of V within 2^-kNearExp of the warp's,
+constexpr unsigned kNearSpread = 5u << 10;       // its smallest (as bits) at most so far below its largest
+constexpr unsigned kSpread = 10u << 10;          // the same for "apart"
+constexpr int kNoExp = 64;                       // no scale of V seen yet
 constexpr float kNoMax = -3.0e38f;               // no cell seen yet (below every score, and finite)
 constexpr int kBlocks = kHeadDim / 32;           // q4_0 blocks of a row
 
@@ -61,7 +79,7 @@ struct Smem {
   uint4 q[kBlocks][32];                          // a lane's query fragments of a block: step 0, step 1
   float4 kd[kWarps][kBlocks][9];                 // a chunk's K scales: block, gid -> cells gid, gid + 8, each twice
                                                  // (blocks 144 B apart: their stores do not conflict)
-  uint2 vd[kWarps][kBlocks][4];                  // its V scales times 2^wexp: block, l4 -> cells 2 l4 + {0, 1, 8, 9}
+  uint2 vd[kWarps][kBlocks][4];                  // its V scales times a power of two: block, l4 -> cells 2 l4 + {0, 1, 8, 9}
   float m[kWarps][kGqa], l[kWarps][kGqa];
   float cta[2 * kGqa];                           // the CTA's (max, sum)
   alignas(16) float po[kGqa * kHeadDim];         // the cluster's partials of this CTA's dims: [NC][8][256 / NC]
@@ -81,9 +99,6 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4])
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
-}
-__device__ __forceinline__ void ldmatrix2(uint32_t addr, uint32_t (&r)[2]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];\n" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
 }
 __device__ __forceinline__ void ldmatrix2_trans(uint32_t addr, uint32_t (&r)[2]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];\n"
@@ -122,11 +137,11 @@ __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t o) {
   asm("lop3.b32 %0, %1, %2, %3, 0xea;\n" : "=r"(r) : "r"(x), "r"(m), "r"(o));
   return r;
 }
-// s += d * c, two fp32 values each
-__device__ __forceinline__ void fma2(float2& s, float dx, float dy, float cx, float cy) {
+// (sx, sy) += (dx, dy) * (cx, cy)
+__device__ __forceinline__ void fma2(float& sx, float& sy, float dx, float dy, float cx, float cy) {
   asm("{\n .reg .b64 s, d, c;\n mov.b64 s, {%0, %1};\n mov.b64 d, {%2, %3};\n mov.b64 c, {%4, %5};\n"
       " fma.rn.f32x2 s, d, c, s;\n mov.b64 {%0, %1}, s;\n}\n"
-      : "+f"(s.x), "+f"(s.y)
+      : "+f"(sx), "+f"(sy)
       : "f"(dx), "f"(dy), "f"(cx), "f"(cy));
 }
 __device__ __forceinline__ uint32_t bits(__half2 h) {
@@ -275,11 +290,10 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[b][i][j] = 0.f;
-  // of heads 2 l4, 2 l4 + 1; run_m: a running maximum less kUp, run_l: this thread's cells only
+  // of heads 2 l4, 2 l4 + 1; run_m: the reference (a whole number), run_l: this thread's cells only;
+  // acc and run_l carry 2^kUp, acc 2^wexp too
   float run_m[2] = {kNoMax, kNoMax}, run_l[2] = {0.f, 0.f};
-  int wexp = kNoExp;                      // weights carry 2^wexp
-  uint32_t dlim = 0u;                     // the largest V scale (as bits) that wexp allows
-  __half2 up = pow2h(0);                  // 2^wexp
+  int wexp = kNoExp;
   unsigned valid[kStages - 1] = {};       // of the chunks in flight, oldest first: which of the 16 cells exist
 
   int ahead = i_first < cnt ? id_first : kPast;
@@ -316,6 +330,7 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
     }
     const uint32_t sk = ring + (uint32_t)st * kStageBytes, sv = sk + kChunk * kRow;
     st = st == kStages - 1 ? 0 : st + 1;
+    if (ok == 0u) continue;   // none of the chunk's cells exists
 
     // ---- the chunk's scales, laid out once for all lanes.  The transposing
     // ldmatrix gives this thread those of cells 2 l4 + {0, 1, 8, 9} in block gid.
@@ -331,20 +346,24 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
       ldmatrix2_trans(sv + (lane & 15) * kRow + 128, d);
       dv[0] = half2_of(d[0]), dv[1] = half2_of(d[1]);
     }
-    // the largest scale of V sets the weights' exponent: d_max * 2^wexp lies in
-    // [2^-2, 2^-1) (below, for subnormal scales) when it is set, and stays below 1
-    const uint32_t dm = bits(__hmax2(__habs2(dv[0]), __habs2(dv[1])));
-    uint32_t db = __reduce_max_sync(kFull, max(dm >> 16, dm & 0xffffu));
-    int nexp = wexp;
-    // (an infinite scale spoils its own block's dims, not the others' weights)
-    if (db >= 0x7c00u)
-      db = __reduce_max_sync(kFull, max((dm >> 16) >= 0x7c00u ? 0u : dm >> 16,
-                                        (dm & 0xffffu) >= 0x7c00u ? 0u : dm & 0xffffu));
-    if (db > dlim) {
-      nexp = 13 - (int)(db >> 10);   // -17 .. 13
-      dlim = ((uint32_t)(15 - nexp) << 10) - 1u;
-      up = pow2h(nexp);
+    // the chunk's largest and smallest scale of V, and the exponent of its weights
+    const uint32_t dx = bits(__hmax2(__habs2(dv[0]), __habs2(dv[1])));
+    uint32_t dn = bits(__hmin2(__habs2(dv[0]), __habs2(dv[1])));
+    if (ok != kFull) {   // the cells that exist
+      const uint32_t a0 = bits(__habs2(dv[0])), a1 = bits(__habs2(dv[1])), o = ok >> (2 * l4);
+      const uint32_t e0 = (o & 1u) ? a0 & 0xffffu : 0xffffu, e1 = (o & 2u) ? a0 >> 16 : 0xffffu;
+      const uint32_t e2 = (o & 256u) ? a1 & 0xffffu : 0xffffu, e3 = (o & 512u) ? a1 >> 16 : 0xffffu;
+      const uint32_t e = min(min(e0, e1), min(e2, e3));
+      dn = e | (e << 16);
     }
+    const uint32_t dtop = __reduce_max_sync(kFull, max(dx >> 16, dx & 0xffffu));
+    const uint32_t dbot = __reduce_min_sync(kFull, min(dn >> 16, dn & 0xffffu));
+    const bool plain = dbot >= 0x0400u && dtop < 0x7c00u && dtop <= dbot + kSpread;
+    int vexp = plain ? 13 - (int)(dtop >> 10) : 0;   // brings the chunk's largest scale to [2^-2, 2^-1)
+    const int nexp = min(wexp, vexp);                // the warp's
+    bool near = plain && vexp <= nexp + kNearExp && dtop <= dbot + kNearSpread;
+    if (near) vexp = nexp;
+    const __half2 up = pow2h(vexp);
     sm.vd[warp][gid][l4] = make_uint2(bits(__hmul2(dv[0], up)), bits(__hmul2(dv[1], up)));
     __syncwarp();
 
@@ -363,8 +382,8 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
         float c[4];
         mma0(c, low_codes(w0), low_codes(w1), high_codes(w0), high_codes(w1), q.x, q.y);
         mma(c, low_codes(u0), low_codes(u1), high_codes(u0), high_codes(u1), q.z, q.w);
-        fma2(s[0], d.x, d.y, c[0], c[1]);
-        fma2(s[1], d.z, d.w, c[2], c[3]);
+        fma2(s[0].x, s[0].y, d.x, d.y, c[0], c[1]);
+        fma2(s[1].x, s[1].y, d.z, d.w, c[2], c[3]);
       }
     }
     // ---- softmax of the two heads over the 16 cells (8 lanes hold them)
@@ -378,13 +397,15 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
     for (int o = 4; o <= 16; o <<= 1)
 #pragma unroll
       for (int h = 0; h < 2; ++h) cm[h] = fmaxf(cm[h], __shfl_xor_sync(kFull, cm[h], o));
-    if (__any_sync(kFull, cm[0] > run_m[0] + (kUp + kLazy) || cm[1] > run_m[1] + (kUp + kLazy)) || nexp != wexp) {
+    // m: the next whole numbers, so that the factors between chunks are powers of two (no finite score: far below all)
+    const float m[2] = {fmaxf(ceilf(cm[0]), kNoMax), fmaxf(ceilf(cm[1]), kNoMax)};
+    if (__any_sync(kFull, m[0] > run_m[0] || m[1] > run_m[1]) || nexp != wexp) {
       float f[2];
       const float fe = wexp == kNoExp ? 1.f : exp2f((float)(nexp - wexp));   // accumulators of an unset exponent are zero
       wexp = nexp;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float nm = cm[h] > run_m[h] + (kUp + kLazy) ? cm[h] - kUp : run_m[h];
+        const float nm = m[h] > run_m[h] ? m[h] + kSlack : run_m[h];
         f[h] = exp2f(run_m[h] - nm);
         run_l[h] *= f[h];
         run_m[h] = nm;
@@ -398,49 +419,107 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
           acc[b][i][2] *= f[0], acc[b][i][3] *= f[1];
         }
     }
-    // probabilities in two parts, then from (cell, heads) to (head, cells)
+    near = near && !__any_sync(kFull, m[0] < run_m[0] - kNear || m[1] < run_m[1] - kNear);
+    const float m0 = near ? run_m[0] : m[0], m1 = near ? run_m[1] : m[1];
+    float p[2][2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      p[j][0] = ex2(fmaf(s[j].x, scale[0], kUp - m0));
+      p[j][1] = ex2(fmaf(s[j].y, scale[1], kUp - m1));
+      if (ok != kFull && !((ok >> (gid + 8 * j)) & 1u)) p[j][0] = p[j][1] = 0.f;
+    }
+    float fac[2] = {1.f, 1.f};   // of the chunk
+    if (!near) fac[0] = ex2(m0 - run_m[0]), fac[1] = ex2(m1 - run_m[1]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) run_l[h] = fmaf(p[0][h] + p[1][h], fac[h], run_l[h]);
+
+    if (!plain) {
+      // ---- the same cell by cell in fp32: this thread's dims 32 b + 2 gid + {0, 1} and the two 16 further
+      // (kept 16 times too large, as below)
+      const float up1 = exp2f((float)wexp);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          const unsigned char* row = sm.stage[warp][st == 0 ? kStages - 1 : st - 1] + (kChunk + 8 * j + i) * kRow;
+          const float w0 = __shfl_sync(kFull, p[j][0], 4 * i + l4) * (fac[0] * up1);
+          const float w1 = __shfl_sync(kFull, p[j][1], 4 * i + l4) * (fac[1] * up1);
+          const uint4 dr = *reinterpret_cast<const uint4*>(row + 128);
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b) {
+            const __half2 dh = nan_of_inf(half2_of(b < 2 ? dr.x : b < 4 ? dr.y : b < 6 ? dr.z : dr.w));
+            const float d = b & 1 ? __high2float(dh) : __low2float(dh), d0 = w0 * d, d1 = w1 * d;
+            const uint32_t c = *reinterpret_cast<const unsigned short*>(row + 16 * b + 2 * gid);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float lo = (float)((int)((c >> (8 * k)) & 15u) - 8), hi = 16.f * (float)((int)((c >> (8 * k + 4)) & 15u) - 8);
+              acc[b][k][0] = fmaf(d0, lo, acc[b][k][0]), acc[b][k][1] = fmaf(d1, lo, acc[b][k][1]);
+              acc[b][k][2] = fmaf(d0, hi, acc[b][k][2]), acc[b][k][3] = fmaf(d1, hi, acc[b][k][3]);
+            }
+          }
+        }
+      continue;
+    }
+
+    // the probabilities in two parts, from (cell, heads) to (head, cells)
     __half2 ph[2], pl[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      float p0 = ex2(fmaf(s[j].x, scale[0], -run_m[0])), p1 = ex2(fmaf(s[j].y, scale[1], -run_m[1]));
-      if (ok != kFull && !((ok >> (gid + 8 * j)) & 1u)) p0 = p1 = 0.f;
-      run_l[0] += p0;
-      run_l[1] += p1;
-      const __half2 hi = __floats2half2_rn(p0, p1);
+      const __half2 hi = __floats2half2_rn(p[j][0], p[j][1]);
       const float2 h = __half22float2(hi);
       ph[j] = half2_of(transposed(bits(hi)));
-      pl[j] = half2_of(transposed(bits(__floats2half2_rn(p0 - h.x, p1 - h.y))));
+      pl[j] = half2_of(transposed(bits(__floats2half2_rn(p[j][0] - h.x, p[j][1] - h.y))));
     }
 
     // ---- o^T[dim][head] += V^T . w, per block of 32 dims: tile i, row gid is
     // dim 32 b + 2 gid + i, row gid + 8 the dim 16 further (16 times too large)
+    auto add = [&](auto in_place) {
 #pragma unroll
-    for (int bp = 0; bp < 4; ++bp) {   // two blocks: lane l's address is row l % 16 of block 2 bp + l / 16
-      uint32_t v[4];
-      ldmatrix4_trans(sv + (lane & 15) * kRow + (2 * bp + (lane >> 4)) * 16, v);
+      for (int bp = 0; bp < 4; ++bp) {   // two blocks: lane l's address is row l % 16 of block 2 bp + l / 16
+        uint32_t v[4];
+        ldmatrix4_trans(sv + (lane & 15) * kRow + (2 * bp + (lane >> 4)) * 16, v);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int b = 2 * bp + i;
-        const uint2 d = sm.vd[warp][b][l4];
-        const __half2 d0 = half2_of(d.x), d1 = half2_of(d.y);
-        const __half2 h0 = __hmul2(ph[0], d0), h1 = __hmul2(ph[1], d1);
-        const uint32_t wh0 = bits(h0), wh1 = bits(h1);
-        const uint32_t wl0 = bits(__hfma2(pl[0], d0, __hfma2(ph[0], d0, __hneg2(h0))));
-        const uint32_t wl1 = bits(__hfma2(pl[1], d1, __hfma2(ph[1], d1, __hneg2(h1))));
-        uint32_t x[2][4];
+        for (int i = 0; i < 2; ++i) {
+          const int b = 2 * bp + i;
+          const uint2 d = sm.vd[warp][b][l4];
+          const __half2 d0 = half2_of(d.x), d1 = half2_of(d.y);
+          const __half2 h0 = __hmul2(ph[0], d0), h1 = __hmul2(ph[1], d1);
+          const uint32_t wh0 = bits(h0), wh1 = bits(h1);
+          const uint32_t wl0 = bits(__hfma2(pl[0], d0, __hfma2(ph[0], d0, __hneg2(h0))));
+          const uint32_t wl1 = bits(__hfma2(pl[1], d1, __hfma2(ph[1], d1, __hneg2(h1))));
+          uint32_t x[2][4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t x0 = k ? v[2 * i] >> 8 : v[2 * i], x1 = k ? v[2 * i + 1] >> 8 : v[2 * i + 1];
-          x[k][0] = low_codes(x0);
-          x[k][1] = high_codes(x0);
-          x[k][2] = low_codes(x1);
-          x[k][3] = high_codes(x1);
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t x0 = k ? v[2 * i] >> 8 : v[2 * i], x1 = k ? v[2 * i + 1] >> 8 : v[2 * i + 1];
+            x[k][0] = low_codes(x0);
+            x[k][1] = high_codes(x0);
+            x[k][2] = low_codes(x1);
+            x[k][3] = high_codes(x1);
+          }
+          if constexpr (decltype(in_place)::value) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) mma(acc[b][k], x[k][0], x[k][1], x[k][2], x[k][3], wh0, wh1);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) mma(acc[b][k], x[k][0], x[k][1], x[k][2], x[k][3], wl0, wl1);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float c[4];
+              mma0(c, x[k][0], x[k][1], x[k][2], x[k][3], wh0, wh1);
+              mma(c, x[k][0], x[k][1], x[k][2], x[k][3], wl0, wl1);
+              fma2(acc[b][k][0], acc[b][k][1], fac[0], fac[1], c[0], c[1]);
+              fma2(acc[b][k][2], acc[b][k][3], fac[0], fac[1], c[2], c[3]);
+            }
+          }
         }
-        mma(acc[b][0], x[0][0], x[0][1], x[0][2], x[0][3], wh0, wh1);
-        mma(acc[b][1], x[1][0], x[1][1], x[1][2], x[1][3], wh0, wh1);
-        mma(acc[b][0], x[0][0], x[0][1], x[0][2], x[0][3], wl0, wl1);
-        mma(acc[b][1], x[1][0], x[1][1], x[1][2], x[1][3], wl0, wl1);
       }
+    };
+    if (near) {
+      add(std::true_type{});
+    } else {
+      const float back = exp2f((float)(wexp - vexp));
+      fac[0] *= back, fac[1] *= back;
+      add(std::false_type{});
     }
   }
   asm volatile("cp.async.wait_all;\n" ::: "memory");
