@@ -186,8 +186,8 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
   // ---- the query fragments, column gid = head gid (an input: read before the
   // wait).  Block b, step s: k index 2 l4 + {0, 1} is dim 32 b + 4 l4 + s + {0, 2},
   // k index 8 + 2 l4 + {0, 1} the dim 16 further (divided by 16).  A power of
-  // two per head brings its largest query to [2^6, 2^7) first, so that small
-  // queries keep their bits through that division.
+  // two per head brings its largest query to [2^14, 2^15) first, so that the
+  // others keep their bits through that division down to 2^-24 of it.
   float scale[2];   // of heads 2 l4, 2 l4 + 1's scores, to the log2 domain: without the queries' power of two
   {
     const __half* q = a.q + ((int64_t)t * Hq + g * kGqa + gid) * kHeadDim;
@@ -206,7 +206,7 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
     }
     qmax = __hmax2(qmax, half2_of(__shfl_xor_sync(kFull, bits(qmax), 1)));
     qmax = __hmax2(qmax, half2_of(__shfl_xor_sync(kFull, bits(qmax), 2)));
-    const int e = 21 - (int)((bits(__hmax2(qmax, __lowhigh2highlow(qmax))) & 0x7fffu) >> 10);   // -10 .. 21
+    const int e = 29 - (int)((bits(__hmax2(qmax, __lowhigh2highlow(qmax))) & 0x7fffu) >> 10);   // -2 .. 29
     const int e0 = min(e, 15);
     const __half2 up0 = pow2h(e0), up1 = pow2h(e - e0), sixteenth = __float2half2_rn(0.0625f);
     const float mine = a.attn_scale * 1.4426950408889634f * exp2f((float)-e);

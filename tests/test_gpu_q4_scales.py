@@ -105,3 +105,18 @@ def test_scales_over_the_whole_range(T):
     _check(k, v, q, [rng.permutation(1000)[:700] for _ in range(T)])
     v = rng.standard_normal((1000, 2, 256)) * 1e-6     # subnormal scales only
     _check(k, v, q, [rng.permutation(1000)[:700] for _ in range(T)])
+
+
+@pytest.mark.parametrize("down", [12, 16, 20])
+def test_queries_of_large_and_small_dims(down):
+    """One block of a head's queries 2^down times as large as the others, the keys the other way round: both
+    parts count alike in the scores.  With the largest query brought to 2^14 the others lie, divided by 16,
+    around 2^(10 - down) or above: at down = 20 some 4 % of them are subnormal halves, off by at most 2^-25,
+    2^-15 of their deviation, which moves a score by less than 2e-6."""
+    rng, k, v = _rows(down, 1500)
+    big = np.s_[..., 160:192]
+    q = rng.standard_normal((2, 16, 256)) * 2.0 ** (14 - down)
+    q[big] = rng.standard_normal((2, 16, 32)) * 2.0 ** 13
+    k *= 2.0 ** (down - 14)
+    k[big] = rng.standard_normal((1500, 2, 32)) * 2.0 ** -13
+    _check(k, v, q.astype(np.float16), [np.arange(1500), rng.permutation(1500)[:33]])
