@@ -417,11 +417,12 @@ uint32_t qsa_index_attn_kernels(const qsa_config* cfg, int32_t n_tokens, int32_t
  * reduced exactly in integers; each output is rounded once.
  *
  * qsa_rope describes the rotation of the 256-dim heads: qsa_rope_init fills it
- * on the host, once, for a configuration (it depends on rope_theta), and calls
- * take it by reference.  sections[a], a < n_axes <= 4: how many pairs turn by
- * axis a's position (time, height, width, ...); n_rot = 2 * their sum, which
- * must be a multiple of 8 (QSA_ERR_UNSUPPORTED) and at most head_dim / 2
- * (QSA_ERR_SHAPE).  interleaved = 0: axis 0's pairs come first, then axis 1's,
+ * on the host, once, for a configuration, and calls take it by reference; one of
+ * another rope_theta than the call's is refused (QSA_ERR_INVALID_ARG), as the
+ * block keys turn by the configuration's.  sections[a], a < n_axes <= 4: how
+ * many pairs turn by axis a's position (time, height, width, ...); n_rot = 2 *
+ * their sum, which must be a multiple of 8 (QSA_ERR_UNSUPPORTED) and at most
+ * head_dim / 2 (QSA_ERR_SHAPE).  interleaved = 0: axis 0's pairs come first, then axis 1's,
  * and so on; 1: pair i goes to axis i mod n_axes while that axis has pairs left
  * (i / n_axes < sections[axis]) and to axis 0 otherwise (QSA_ERR_SHAPE if an
  * axis past the first would not get its number).
@@ -438,6 +439,7 @@ uint32_t qsa_index_attn_kernels(const qsa_config* cfg, int32_t n_tokens, int32_t
 typedef struct {
   uint32_t magic;             /* set by qsa_rope_init */
   int32_t n_rot, n_axes;
+  float rope_theta;           /* the configuration's */
   uint8_t axis[128];          /* of each pair */
   uint64_t turns[128];        /* theta^(-2i/n_rot) / (2 pi) * 2^64 */
   uint64_t idx_turns[64];     /* the same for the idx_dim dims of q_idx */

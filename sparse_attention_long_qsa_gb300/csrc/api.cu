@@ -383,6 +383,7 @@ qsa_status qsa_rope_init(const qsa_config* cfg, int32_t n_axes, const int32_t* s
   o.magic = kRopeMagic;
   o.n_rot = (int32_t)(2 * pairs);   // a multiple of 16: a lane's 8 dims have one partner lane
   o.n_axes = n_axes;
+  o.rope_theta = cfg->rope_theta;
   if (interleaved == 0) {
     int i = 0;
     for (int a = 0; a < n_axes; ++a)
@@ -411,6 +412,7 @@ qsa_status qsa_qk_norm_rope(const qsa_config* cfg, const qsa_rope* rope, int32_t
   if (rope == nullptr || rope->magic != kRopeMagic || rope->n_rot < 0 || rope->n_rot > kHeadDim ||
       rope->n_rot % 16 != 0 || rope->n_axes < 1 || rope->n_axes > 4 || n_tokens < 0)
     return QSA_ERR_INVALID_ARG;
+  if (rope->rope_theta != cfg->rope_theta) return QSA_ERR_INVALID_ARG;   // the block keys turn by the latter
   for (int i = 0; i < rope->n_rot / 2; ++i)
     if (rope->axis[i] >= rope->n_axes) return QSA_ERR_INVALID_ARG;
   if (in_type != QSA_ELEM_F16 && in_type != QSA_ELEM_BF16 && in_type != QSA_ELEM_F32) return QSA_ERR_INVALID_ARG;

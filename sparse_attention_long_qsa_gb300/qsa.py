@@ -60,7 +60,8 @@ class Config(ctypes.Structure):
 class Rope(ctypes.Structure):
     """The rotation of the 256-dim heads (qsa_rope); made by rope_config."""
     _fields_ = [("magic", ctypes.c_uint32), ("n_rot", ctypes.c_int32), ("n_axes", ctypes.c_int32),
-                ("axis", ctypes.c_uint8 * 128), ("turns", ctypes.c_uint64 * 128), ("idx_turns", ctypes.c_uint64 * 64)]
+                ("rope_theta", ctypes.c_float), ("axis", ctypes.c_uint8 * 128), ("turns", ctypes.c_uint64 * 128),
+                ("idx_turns", ctypes.c_uint64 * 64)]
 
 
 _lib = None
@@ -403,7 +404,8 @@ def rope_config(sections, interleaved: bool = False, cfg: Optional[Config] = Non
     """The rotation qk_norm_rope applies to the query and key heads, made once
     per model: sections[a] pairs of dims turn by position axis a, dealt to the
     axes one after the other or (interleaved) in turn; 2 * sum(sections) dims
-    of a head are rotated.  cfg: whose rope_theta (default config())."""
+    of a head are rotated.  cfg: whose rope_theta (default config()); a call
+    with a configuration of another rope_theta refuses the table."""
     sec = [int(x) for x in sections]
     r = Rope()
     c = config() if cfg is None else cfg
