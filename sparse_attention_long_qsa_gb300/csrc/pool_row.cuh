@@ -15,32 +15,24 @@
 // the device (fp64 is a small fraction of fp32 throughput on this part).
 #pragma once
 
-#include <cmath>
-
 #include "qsa_internal.cuh"
 
 namespace qsa {
 
 constexpr int kMaxR = 8;     // compress_ratio limit of the library
 
-// Rotation frequencies as exact fixed-point fractions of a turn:
-// turns[d] = round(theta^(-2d/128) / (2*pi) * 2^64).  For an integer position
+// Rotation frequencies as exact fixed-point fractions of a turn, less whole
+// turns: turns[d] = round(theta^(-2d/128) / (2*pi) * 2^64) mod 2^64 (turn_of, as
+// for the indexer queries, which have to turn alike).  For an integer position
 // p, the low 64 bits of p * turns[d] are the angle's fractional turn (the
 // integer multiply wraps modulo one turn exactly), accurate to p * 2^-64 turns.
 struct Turns {
   unsigned long long f[kIdxDim / 2];
 };
 
-// f_d = theta^(-2d/128) in double (as the method's definition computes it),
-// then its fraction of a turn in long double, scaled to 2^64.
 inline Turns make_turns(float theta) {
   Turns turns{};
-  const long double two_pi = 6.28318530717958647692528676655900577L;
-  for (int d = 0; d < kIdxDim / 2; ++d) {
-    const double f = std::pow((double)theta, (-2.0 * (double)d) / (double)kIdxDim);
-    const long double x = ((long double)f / two_pi) * 18446744073709551616.0L;   // * 2^64
-    turns.f[d] = x >= 18446744073709551615.0L ? ~0ull : (unsigned long long)(x + 0.5L);
-  }
+  for (int d = 0; d < kIdxDim / 2; ++d) turns.f[d] = turn_of(theta, (-2.0 * d) / (double)kIdxDim);
   return turns;
 }
 
