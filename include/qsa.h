@@ -503,8 +503,8 @@ qsa_status qsa_seq_fork(const qsa_config* cfg, int32_t n_fork, const int32_t* sr
                         int64_t max_blocks, int32_t* copy_src, int32_t* copy_dst, qsa_stream_t stream);
 
 /* qsa_cache_sweep: what the sequences still hold, and the rest freed.
- * Sequence s holds positions 0 .. seq_len[s] - 1 (<= 0: none; past its list:
- * what the list has, flagged).  A slot is held if a sequence's list names it for
+ * Sequence s holds positions 0 .. seq_len[s] - 1 (<= 0: none; past its list, or
+ * a list past n_list: what is there, flagged).  A slot is held if a sequence's list names it for
  * a block that starts before seq_len; a cell is held if a held position's table
  * entry names it.  Freeing or rolling back a sequence is therefore a smaller
  * seq_len; shared blocks stay while anyone holds them.  Writes

@@ -267,8 +267,9 @@ __device__ __forceinline__ SweepEntry sweep_entry(const SweepArgs& a, const Swee
   SweepEntry r;
   r.slot = -1;
   r.held = 0;
-  if (e < a.n_seq) {   // a length that its list cannot hold
-    if (q.len[e] > 0 && (q.len[e] + (int64_t)a.r - 1) / a.r > q.off[e + 1] - q.off[e]) atomicOr(err, kErrBlockList);
+  if (e < a.n_seq) {   // a length that its list, as far as it is there, cannot hold
+    const int64_t end = q.off[e + 1] < a.n_list ? q.off[e + 1] : a.n_list;
+    if (q.len[e] > 0 && (q.len[e] + (int64_t)a.r - 1) / a.r > end - q.off[e]) atomicOr(err, kErrBlockList);
   }
   if (e >= q.lists || e < q.off[0]) return r;
   int lo = 0, hi = a.n_seq;                   // the last sequence whose list starts at or before e
