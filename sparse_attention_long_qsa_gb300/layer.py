@@ -184,16 +184,15 @@ class QSALayer:
 
     def fork(self, src_seq, dst_seq, n_pos, tail_slot, tail_cells, stream=None):
         """Sequence dst_seq[f] becomes the first n_pos[f] positions of
-        src_seq[f] (int32 CUDA tensors; tail_cells [n_fork][r]): the block
-        lists and tables, and this layer's rows of the private tail cells.
+        src_seq[f] (int32 CUDA tensors; tail_cells [n_fork][r]; at most the
+        layer's max_blocks whole blocks, as for the steps): the block lists and
+        tables, and this layer's rows of the private tail cells.
         Returns the (source, destination) cell pairs, for other layers."""
         n, r = int(src_seq.numel()), self.cfgd["compress_ratio"]
         with _on(stream):
             pairs = torch.empty((2, n, r), dtype=torch.int32, device=self.device)
-        # the lists bound every sequence's blocks
         qsa.seq_fork(self.cfg, src_seq, dst_seq, n_pos, tail_slot, tail_cells, self.seq_blk_off, self.seq_blk_slots,
-                     self.blk_cells, self.slot_block_idx, int(self.seq_blk_slots.numel()), pairs[0], pairs[1],
-                     self.n_cells, stream)
+                     self.blk_cells, self.slot_block_idx, self.max_blocks, pairs[0], pairs[1], self.n_cells, stream)
         qsa.cells_copy(self.cfg, pairs[0], pairs[1], self.k_cache, self.v_cache, self.idx_k, self.n_cells,
                        stream=stream)
         return pairs[0], pairs[1]
