@@ -31,10 +31,12 @@
 //          apart  weights relative to the chunk's own largest, summed in an
 //                 accumulator of its own, which is added with the chunk's factor
 //                 in fp32 (2^-22)
-//          wild   scales of V in the chunk more than 2^10 apart, zero, subnormal
-//                 or infinite: products in fp32, cell by cell
-//        512 tokens at 250k cells take 146 us so; 151 with every chunk apart; 140
-//        with weights relative to the warp's largest throughout, but then one
+//          wild   scales of V in the chunk more than 2^10 apart, subnormal, zero
+//                 for some of the cells only, or infinite: products in fp32, cell
+//                 by cell
+//        512 tokens at 250k cells take 147 us so (156 with scales or scores that
+//        set most chunks apart, 606 with all of them wild); 151 without the near
+//        form; 140 with weights relative to the warp's largest throughout, but then one
 //        cell or block of large values, however unlikely, cost all others their
 //        bits (5e-4 of a block's norm at a ratio of 3,000, a tenth of it at 1e6).
 //
@@ -357,7 +359,11 @@ k_attn_q4(const AttnArgs a, unsigned* err) {
       dn = e | (e << 16);
     }
     const uint32_t dtop = __reduce_max_sync(kFull, max(dx >> 16, dx & 0xffffu));
-    const uint32_t dbot = __reduce_min_sync(kFull, min(dn >> 16, dn & 0xffffu));
+    uint32_t dbot = __reduce_min_sync(kFull, min(dn >> 16, dn & 0xffffu));
+    if (dbot == 0u) {   // a block that is zero in all of the chunk's cells (dims of padding) takes nothing from the others
+      const bool zeros = ((__ballot_sync(kFull, dx == 0u) >> (lane & 28)) & 15u) == 15u;
+      dbot = __reduce_min_sync(kFull, zeros ? 0x7bffu : min(dn >> 16, dn & 0xffffu));
+    }
     const bool plain = dbot >= 0x0400u && dtop < 0x7c00u && dtop <= dbot + kSpread;
     int vexp = plain ? 13 - (int)(dtop >> 10) : 0;   // brings the chunk's largest scale to [2^-2, 2^-1)
     const int nexp = min(wexp, vexp);                // the warp's

@@ -120,3 +120,30 @@ def test_queries_of_large_and_small_dims(down):
     k *= 2.0 ** (down - 14)
     k[big] = rng.standard_normal((1500, 2, 32)) * 2.0 ** -13
     _check(k, v, q.astype(np.float16), [np.arange(1500), rng.permutation(1500)[:33]])
+
+
+@pytest.mark.parametrize("T", [1, 200])
+@pytest.mark.parametrize("blocks", [[0], [6, 7], list(range(8))])
+def test_blocks_of_zeros_in_every_cell(T, blocks):
+    """Dims of padding: exact zeros there, the other blocks as without them; and one cell of the list that is
+    zero throughout."""
+    rng, k, v = _rows(17 + T, 1000)
+    v.reshape(1000, 2, 8, 32)[:, :, blocks] = 0
+    v[500] = 0
+    q = rng.standard_normal((T, 16, 256)).astype(np.float16)
+    _check(k, v, q, [rng.permutation(1000)[:701] for _ in range(T)])
+
+
+@pytest.mark.parametrize("top", [1.0, 2.0 ** -8, 2.0 ** -11, 2.0 ** -13, 2.0 ** -14, 2.0 ** -15, 2.0 ** -18])
+@pytest.mark.parametrize("ratio", [2.0 ** 5, 2.0 ** 9, 2.0 ** 11, 2.0 ** 13])
+def test_scales_around_the_forms_limits(top, ratio):
+    """Scales spread over a ratio below a largest one, normal and subnormal, with the likely cells at either end."""
+    rng, k, v = _rows(23, 640)
+    q, u = _alike(rng)
+    f = np.exp2(-rng.uniform(0, np.log2(ratio), (640, 2, 8)))
+    f[::16], f[5::16] = 1.0, 1.0 / ratio             # both ends in every chunk
+    v *= (f * top * 3).repeat(32, axis=-1)
+    for sign in (-0.5, 0.5):
+        kk = k.copy()
+        kk[5::16] += sign * u
+        _check(kk, v, q, [np.arange(640)])
