@@ -20,7 +20,6 @@ from gpu_util import assert_no_device_errors, to_np
 
 pytestmark = pytest.mark.gpu
 TOL = 2e-5
-CFG = default_cfg(kv_type="q4_0")
 
 
 def _pack(x):
@@ -28,10 +27,11 @@ def _pack(x):
     return np.concatenate([codes.reshape(-1), d.reshape(-1).view(np.uint8)])
 
 
-def _check(k, v, q, lists):
+def _check(k, v, q, lists, scale=1.0 / 16.0):
     """k, v: fp32 rows [n][2][256]; q fp16 [T][16][256]."""
     n, T = len(k), len(lists)
-    kc, vc, cfg = _pack(k), _pack(v), qsa.config(kv_type="q4_0")
+    kc, vc, cfg = _pack(k), _pack(v), qsa.config(kv_type="q4_0", attn_scale=scale)
+    plain = default_cfg(kv_type="q4_0", attn_scale=scale)
     cells = np.full((T, qsa.cells_per_token(cfg)), -1, np.int32)
     for t, c in enumerate(lists):
         cells[t, :len(c)] = c
@@ -39,10 +39,11 @@ def _check(k, v, q, lists):
     qsa.sparse_attn(cfg, torch.from_numpy(q).cuda(), torch.from_numpy(kc).cuda(), torch.from_numpy(vc).cuda(), n,
                     torch.from_numpy(cells).cuda(), torch.tensor([len(c) for c in lists], dtype=torch.int32, device="cuda"),
                     out)
-    ref = np.stack([O.attend(CFG, q[t], kc, vc, n, np.asarray(lists[t])) for t in range(T)])
+    ref = np.stack([O.attend(plain, q[t], kc, vc, n, np.asarray(lists[t])) for t in range(T)])
     err = np.linalg.norm((to_np(out) - ref).reshape(T, 16, 8, 32), axis=-1)
     size = np.linalg.norm(ref.reshape(T, 16, 8, 32), axis=-1)
-    assert np.all(err <= TOL * size), np.max(err / size, axis=(0, 1))
+    tol = TOL * max(1.0, 16 * abs(scale))   # a score's error grows with the scale
+    assert np.all(err <= tol * size), np.max(err / size, axis=(0, 1))
     assert_no_device_errors()
 
 
@@ -147,3 +148,12 @@ def test_scales_around_the_forms_limits(top, ratio):
         kk = k.copy()
         kk[5::16] += sign * u
         _check(kk, v, q, [np.arange(640)])
+
+
+@pytest.mark.parametrize("scale", [0.0, -1.0 / 16.0, 1.0 / 256.0, 0.5])
+@pytest.mark.parametrize("T", [1, 200])
+def test_attention_scales(T, scale):
+    """From all cells alike to one or two that count (a chunk's likeliest cells 2^100 apart)."""
+    rng, k, v = _rows(31 + T, 900)
+    q = rng.standard_normal((T, 16, 256)).astype(np.float16)
+    _check(k, v, q, [rng.permutation(900)[:650 + t % 50] for t in range(T)], scale)
