@@ -1,12 +1,14 @@
 """qsa_qk_norm_rope against the 64-bit definition.
 
 Tolerance of one output (derived from the fp32 steps, u = 2^-24):
-  sum of 256 squares by lanes of 8 and 5 shuffle levels: relative 13u, halved
-  by the root; division, root, two products: 4u; the rotated pair: cos and sin
-  each off by at most 2^-22 (sincospif's 2 ulp, the angle itself is exact to
-  2^-60 turns), two products and a sum: 3u more.  In all below 2^-20 of
-  |y_i| + |y_partner|.  fp16 outputs add half a step: 2^-11 of the value, or
-  2^-25 where fp16 is subnormal."""
+  a lane's 8 squares in two chains of four, their sum and 5 shuffle levels:
+  relative 10u, halved by the root; eps 0.5u; rsqrtf's 2 ulp: 4u; the products
+  with weight, partner and root: 4u.  In all 13.5u of |y_i cos| + |y_p sin|.
+  Sine and cosine of |x| <= pi/4, a Taylor series to below 2e-9: x is off by 3u
+  of itself (conversion, constant, product) and the angle by 2^-32 of a turn,
+  the last steps by 1u: 2.7u at pi/4, where the first part is 0.71 of its
+  largest, and 0.5u at 0.  In all below 15u < 2^-20 of |y_i| + |y_p|.  fp16
+  outputs add half a step: 2^-11 of the value, or 2^-25 where fp16 is subnormal."""
 import numpy as np
 import pytest
 import torch
