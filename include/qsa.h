@@ -340,9 +340,8 @@ qsa_status qsa_sparse_attn(const qsa_config* cfg, int32_t n_tokens,
  * tiles hold other cells, so the fp16 rounding of the probabilities and the
  * order of the sums differ (both within 2e-3 max-relative of the exact
  * result for fp16 K/V, 5e-3 for q8_0).  cells_pitch (top_k + r - 1)
- * must be at most 4104, else QSA_ERR_UNSUPPORTED; so does a q4_0 cache (its
- * rows are small enough that gathering them twice costs less than the union).
- * Needs no workspace. */
+ * must be at most 4104, else QSA_ERR_UNSUPPORTED; a q4_0 cache is
+ * QSA_ERR_UNSUPPORTED too (its kernel has no union form).  Needs no workspace. */
 qsa_status qsa_sparse_attn_union(const qsa_config* cfg, int32_t n_tokens,
                                  const void* q, const void* k_cache, const void* v_cache,
                                  int64_t n_cells, const int32_t* cells, const int32_t* count,
@@ -414,7 +413,7 @@ uint32_t qsa_index_attn_kernels(const qsa_config* cfg, int32_t n_tokens, int32_t
  * [T][n_kv_heads][head_dim]; q_idx as fp32 [T][n_idx_heads][idx_dim], all its
  * idx_dim dims rotated by idx_pos[t] (the cache position that the block keys
  * are rotated by), whatever `rope` says.  Arithmetic is fp32 with the angle
- * reduced exactly in integers; each output is rounded once.
+ * reduced in integers, to 2^-32 of a turn; each output is rounded once.
  *
  * qsa_rope describes the rotation of the 256-dim heads: qsa_rope_init fills it
  * on the host, once, for a configuration, and calls take it by reference; one of

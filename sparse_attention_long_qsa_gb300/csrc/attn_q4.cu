@@ -5,13 +5,14 @@
 //   out[h] = sum_c softmax_c(scale * q_h . K_c) V_c,   K_c[i] = d_K[c][i/32] (n_K[c][i] - 8)
 //
 // A row is 128 bytes of codes and 16 bytes of scales, a quarter of its fp16
-// form.  Writing the expanded rows to shared memory for a tcgen05 operand and
-// reading them back costs 1 KB + 1 KB of shared-memory traffic per cell and
-// head (about 2,000 cycles per 128 cells on an SM), several times the gather
-// itself, and the tensor core would use 8 of the 16 columns it needs at least.
-// mma.sync takes its operands from registers: ldmatrix hands each thread
-// exactly the nibbles of its fragment, and two instructions make two of them
-// fp16 operands.
+// form.  mma.sync takes its operands from registers: ldmatrix hands each thread
+// exactly the nibbles of its fragment, and two instructions make two of them fp16
+// operands.  (A code put under the exponent of 1024 is 1024 + code: published for
+// int4 weights by Kim et al., "Who Says Elephants Can't Run", 2022.)  A tcgen05
+// operand in shared memory would be written and read back expanded, 1 KB each a
+// cell and head, some 2,000 cycles per 128 cells on an SM, where all of this
+// kernel takes 2,550.  Codes stored to tensor memory as the A operand would not
+// pay that; such a form is not built.
 //
 // Both products are exact in their codes; no K or V value is ever rounded:
 //   Q.K  per 32-value block with integer codes, the block's sum then scaled by
@@ -34,11 +35,12 @@
 //          wild   scales of V in the chunk more than 2^10 apart, subnormal, zero
 //                 for some of the cells only, or infinite: products in fp32, cell
 //                 by cell
-//        512 tokens at 250k cells take 147 us so (156 with scales or scores that
-//        set most chunks apart, 606 with all of them wild); 151 without the near
-//        form; 140 with weights relative to the warp's largest throughout, but then one
-//        cell or block of large values, however unlikely, cost all others their
-//        bits (5e-4 of a block's norm at a ratio of 3,000, a tenth of it at 1e6).
+//        512 tokens at 250k cells take 147 us so (156 to 158 with scales or scores
+//        that set most chunks apart, 606 with all of them wild), and 151 with the
+//        apart form for every chunk that is not wild.  Weights relative to the
+//        warp's largest throughout take 140, but one cell or block of large
+//        values, however unlikely, then costs all others their bits (5e-4 of a
+//        block's norm at a ratio of 3,000, a tenth of it at 1e6).
 //
 // Work split.  A warp takes 16 cells at a time: it copies their rows with
 // cp.async into its own ring of stages (kStages - 1 chunks in flight), forms

@@ -318,7 +318,7 @@ def index_attn(cfg, q_idx, w_idx, tok_seq, tok_pos, pooled, blk_cells, seq_blk_o
     """qsa_index_topk then qsa_sparse_attn in one call (same workspace and
     hint as index_topk); fills cells, count and out.  in_cluster: the
     selection runs inside the attention clusters where the call's limits
-    allow (QSA_INDEX_ATTN_IN_CLUSTER); union: token pairs attend over the
+    allow (QSA_INDEX_ATTN_IN_CLUSTER; never for a q4_0 cache); union: token pairs attend over the
     union of their lists (QSA_INDEX_ATTN_UNION)."""
     import torch
     T = int(tok_pos.numel())
@@ -526,7 +526,8 @@ def seq_fork(cfg, src_seq, dst_seq, n_pos, tail_slot, tail_cells, seq_blk_off, s
     """Sequence dst_seq[f] becomes the first n_pos[f] positions of src_seq[f]:
     whole blocks shared, a partial last block private (tail_slot[f],
     tail_cells[f]); copy_src / copy_dst [n_fork][r] get the pairs for
-    cells_copy."""
+    cells_copy.  n_cells: the cache's cells; tail cells at or past it are
+    flagged here (without it only by the calls that use them)."""
     torch, dev, i32 = _torch_dev()
     n, r, n_slots = src_seq.numel(), cfg.compress_ratio, blk_cells.shape[0]
     if not (dst_seq.numel() == n_pos.numel() == tail_slot.numel() == n
