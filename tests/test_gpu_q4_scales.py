@@ -4,8 +4,8 @@ an output measured by its own size.
 Tolerance 2e-5 of a block's norm: as for rows of equal scales, a cell's score is
 off by the rounding of some 270 fp32 additions, so its probability by a relative
 1.6e-5 at four standard deviations, and the errors of different cells are
-independent; the weights and sums behind it keep at least 21 bits of what they
-add to a block.  A block's norm over 32 dims and the sum over cells average these
+independent; the weights behind it lose at most 2^-18 (4e-6) of what a chunk of
+cells adds to a block.  A block's norm over 32 dims and the sum over cells average these
 errors, and the values of different cells are independent, so that a block's
 norm is not the remainder of a cancellation."""
 import numpy as np
