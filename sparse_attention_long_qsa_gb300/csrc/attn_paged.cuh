@@ -317,6 +317,15 @@ __device__ __forceinline__ int checked_cell(const PagedArgs& a, int c, bool repo
   return -1;
 }
 
+// Adds those of two halves that are infinite or NaN to (x, y).
+__device__ __forceinline__ void add_not_finite(float& x, float& y, uint32_t w) {
+  __half2 h;
+  memcpy(&h, &w, 4);
+  const float2 v = __half22float2(h);
+  if (!isfinite(v.x)) x += v.x;
+  if (!isfinite(v.y)) y += v.y;
+}
+
 // Adds the runs of a group that is spread over several parts.  Entries per token: a
 // block is a token and head; four dims a thread, every eighth part, the first of these
 // loaded with the parts' (max, sum), so that a row costs one wait for memory.  Entries

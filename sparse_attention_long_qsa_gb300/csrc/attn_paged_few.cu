@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(KV == QSA_KV_F16 ? 896 : 768, 1) k_paged_few(c
           if (begins) {   // the sums of the stretch before, of the reference before
             if (!mbar_wait(bpv + 8 * (b ^ 1), (uint32_t)((base + i - 1) >> 1) & 1u)) timed_out = true;
             tc_fence_after();
-            write_rows(tl + 128 * half, sm.out[warp], 1.f, sums, kGqa * kHeadDim, i > stretch ? sums : nullptr, fs, 32 * quarter, gr.nt,
+            write_rows<false>(tl + 128 * half, sm.out[warp], 1.f, sums, kGqa * kHeadDim, i > stretch ? sums : nullptr, fs, 32 * quarter, gr.nt,
                        [](int, uint32_t (&)[16]) {});
             fs = 1.f;
             next += stretch;
@@ -394,33 +394,32 @@ __global__ void __launch_bounds__(KV == QSA_KV_F16 ? 896 : 768, 1) k_paged_few(c
       }
       const float w = whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
       float* rows = whole ? a.out + ((int64_t)gr.t0 * G + g) * kGqa * kHeadDim + 128 * half : sums;
-      const bool stray = mine && *reinterpret_cast<volatile unsigned*>(&sm.stray[runs & 7]) != 0u;
-      write_rows(tl + 128 * half, sm.out[warp], w, rows, (whole ? G : 1) * (kGqa * kHeadDim), stretch < n ? sums : nullptr, fs,
+      const bool stray = *reinterpret_cast<volatile unsigned*>(&sm.stray[runs & 7]) != 0u;   // (one value for the warp)
+      write_rows<false>(tl + 128 * half, sm.out[warp], w, rows, (whole ? G : 1) * (kGqa * kHeadDim), stretch < n ? sums : nullptr, fs,
                  32 * quarter, gr.nt,
                  [&](int k, uint32_t (&o)[16]) {
         if (!stray) return;
-#pragma unroll 1
-        for (int v = v_first; v < min(gr.nv, v_first + n * kCells); ++v) {
-          const int p = pos_of(gr, v);
-          if (p > pos || (a.window > 0 && p <= pos - a.window && p >= a.n_sink)) continue;
-          const int c = cell_at(a, run, v, slot_at(a, run, v, gr.nv, false, err), false, err);
-          if (c < 0 || c >= a.n_cells) continue;
-          if constexpr (kF16) {
-            const __half* x = static_cast<const __half*>(a.v_cache) + ((int64_t)c * G + g) * kHeadDim + 128 * half + 16 * k;
+        float y[16] = {};
+        add_not_finite_seen(
+            a, run, v_first, min(gr.nv, v_first + n * kCells), y,
+            [&](int p) { return p <= pos && (a.window == 0 || p > pos - a.window || p < a.n_sink); },
+            [&](int c, uint32_t (&x)[8]) {
+              if constexpr (kF16) {
+                const uint4* from = reinterpret_cast<const uint4*>(static_cast<const __half*>(a.v_cache) +
+                                                                   ((int64_t)c * G + g) * kHeadDim + 128 * half + 16 * k);
+                const uint4 lo = from[0], hi = from[1];
+                x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w, x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
+              } else {
+                const unsigned short* d = reinterpret_cast<const unsigned short*>(static_cast<const unsigned char*>(a.v_cache) +
+                                                                                  a.n_cells * (int64_t)(G * kCodes));
+                if ((d[((int64_t)c * G + g) * 8 + 4 * half + (k >> 1)] & 0x7fffu) >= Row<KV>::kLimit) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float y = __half2float(x[j]);
-              if (!isfinite(y)) o[j] = __float_as_uint(__uint_as_float(o[j]) + y);
-            }
-          } else {
-            const unsigned short* d = reinterpret_cast<const unsigned short*>(static_cast<const unsigned char*>(a.v_cache) +
-                                                                              a.n_cells * (int64_t)(G * kCodes));
-            if ((d[((int64_t)c * G + g) * 8 + 4 * half + (k >> 1)] & 0x7fffu) >= Row<KV>::kLimit) {
+                  for (int j = 0; j < 8; ++j) x[j] = 0x7fff7fffu;
+                }
+              }
+            });
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] = 0x7fffffffu;
-            }
-          }
-        }
+        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) + y[j]);
       });
       tc_fence_before();
     });

@@ -28,8 +28,8 @@
 // A cell that some tokens of the group do not see may hold infinities or NaN, and a
 // probability of zero would not keep them out.  In tiles at the edge of what the
 // group sees, V values that are not finite are therefore taken out of shared memory
-// before the product, and what they do to the rows that see them is added when the
-// run's result is written.
+// before the product.  Where a run's result is not finite, or such values were taken
+// out, those that the row sees are added up in its place.
 //
 // The two parts of P cost a half more than one would (3,072 instead of 2,048 tensor
 // cycles a tile): the output is fp32, and one part would leave it 2e-4 off.
@@ -220,6 +220,7 @@ __global__ void __launch_bounds__(640, 1) k_paged_prompt(const PagedArgs a, unsi
       const int stretch = stretch_of(n, kAdditions);
       int next = stretch;   // where the next one begins
       float fs = 0.f;       // of the stretches' sums so far
+      bool odd = false;     // some of them are not finite
       float m = kNoMax, l = 0.f;   // the row's reference, and this half's sum relative to it
       for (int i = 0; i < n; ++i) {
         const int b = (base + i) & 1;
@@ -323,8 +324,8 @@ __global__ void __launch_bounds__(640, 1) k_paged_prompt(const PagedArgs a, unsi
         if (begins) {   // the sums of the stretch before, of the reference before
           if (!mbar_wait(bpv + 8 * (b ^ 1), (uint32_t)((base + i - 1) >> 1) & 1u)) timed_out = true;
           tc_fence_after();
-          write_rows(tl + 128 * half, sm.out[warp], 1.f, sums, kGqa * kHeadDim, i > stretch ? sums : nullptr, fs,
-                     128 * rank + 32 * quarter, gr.nt, [](int, uint32_t (&)[16]) {});
+          write_rows<false>(tl + 128 * half, sm.out[warp], 1.f, sums, kGqa * kHeadDim, i > stretch ? sums : nullptr, fs,
+                            128 * rank + 32 * quarter, gr.nt, [&](int, uint32_t (&o)[16]) { odd = odd || !all_finite(o); });
           fs = 1.f;
           next += stretch;
         }
@@ -343,25 +344,24 @@ __global__ void __launch_bounds__(640, 1) k_paged_prompt(const PagedArgs a, unsi
       if (tok < gr.nt && !whole && half == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * (ps + tok * kGqa + head)) = make_float2(m, l);
       const float w = whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
       float* rows = whole ? a.out + ((int64_t)gr.t0 * G + g) * kGqa * kHeadDim + 128 * half : sums;
-      const bool stray = tok < gr.nt && *reinterpret_cast<volatile unsigned*>(&sm.stray[runs & 3]) != 0u;
-      write_rows(tl + 128 * half, sm.out[warp], w, rows, (whole ? G : 1) * (kGqa * kHeadDim), stretch < n ? sums : nullptr, fs,
-                 128 * rank + 32 * quarter, gr.nt, [&](int k, uint32_t (&o)[16]) {
-        if (!stray) return;
-        for (int i = 0; i < n; ++i) {
-          if (!edge_tile(gr, a.window, v_first + i * kCells)) continue;
-          for (int v = v_first + i * kCells; v < min(gr.nv, v_first + (i + 1) * kCells); ++v) {
-            const int p = pos_of(gr, v);
-            if (p > pos || (a.window > 0 && p <= pos - a.window && p >= a.n_sink)) continue;
-            const int c = cell_at(a, run, v, slot_at(a, run, v, gr.nv, false, err), false, err);
-            if (c < 0 || c >= a.n_cells) continue;
-            const __half* x = static_cast<const __half*>(a.v_cache) + ((int64_t)c * G + g) * kHeadDim + 128 * half + 16 * k;
+      // infinite values and NaN make the sum of their dim, whatever else it has (the products with a weight's second part, of
+      // zero or below it, have made NaN of them, or they were taken out)
+      odd = odd || *reinterpret_cast<volatile unsigned*>(&sm.stray[runs & 3]) != 0u;
+      write_rows<true>(tl + 128 * half, sm.out[warp], w, rows, (whole ? G : 1) * (kGqa * kHeadDim), stretch < n ? sums : nullptr, fs,
+                       128 * rank + 32 * quarter, gr.nt, [&](int k, uint32_t (&o)[16]) {
+        if (__all_sync(kFull, tok >= gr.nt || l - l != 0.f || (!odd && all_finite(o)))) return;
+        float y[16] = {};
+        add_not_finite_seen(
+            a, run, v_first, min(gr.nv, v_first + n * kCells), y,
+            [&](int p) { return p <= pos && (a.window == 0 || p > pos - a.window || p < a.n_sink); },
+            [&](int c, uint32_t (&x)[8]) {
+              const uint4* from = reinterpret_cast<const uint4*>(static_cast<const __half*>(a.v_cache) +
+                                                                 ((int64_t)c * G + g) * kHeadDim + 128 * half + 16 * k);
+              const uint4 lo = from[0], hi = from[1];
+              x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w, x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
+            });
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float y = __half2float(x[j]);
-              if (!isfinite(y)) o[j] = __float_as_uint(__uint_as_float(o[j]) + y);
-            }
-          }
-        }
+        for (int j = 0; j < 16; ++j) o[j] = y[j] != 0.f ? __float_as_uint(y[j]) : o[j];
       });
       tc_fence_before();
     });

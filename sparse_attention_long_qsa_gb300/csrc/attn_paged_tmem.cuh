@@ -30,8 +30,45 @@ __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
       : "+f"(x), "+f"(y)
       : "f"(a), "f"(b));
 }
+// Whether 16 values are all finite.
+__device__ __forceinline__ bool all_finite(const uint32_t (&o)[16]) {
+  float z = 0.f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) z = fmaf(__uint_as_float(o[j]), 0.f, z);
+  return z == 0.f;
+}
 // bits [0, n) of a word, any n
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+// Adds to y the values that are not finite which a lane's row sees among the run's cells [v, v_end) (reading order), in 16
+// dims.  sees(p): whether the lane's row sees position p.  load(c, x): those dims of cell c, as halves.  By a whole warp, a
+// lane a cell (a chain of three loads), then a lane a row.
+template <typename Sees, typename Load>
+__device__ __forceinline__ void add_not_finite_seen(const PagedArgs& a, const Run& run, int v, int v_end, float (&y)[16], Sees sees,
+                                                    Load load) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (; v < v_end; v += 32) {
+    const int at = v + lane;
+    const int c = checked_cell(a, cell_at(a, run, at, slot_at(a, run, at, v_end, false, nullptr), false, nullptr), false, nullptr);
+    uint32_t x[8] = {}, any = 0u;
+    if (c >= 0) load(c, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) any |= ((x[j] & 0x7c007c00u) + 0x04000400u) & 0x80008000u;   // an exponent of ones
+    unsigned who = __ballot_sync(kFull, any != 0u);
+    const int p = at < v_end ? pos_of(run.g, at) : 0;
+#pragma unroll 1
+    for (; who; who &= who - 1u) {
+      const int l = __ffs((int)who) - 1;
+      const bool s = sees(__shfl_sync(kFull, p, l));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t w = __shfl_sync(kFull, x[j], l);
+        if (s) add_not_finite(y[2 * j], y[2 * j + 1], w);
+      }
+    }
+  }
+}
 
 // The tensor cores cut each sum to 24 bits, and 2,600 additions in place would leave a run's result 4e-5 too small.  So a
 // run is cut into stretches of about 280 additions (5e-6), whose sums are added in fp32 in the run's rows of the workspace.
@@ -44,9 +81,9 @@ __device__ __forceinline__ int stretch_of(int tiles, int additions) {
 // tensor memory, and `old` (if there is one: rows of the same order, 256 values apart) times fs, all times w, to
 // base[token * stride + head * 256].  A warp's stores of a lane a row would touch 32 lines each, so 16 columns at a time
 // pass through shared memory and go out as 64 bytes of eight rows.  fix(k, o): the lane's values of columns
-// 16 k .. + 15 on the way.
+// 16 k .. + 15 on the way.  kWithout: sums in `old` that are not finite are left out.
 constexpr int kOutPitch = 20;
-template <typename Fix>
+template <bool kWithout, typename Fix>
 __device__ __forceinline__ void write_rows(uint32_t taddr, float (*buf)[kOutPitch], float w, float* base, int64_t stride,
                                            const float* old, float fs, int first, int tokens, Fix fix) {
   const int lane = threadIdx.x & 31, col = 4 * (lane & 3), sub = lane >> 2;
@@ -73,7 +110,13 @@ __device__ __forceinline__ void write_rows(uint32_t taddr, float (*buf)[kOutPitc
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (read && i < have) y[i] = __ldcg(reinterpret_cast<const float4*>(from + i * (8 * kHeadDim) + 16 * (k + c)));
+        if (read && i < have) {
+          y[i] = __ldcg(reinterpret_cast<const float4*>(from + i * (8 * kHeadDim) + 16 * (k + c)));
+          if constexpr (kWithout) {
+            y[i].x = isfinite(y[i].x) ? y[i].x : 0.f, y[i].y = isfinite(y[i].y) ? y[i].y : 0.f;
+            y[i].z = isfinite(y[i].z) ? y[i].z : 0.f, y[i].w = isfinite(y[i].w) ? y[i].w : 0.f;
+          }
+        }
       }
       fix(k + c, o[c]);
       __syncwarp();
