@@ -352,8 +352,7 @@ __global__ void __launch_bounds__(KV == QSA_KV_F16 ? 896 : 768, 1) k_paged_few(c
           if (begins) {   // the sums of the stretch before, of the reference before
             if (!mbar_wait(bpv + 8 * (b ^ 1), (uint32_t)((base + i - 1) >> 1) & 1u)) timed_out = true;
             tc_fence_after();
-            write_rows<false>(tl + 128 * half, sm.out[warp], 1.f, sums, kGqa * kHeadDim, i > stretch ? sums : nullptr, fs, 32 * quarter, gr.nt,
-                       [](int, uint32_t (&)[16]) {});
+            write_rows<false>(tl + 128 * half, sm.out[warp], 1.f, sums, kGqa * kHeadDim, i > stretch ? sums : nullptr, fs, 32 * quarter, gr.nt);
             fs = 1.f;
             next += stretch;
           }
@@ -395,15 +394,13 @@ __global__ void __launch_bounds__(KV == QSA_KV_F16 ? 896 : 768, 1) k_paged_few(c
       const float w = whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
       float* rows = whole ? a.out + ((int64_t)gr.t0 * G + g) * kGqa * kHeadDim + 128 * half : sums;
       const bool stray = *reinterpret_cast<volatile unsigned*>(&sm.stray[runs & 7]) != 0u;   // (one value for the warp)
-      write_rows<false>(tl + 128 * half, sm.out[warp], w, rows, (whole ? G : 1) * (kGqa * kHeadDim), stretch < n ? sums : nullptr, fs,
-                 32 * quarter, gr.nt,
-                 [&](int k, uint32_t (&o)[16]) {
-        if (!stray) return;
-        float y[16] = {};
-        add_not_finite_seen(
-            a, run, v_first, min(gr.nv, v_first + n * kCells), y,
+      const int64_t stride = (whole ? G : 1) * (kGqa * kHeadDim);
+      write_rows<false>(tl + 128 * half, sm.out[warp], w, rows, stride, stretch < n ? sums : nullptr, fs, 32 * quarter, gr.nt);
+      if (stray) {
+        put_not_finite(
+            a, run, v_first, min(gr.nv, v_first + n * kCells), mine ? rows + tok * stride + head * kHeadDim : nullptr,
             [&](int p) { return p <= pos && (a.window == 0 || p > pos - a.window || p < a.n_sink); },
-            [&](int c, uint32_t (&x)[8]) {
+            [&](int c, int k, uint32_t (&x)[8]) {
               if constexpr (kF16) {
                 const uint4* from = reinterpret_cast<const uint4*>(static_cast<const __half*>(a.v_cache) +
                                                                    ((int64_t)c * G + g) * kHeadDim + 128 * half + 16 * k);
@@ -418,9 +415,7 @@ __global__ void __launch_bounds__(KV == QSA_KV_F16 ? 896 : 768, 1) k_paged_few(c
                 }
               }
             });
-#pragma unroll
-        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) + y[j]);
-      });
+      }
       tc_fence_before();
     });
   } else if (warp < 16) {

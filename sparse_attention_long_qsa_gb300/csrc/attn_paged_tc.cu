@@ -324,8 +324,8 @@ __global__ void __launch_bounds__(640, 1) k_paged_prompt(const PagedArgs a, unsi
         if (begins) {   // the sums of the stretch before, of the reference before
           if (!mbar_wait(bpv + 8 * (b ^ 1), (uint32_t)((base + i - 1) >> 1) & 1u)) timed_out = true;
           tc_fence_after();
-          write_rows<false>(tl + 128 * half, sm.out[warp], 1.f, sums, kGqa * kHeadDim, i > stretch ? sums : nullptr, fs,
-                            128 * rank + 32 * quarter, gr.nt, [&](int, uint32_t (&o)[16]) { odd = odd || !all_finite(o); });
+          odd |= write_rows<true>(tl + 128 * half, sm.out[warp], 1.f, sums, kGqa * kHeadDim, i > stretch ? sums : nullptr, fs,
+                                  128 * rank + 32 * quarter, gr.nt);
           fs = 1.f;
           next += stretch;
         }
@@ -344,25 +344,24 @@ __global__ void __launch_bounds__(640, 1) k_paged_prompt(const PagedArgs a, unsi
       if (tok < gr.nt && !whole && half == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * (ps + tok * kGqa + head)) = make_float2(m, l);
       const float w = whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
       float* rows = whole ? a.out + ((int64_t)gr.t0 * G + g) * kGqa * kHeadDim + 128 * half : sums;
-      // infinite values and NaN make the sum of their dim, whatever else it has (the products with a weight's second part, of
-      // zero or below it, have made NaN of them, or they were taken out)
+      const int64_t stride = (whole ? G : 1) * (kGqa * kHeadDim);
+      odd |= write_rows<true>(tl + 128 * half, sm.out[warp], w, rows, stride, stretch < n ? sums : nullptr, fs,
+                              128 * rank + 32 * quarter, gr.nt);
+      // (the products of infinite values with a weight's second part, of zero or below it, are NaN; a row whose sum is not
+      // finite is NaN throughout)
       odd = odd || *reinterpret_cast<volatile unsigned*>(&sm.stray[runs & 3]) != 0u;
-      write_rows<true>(tl + 128 * half, sm.out[warp], w, rows, (whole ? G : 1) * (kGqa * kHeadDim), stretch < n ? sums : nullptr, fs,
-                       128 * rank + 32 * quarter, gr.nt, [&](int k, uint32_t (&o)[16]) {
-        if (__all_sync(kFull, tok >= gr.nt || l - l != 0.f || (!odd && all_finite(o)))) return;
-        float y[16] = {};
-        add_not_finite_seen(
-            a, run, v_first, min(gr.nv, v_first + n * kCells), y,
+      if (__any_sync(kFull, odd && tok < gr.nt && l - l == 0.f)) {
+        put_not_finite(
+            a, run, v_first, min(gr.nv, v_first + n * kCells),
+            tok < gr.nt && l - l == 0.f ? rows + tok * stride + head * kHeadDim : nullptr,
             [&](int p) { return p <= pos && (a.window == 0 || p > pos - a.window || p < a.n_sink); },
-            [&](int c, uint32_t (&x)[8]) {
+            [&](int c, int k, uint32_t (&x)[8]) {
               const uint4* from = reinterpret_cast<const uint4*>(static_cast<const __half*>(a.v_cache) +
                                                                  ((int64_t)c * G + g) * kHeadDim + 128 * half + 16 * k);
               const uint4 lo = from[0], hi = from[1];
               x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w, x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
             });
-#pragma unroll
-        for (int j = 0; j < 16; ++j) o[j] = y[j] != 0.f ? __float_as_uint(y[j]) : o[j];
-      });
+      }
       tc_fence_before();
     });
   } else if (warp < 16) {

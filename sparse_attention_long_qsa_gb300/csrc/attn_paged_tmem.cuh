@@ -30,42 +30,46 @@ __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
       : "+f"(x), "+f"(y)
       : "f"(a), "f"(b));
 }
-// Whether 16 values are all finite.
-__device__ __forceinline__ bool all_finite(const uint32_t (&o)[16]) {
-  float z = 0.f;
-#pragma unroll
-  for (int j = 0; j < 16; ++j) z = fmaf(__uint_as_float(o[j]), 0.f, z);
-  return z == 0.f;
-}
 // bits [0, n) of a word, any n
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
-// Adds to y the values that are not finite which a lane's row sees among the run's cells [v, v_end) (reading order), in 16
-// dims.  sees(p): whether the lane's row sees position p.  load(c, x): those dims of cell c, as halves.  By a whole warp, a
-// lane a cell (a chain of three loads), then a lane a row.
+// Infinite values of V and NaN make the sum of their dim, whatever else it has: those that a lane's row sees among the run's
+// cells [v0, v_end) (reading order), added up, take its place in the row's 128 columns (null: the lane has no row).
+// sees(p): whether the row sees position p.  load(c, k, x): dims 16 k .. + 15 of cell c, as halves.  By a whole warp, after
+// its results are out: a lane a cell (a chain of three loads for 32 of them), then a lane a row.
 template <typename Sees, typename Load>
-__device__ __forceinline__ void add_not_finite_seen(const PagedArgs& a, const Run& run, int v, int v_end, float (&y)[16], Sees sees,
-                                                    Load load) {
+__device__ __forceinline__ void put_not_finite(const PagedArgs& a, const Run& run, int v0, int v_end, float* row, Sees sees,
+                                               Load load) {
   const int lane = threadIdx.x & 31;
+  __syncwarp();   // the rows have been written, by other lanes
 #pragma unroll 1
-  for (; v < v_end; v += 32) {
-    const int at = v + lane;
-    const int c = checked_cell(a, cell_at(a, run, at, slot_at(a, run, at, v_end, false, nullptr), false, nullptr), false, nullptr);
-    uint32_t x[8] = {}, any = 0u;
-    if (c >= 0) load(c, x);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) any |= ((x[j] & 0x7c007c00u) + 0x04000400u) & 0x80008000u;   // an exponent of ones
-    unsigned who = __ballot_sync(kFull, any != 0u);
-    const int p = at < v_end ? pos_of(run.g, at) : 0;
+  for (int k = 0; k < 8; ++k) {
+    float y[16] = {};
 #pragma unroll 1
-    for (; who; who &= who - 1u) {
-      const int l = __ffs((int)who) - 1;
-      const bool s = sees(__shfl_sync(kFull, p, l));
+    for (int v = v0; v < v_end; v += 32) {
+      const int at = v + lane;
+      const int c = checked_cell(a, cell_at(a, run, at, slot_at(a, run, at, v_end, false, nullptr), false, nullptr), false, nullptr);
+      uint32_t x[8] = {}, any = 0u;
+      if (c >= 0) load(c, k, x);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t w = __shfl_sync(kFull, x[j], l);
-        if (s) add_not_finite(y[2 * j], y[2 * j + 1], w);
+      for (int j = 0; j < 8; ++j) any |= ((x[j] & 0x7c007c00u) + 0x04000400u) & 0x80008000u;   // an exponent of ones
+      unsigned who = __ballot_sync(kFull, any != 0u);
+      const int p = at < v_end ? pos_of(run.g, at) : 0;
+#pragma unroll 1
+      for (; who; who &= who - 1u) {
+        const int l = __ffs((int)who) - 1;
+        const bool s = sees(__shfl_sync(kFull, p, l));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t w = __shfl_sync(kFull, x[j], l);
+          if (s) add_not_finite(y[2 * j], y[2 * j + 1], w);
+        }
       }
+    }
+    if (row != nullptr) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (y[j] != 0.f) row[16 * k + j] = y[j];
     }
   }
 }
@@ -80,12 +84,12 @@ __device__ __forceinline__ int stretch_of(int tiles, int additions) {
 // A stretch's or a run's sums: of the warp's 32 rows (token first / 8 and on, head first % 8; a lane a row) 128 columns of
 // tensor memory, and `old` (if there is one: rows of the same order, 256 values apart) times fs, all times w, to
 // base[token * stride + head * 256].  A warp's stores of a lane a row would touch 32 lines each, so 16 columns at a time
-// pass through shared memory and go out as 64 bytes of eight rows.  fix(k, o): the lane's values of columns
-// 16 k .. + 15 on the way.  kWithout: sums in `old` that are not finite are left out.
+// pass through shared memory and go out as 64 bytes of eight rows.  kCheck: returns whether the lane's row holds columns
+// that are not finite.
 constexpr int kOutPitch = 20;
-template <bool kWithout, typename Fix>
-__device__ __forceinline__ void write_rows(uint32_t taddr, float (*buf)[kOutPitch], float w, float* base, int64_t stride,
-                                           const float* old, float fs, int first, int tokens, Fix fix) {
+template <bool kCheck>
+__device__ __forceinline__ bool write_rows(uint32_t taddr, float (*buf)[kOutPitch], float w, float* base, int64_t stride,
+                                           const float* old, float fs, int first, int tokens) {
   const int lane = threadIdx.x & 31, col = 4 * (lane & 3), sub = lane >> 2;
   const bool wide = (reinterpret_cast<uintptr_t>(base) & 15u) == 0u;
   // sums added where they are: without waiting for them, where no row has another reference since
@@ -98,6 +102,7 @@ __device__ __forceinline__ void write_rows(uint32_t taddr, float (*buf)[kOutPitc
   float rw[4], rf[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) rw[i] = __shfl_sync(kFull, w, 8 * i + sub), rf[i] = __shfl_sync(kFull, fs, 8 * i + sub);
+  float z[4] = {};   // zeros, or NaN
 #pragma unroll 1
   for (int k = 0; k < 8; k += 2) {
     uint32_t o[2][16];
@@ -110,15 +115,12 @@ __device__ __forceinline__ void write_rows(uint32_t taddr, float (*buf)[kOutPitc
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (read && i < have) {
-          y[i] = __ldcg(reinterpret_cast<const float4*>(from + i * (8 * kHeadDim) + 16 * (k + c)));
-          if constexpr (kWithout) {
-            y[i].x = isfinite(y[i].x) ? y[i].x : 0.f, y[i].y = isfinite(y[i].y) ? y[i].y : 0.f;
-            y[i].z = isfinite(y[i].z) ? y[i].z : 0.f, y[i].w = isfinite(y[i].w) ? y[i].w : 0.f;
-          }
-        }
+        if (read && i < have) y[i] = __ldcg(reinterpret_cast<const float4*>(from + i * (8 * kHeadDim) + 16 * (k + c)));
       }
-      fix(k + c, o[c]);
+      if constexpr (kCheck) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) z[j & 3] = fmaf(__uint_as_float(o[c][j]), 0.f, z[j & 3]);
+      }
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < 16; j += 4)
@@ -144,6 +146,7 @@ __device__ __forceinline__ void write_rows(uint32_t taddr, float (*buf)[kOutPitc
       }
     }
   }
+  return kCheck && (z[0] + z[1]) + (z[2] + z[3]) != 0.f;
 }
 
 }  // namespace
