@@ -549,11 +549,16 @@ qsa_status qsa_cache_sweep(const qsa_config* cfg, uint32_t flags, const int32_t*
  * output, were it NaN.  Any number of tokens from one on, of any sequences;
  * neighbouring tokens of one sequence at neighbouring positions (drafted tokens, a
  * prompt) share the reading of its cells.
- * Arithmetic is fp32 on the rows as stored (kv_type f16, q8_0, q4_0): nothing is
- * rounded to fp16, neither values of a row nor probabilities (against 64 bits outputs
- * of N(0, 1) rows are off by 4e-7 to 7e-6 of their norm).  Within a sequence's
+ * Sums and the softmax are fp32; values of a row enter the products as stored
+ * (kv_type f16, q8_0, q4_0: code times scale, exactly).  A weight has 22 bits, or, of
+ * 16 to 128 cells that are read together, 2^-39 of the largest where that stands out;
+ * where neighbouring tokens share their reading a sum is cut to 24 bits at each
+ * addition of up to 288.  Against 64 bits outputs of N(0, 1) rows are off by 4e-7 to
+ * 7e-6 of their norm, and by no more below a sink that takes all but 2^-24 of a
+ * cell's weight.  Within a sequence's
  * range the sums run over tiles whose order depends on the call's shape and the
- * device, not on timing.  An infinite or NaN scale of a visible K block gives NaN,
+ * device, not on timing.  An infinite fp16 value of a visible V is one of the output.
+ * An infinite or NaN scale of a visible K block gives NaN,
  * one of a V block NaN in that block's dims.  Where neighbouring tokens share their
  * reading, a block of a quantised cache counts as such from the scale on that takes its
  * codes past fp16's largest value (512 for q8_0, 8,192 for q4_0).

@@ -8,8 +8,7 @@
 //                 from shared memory (an operand A there costs 36 cycles more a
 //                 product of any N)
 //   P             exp2 of S relative to a reference of each row, in two fp16 parts
-//                 (22 bits), over S in tensor memory; the reference follows the
-//                 row's maximum only when that is 2^8 above it
+//                 (22 bits), over S in tensor memory (attn_paged_tmem.cuh)
 //   O += P V      M 128, N 256, K 64, in place
 // 256 columns of tensor memory hold O, 128 Q, and 2 x 64 S and P of two tiles: all
 // 512.  The tensor cores form tile i + 1's scores while the softmax warps work on
@@ -53,7 +52,6 @@ constexpr int kUncut = 4;                    // tiles (see plan): 2 us each
 constexpr int kSoft = 256, kConv = 256;
 constexpr int kSuper = 512;                  // cells whose ids are looked up together
 constexpr int kTiles = kSuper / kCells;
-constexpr float kUp = 7.f, kSlack = 8.f;     // probabilities: 2^(s - reference + kUp), at most 2^15
 constexpr uint32_t kColQ = 256, kColS = 384;
 constexpr uint32_t kPartBytes = 64 * 512;    // 64 cells, 256 dims
 
@@ -276,7 +274,7 @@ __global__ void __launch_bounds__(KV == QSA_KV_F16 ? 896 : 768, 1) k_paged_few(c
       const int stretch = stretch_of(n, kAdditions);
       int next = stretch;   // where the next one begins
       float fs = 0.f;       // of the stretches' sums so far
-      float m = mine ? kNoMax : 0.f, l = 0.f;   // the row's reference, and this half's sum relative to it
+      float m = mine ? kNoMax : 0.f, high = kNoMax, l = 0.f;   // the row's reference, the highest, this half's sum relative to it
       for (int i = 0; i < n; ++i) {
         const int b = (base + i) & 1;
         const uint32_t ts = tl + kColS + kCells * b + 32 * half;
@@ -301,14 +299,12 @@ __global__ void __launch_bounds__(KV == QSA_KV_F16 ? 896 : 768, 1) k_paged_few(c
           float t4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
           for (int j = 4; j < 32; ++j) t4[j & 3] = fmaxf(t4[j & 3], s[j]);
-          float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+          const float top = tile_top(t4, scale2);
           sm.max[b][half][row] = top;
           bar_named(2 + quarter, 64);   // the row's two threads
-          top = fmaxf(top, sm.max[b][half ^ 1][row]);
-          top = top == -INFINITY ? top : top * scale2;
-          const bool raise = mine && (top > m + kSlack || top != top);
-          if (__any_sync(kFull, raise)) {
-            const float nm = raise ? top : m, f = ex2(m - nm);
+          const float nm = mine ? next_reference(m, high, top, sm.max[b][half ^ 1][row], scale2) : m;
+          if (__any_sync(kFull, nm != m)) {
+            const float f = ex2(m - nm);
             l *= f;
             m = nm;
             raised = f;
@@ -340,9 +336,9 @@ __global__ void __launch_bounds__(KV == QSA_KV_F16 ? 896 : 768, 1) k_paged_few(c
               x = ex2(x), y = ex2(y);
               add2(sx, sy, x, y);
               if constexpr (kWeigh) s[c] = x, s[c + 1] = y;
-              const float hx = __uint_as_float(__float_as_uint(x) & 0xffffe000u), hy = __uint_as_float(__float_as_uint(y) & 0xffffe000u);
-              w[j] = bits(__floats2half2_rn(hx, hy));
-              add2(x, y, -hx, -hy);
+              float2 h;
+              w[j] = first_part(x, y, h);
+              add2(x, y, -h.x, -h.y);
               w[8 + j] = bits(__floats2half2_rn(x, y));
             }
             tmem_st16(ts + 16 * k, w);

@@ -9,9 +9,7 @@
 // tiles, see attn_paged.cu):
 //   S = Q K^T     M 256, N 128 (each CTA holds 64 cells' rows), K 256
 //   P             exp2 of S relative to a reference of each row, in two fp16 parts
-//                 (22 bits), over S in tensor memory; the reference follows the
-//                 row's maximum only when that is 2^8 above it, so the sums are
-//                 hardly ever rescaled
+//                 (22 bits), over S in tensor memory (attn_paged_tmem.cuh)
 //   O += P V      M 256, N 256 (each CTA holds 128 dims), K 128, twice (the two
 //                 parts), in place
 // 2 x 128 columns of tensor memory hold S and P of two tiles, 256 hold O: all 512.
@@ -55,7 +53,6 @@ constexpr int kSoft = 256, kGather = 256, kThreads = kSoft + kGather + 64;
 constexpr int kStages = 4;
 constexpr uint32_t kStageBytes = 32768;      // 64 cells' K rows, or 128 dims of 128 cells' V rows
 constexpr int kSuper = 512;                  // cells whose ids are looked up together
-constexpr float kUp = 7.f, kSlack = 8.f;     // probabilities: 2^(s - reference + kUp), at most 2^15
 constexpr uint32_t kColS = 256;
 constexpr int kAdditions = 16;               // to O, of a tile
 
@@ -221,7 +218,7 @@ __global__ void __launch_bounds__(640, 1) k_paged_prompt(const PagedArgs a, unsi
       int next = stretch;   // where the next one begins
       float fs = 0.f;       // of the stretches' sums so far
       bool odd = false;     // some of them are not finite
-      float m = kNoMax, l = 0.f;   // the row's reference, and this half's sum relative to it
+      float m = kNoMax, high = kNoMax, l = 0.f;   // the row's reference, the highest, this half's sum relative to it
       for (int i = 0; i < n; ++i) {
         const int b = (base + i) & 1;
         const uint32_t ts = tl + kColS + kCells * b + 64 * half;
@@ -247,14 +244,12 @@ __global__ void __launch_bounds__(640, 1) k_paged_prompt(const PagedArgs a, unsi
         float t4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
         for (int j = 4; j < 64; ++j) t4[j & 3] = fmaxf(t4[j & 3], s[j]);
-        float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+        const float top = tile_top(t4, scale2);
         sm.max[b][half][row] = top;
         bar_named(2 + quarter, 64);   // the row's two threads
-        top = fmaxf(top, sm.max[b][half ^ 1][row]);
-        top = top == -INFINITY ? top : top * scale2;
-        const bool raise = top > m + kSlack || top != top;
-        if (__any_sync(kFull, raise)) {
-          const float nm = raise ? top : m, f = ex2(m - nm);
+        const float nm = next_reference(m, high, top, sm.max[b][half ^ 1][row], scale2);
+        if (__any_sync(kFull, nm != m)) {
+          const float f = ex2(m - nm);
           l *= f;
           m = nm;
           raised = f;
@@ -288,9 +283,9 @@ __global__ void __launch_bounds__(640, 1) k_paged_prompt(const PagedArgs a, unsi
             }
             x = ex2(x), y = ex2(y);
             add2(sx, sy, x, y);
-            const float hx = __uint_as_float(__float_as_uint(x) & 0xffffe000u), hy = __uint_as_float(__float_as_uint(y) & 0xffffe000u);
-            hi[j] = half_bits(__floats2half2_rn(hx, hy));
-            add2(x, y, -hx, -hy);
+            float2 h;
+            hi[j] = first_part(x, y, h);
+            add2(x, y, -h.x, -h.y);
             lo[j] = half_bits(__floats2half2_rn(x, y));
           }
           tmem_st16(ts + 32 * k, hi);

@@ -30,6 +30,47 @@ __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
       : "+f"(x), "+f"(y)
       : "f"(a), "f"(b));
 }
+// Probabilities of a tile are 2^(s - reference + kUp) of each row, in two fp16 parts, the second what the first leaves:
+// 22 bits down to 2^-2 and less below, as a part ends at 2^-24.  So the reference follows the tiles.  It goes up where a
+// tile's largest score is kSlack above it (they stay below 2^16), and down where the largest is kLow below (of the tile:
+// what the cells of other tiles weigh does not cost its weights their bits); what has been summed up is scaled along, which
+// fp32 holds as long as no reference is kFar below another.  Ordinary rows are scaled once or twice a run: their tiles'
+// largest scores lie a few places apart.  Where a few cells of a tile stand out (kAlone above some eighth of the tile's,
+// or above the other half's), the others get what is left of fp16's range: the largest weight starts at its top.
+// (With a reference that only went up, 2^7 for the largest: 24 places below a sink without value outputs were 8e-4 off, and
+// 40 below meaningless.  Rows of ordinary scores take the same time; scores spread by 11 places 3 to 8 % more.)
+constexpr float kUp = 8.f, kSlack = 7.9f, kLow = 14.f, kFar = 64.f, kAlone = 14.f;
+// The largest of a row's scores in half a tile, from that of four interleaved parts of it; its last bit says whether it
+// stands out (-inf: nothing is visible).
+__device__ __forceinline__ float tile_top(const float (&t)[4], float scale2) {
+  const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+  float low = top;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) low = t[j] == -INFINITY ? low : fminf(low, t[j]);
+  const float gap = (top - low) * scale2;
+  return __uint_as_float((__float_as_uint(top) & ~1u) | (gap > kAlone && gap < INFINITY ? 1u : 0u));
+}
+// The row's reference after a tile whose halves' tile_top are x and y.  `high`: the highest so far.
+__device__ __forceinline__ float next_reference(float m, float& high, float x, float y, float scale2) {
+  const float top2 = fmaxf(x, y), top = top2 == -INFINITY ? top2 : top2 * scale2;   // (-inf times zero would be NaN)
+  float nm = m;
+  if (top > m + kSlack || top != top) {
+    const bool alone = ((__float_as_uint(x) | __float_as_uint(y)) & 1u) || fabsf(x - y) * scale2 > kAlone;
+    nm = alone && fminf(x, y) > -INFINITY ? top - kSlack : top;
+  } else if (top < m - kLow && top > -INFINITY) {
+    nm = fminf(m, fmaxf(top, high - kFar));
+  }
+  high = fmaxf(high, nm);
+  return nm;
+}
+// Two probabilities' parts.
+__device__ __forceinline__ uint32_t first_part(float x, float y, float2& back) {
+  const __half2 h = __floats2half2_rn(x, y);
+  back = __half22float2(h);
+  uint32_t u;
+  memcpy(&u, &h, 4);
+  return u;
+}
 // bits [0, n) of a word, any n
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
