@@ -487,7 +487,8 @@ qsa_status qsa_cells_copy(const qsa_config* cfg, int32_t n, const int32_t* n_pai
  * sequence src_seq[f].  Whole blocks are shared: their slots are copied into
  * dst's block list.  A partial last block (n_pos % r cells) becomes private, so
  * that both sequences can go on: dst's list gets tail_slot[f], whose table row
- * holds tail_cells[f][0 .. n_pos % r) and -1, with slot_block_idx set, and
+ * holds tail_cells[f][0 .. n_pos % r) and -1, with slot_block_idx that of the source's
+ * block (at least its place in the list, which an eviction leaves behind it), and
  * copy_src / copy_dst (int32 [n_fork][r]) get the cell pairs that
  * qsa_cells_copy has to copy (-1 elsewhere).  The pooled key of tail_slot is
  * stale until it is pooled again (qsa_kv_append with `pooled` does so with the

@@ -176,7 +176,7 @@ k_seq_fork(const ForkArgs a, unsigned* err) {
       if (!bad && tail > 0) {
         a.blk_cells[(int64_t)ts * r + tid] = cell;
         if (tid == 0) {
-          a.slot_block_idx[ts] = nb;
+          a.slot_block_idx[ts] = max(nb, a.slot_block_idx[slot]);   // (after an eviction past its place in the list)
           a.seq_blk_slots[to + nb] = ts;
         }
       }
