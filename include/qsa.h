@@ -24,7 +24,9 @@
  *                     copying, sharing, freeing and compacting a cache's cells
  *   qsa_paged_attn    attention over all of a sequence's cells, or a window of
  *                     them and its first ones; the weight each block receives
- *   qsa_cache_evict   the blocks a sequence keeps, by that weight
+ *   qsa_cache_evict, qsa_weight_trim, qsa_seq_fork_weighed
+ *                     the blocks a sequence keeps, by that weight, and the weight
+ *                     of blocks that go or are shared
  *
  * Conventions for every call:
  *  - Pointers named as device buffers are DEVICE pointers owned by the caller.
@@ -505,6 +507,15 @@ qsa_status qsa_seq_fork(const qsa_config* cfg, int32_t n_fork, const int32_t* sr
                         const int64_t* seq_blk_off, int32_t* seq_blk_slots, int32_t n_seq, int64_t n_list,
                         int32_t* blk_cells, int32_t* slot_block_idx, int64_t n_slots, int64_t n_cells,
                         int64_t max_blocks, int32_t* copy_src, int32_t* copy_dst, qsa_stream_t stream);
+/* The same where blocks gather attention weight (qsa_paged_attn; block_weight may be
+ * NULL): a fork's whole blocks have in dst what they have in src, its tail and all
+ * entries of dst's list behind it 0. */
+qsa_status qsa_seq_fork_weighed(const qsa_config* cfg, int32_t n_fork, const int32_t* src_seq, const int32_t* dst_seq,
+                                const int32_t* n_pos, const int32_t* tail_slot, const int32_t* tail_cells,
+                                const int64_t* seq_blk_off, int32_t* seq_blk_slots, int32_t n_seq, int64_t n_list,
+                                int32_t* blk_cells, int32_t* slot_block_idx, int64_t n_slots, int64_t n_cells,
+                                int64_t max_blocks, int32_t* copy_src, int32_t* copy_dst, float* block_weight,
+                                qsa_stream_t stream);
 
 /* qsa_cache_sweep: what the sequences still hold, and the rest freed.
  * Sequence s holds positions 0 .. seq_len[s] - 1 (<= 0: none; past its list, or
@@ -565,8 +576,9 @@ qsa_status qsa_cache_sweep(const qsa_config* cfg, uint32_t flags, const int32_t*
  * codes past fp16's largest value (512 for q8_0, 8,192 for q4_0).
  * block_weight (optional, NULL to skip): fp32 [n_list], one value per entry of
  * seq_blk_slots; entry seq_blk_off[s] + b gets the sum, over the call's tokens of s
- * and their heads, of the probabilities of block b's cells added.  Zeroed by the
- * caller when a block enters the list.
+ * and their heads, of the probabilities of block b's cells added.  It is 0 when a
+ * block enters the list: qsa_weight_trim, qsa_seq_fork_weighed and qsa_cache_evict
+ * leave it so behind the blocks that sequences hold.
  * After qsa_cache_evict positions here are places in the shortened list.
  * max_len: host upper bound on the tokens' positions + 1 (at most 2^30); a token
  * past it is clamped and flagged.  n_list: entries of seq_blk_slots.  workspace:
@@ -604,6 +616,13 @@ qsa_status qsa_cache_evict(const qsa_config* cfg, int32_t keep, int32_t n_sink, 
                            const float* block_weight, int64_t max_blocks, int32_t* seq_len_out,
                            int32_t* seq_blk_slots_out, float* block_weight_out, int32_t* n_evicted,
                            qsa_stream_t stream);
+
+/* qsa_weight_trim: after sequences were freed or rolled back, block_weight of the
+ * entries behind the ceil(seq_len[s] / r) blocks that each one holds is 0 again
+ * (seq_len <= 0: of its whole list).  A list past n_list is left as it is and
+ * flagged. */
+qsa_status qsa_weight_trim(const qsa_config* cfg, const int32_t* seq_len, const int64_t* seq_blk_off, int32_t n_seq,
+                           int64_t n_list, float* block_weight, qsa_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Host helpers (no GPU).

@@ -532,6 +532,17 @@ qsa_status qsa_seq_fork(const qsa_config* cfg, int32_t n_fork, const int32_t* sr
                         const int64_t* seq_blk_off, int32_t* seq_blk_slots, int32_t n_seq, int64_t n_list,
                         int32_t* blk_cells, int32_t* slot_block_idx, int64_t n_slots, int64_t n_cells,
                         int64_t max_blocks, int32_t* copy_src, int32_t* copy_dst, qsa_stream_t stream) {
+  return qsa_seq_fork_weighed(cfg, n_fork, src_seq, dst_seq, n_pos, tail_slot, tail_cells, seq_blk_off, seq_blk_slots, n_seq,
+                              n_list, blk_cells, slot_block_idx, n_slots, n_cells, max_blocks, copy_src, copy_dst, nullptr,
+                              stream);
+}
+
+qsa_status qsa_seq_fork_weighed(const qsa_config* cfg, int32_t n_fork, const int32_t* src_seq, const int32_t* dst_seq,
+                                const int32_t* n_pos, const int32_t* tail_slot, const int32_t* tail_cells,
+                                const int64_t* seq_blk_off, int32_t* seq_blk_slots, int32_t n_seq, int64_t n_list,
+                                int32_t* blk_cells, int32_t* slot_block_idx, int64_t n_slots, int64_t n_cells,
+                                int64_t max_blocks, int32_t* copy_src, int32_t* copy_dst, float* block_weight,
+                                qsa_stream_t stream) {
   const qsa_status st = check_cfg(cfg);
   if (st != QSA_OK) return st;
   if (n_fork < 0 || n_seq < 0 || n_list < 0 || n_slots < 0 || n_cells < 0 || max_blocks < 0) return QSA_ERR_INVALID_ARG;
@@ -541,7 +552,7 @@ qsa_status qsa_seq_fork(const qsa_config* cfg, int32_t n_fork, const int32_t* sr
   if (!src_seq || !dst_seq || !n_pos || !tail_slot || !tail_cells || !seq_blk_off || !seq_blk_slots || !blk_cells ||
       !slot_block_idx || !copy_src || !copy_dst || n_seq == 0)
     return QSA_ERR_INVALID_ARG;
-  if (!aligned(seq_blk_off, 8)) return QSA_ERR_INVALID_ARG;
+  if (!aligned(seq_blk_off, 8) || !aligned(block_weight, 4)) return QSA_ERR_INVALID_ARG;
   unsigned* err = error_word();
   if (err == nullptr) return QSA_ERR_CUDA;
   ForkArgs a{};
@@ -563,6 +574,7 @@ qsa_status qsa_seq_fork(const qsa_config* cfg, int32_t n_fork, const int32_t* sr
   a.max_blocks = max_blocks;
   a.copy_src = copy_src;
   a.copy_dst = copy_dst;
+  a.block_weight = block_weight;
   return from_cuda(launch_seq_fork(a, err, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -656,6 +668,21 @@ qsa_status qsa_cache_evict(const qsa_config* cfg, int32_t keep, int32_t n_sink, 
   a.weight_out = block_weight_out;
   a.n_evicted = n_evicted;
   return from_cuda(launch_cache_evict(a, err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+qsa_status qsa_weight_trim(const qsa_config* cfg, const int32_t* seq_len, const int64_t* seq_blk_off, int32_t n_seq,
+                           int64_t n_list, float* block_weight, qsa_stream_t stream) {
+  const qsa_status st = check_cfg(cfg);
+  if (st != QSA_OK) return st;
+  if (n_seq < 0 || n_list < 0) return QSA_ERR_INVALID_ARG;
+  if (n_list > kMaxI32) return QSA_ERR_UNSUPPORTED;
+  if (n_seq == 0) return QSA_OK;
+  if (!seq_len || !seq_blk_off || !block_weight || !aligned(seq_blk_off, 8) || !aligned(seq_len, 4) || !aligned(block_weight, 4))
+    return QSA_ERR_INVALID_ARG;
+  unsigned* err = error_word();
+  if (err == nullptr) return QSA_ERR_CUDA;
+  return from_cuda(launch_weight_trim(seq_len, seq_blk_off, n_seq, cfg->compress_ratio, n_list, block_weight, err,
+                                      reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t qsa_cache_sweep_workspace_size(const qsa_config* cfg, int64_t n_cells, int64_t n_slots) {

@@ -135,7 +135,9 @@ k_seq_fork(const ForkArgs a, unsigned* err) {
   unsigned bad = 0u;
   int64_t so = 0, to = 0;
   int nb = 0, tail = 0, slot = -1;
+  int64_t list = 0;            // entries of dst's list
   int v[kForkPer];
+  float w[kForkPer];
   if (s < 0 || s >= a.n_seq || d < 0 || d >= a.n_seq || p < 0) {
     bad = kErrToken;
   } else {
@@ -144,12 +146,16 @@ k_seq_fork(const ForkArgs a, unsigned* err) {
     so = a.seq_blk_off[s];
     to = a.seq_blk_off[d];
     const int64_t need = nb + (tail > 0 ? 1 : 0), sl = a.seq_blk_off[s + 1], tl = a.seq_blk_off[d + 1];
+    list = tl - to;
     if (nb > a.max_blocks) bad |= kErrMaxBlocks;
     if (so < 0 || to < 0 || sl > a.n_list || tl > a.n_list || so + need > sl || to + need > tl) bad |= kErrBlockList;
     if (!bad) {
 #pragma unroll
       for (int i = 0; i < kForkPer; ++i)
-        if (j0 + i * kThreads < nb) v[i] = a.seq_blk_slots[so + j0 + i * kThreads];
+        if (j0 + i * kThreads < nb) {
+          v[i] = a.seq_blk_slots[so + j0 + i * kThreads];
+          w[i] = a.block_weight ? a.block_weight[so + j0 + i * kThreads] : 0.f;
+        }
     }
     if (!bad && tail > 0) {
       slot = a.seq_blk_slots[so + nb];
@@ -185,7 +191,13 @@ k_seq_fork(const ForkArgs a, unsigned* err) {
   if (!bad) {
 #pragma unroll
     for (int i = 0; i < kForkPer; ++i)
-      if (j0 + i * kThreads < nb) a.seq_blk_slots[to + j0 + i * kThreads] = v[i];
+      if (j0 + i * kThreads < nb) {
+        a.seq_blk_slots[to + j0 + i * kThreads] = v[i];
+        if (a.block_weight) a.block_weight[to + j0 + i * kThreads] = w[i];
+      }
+    // the whole blocks' weights go along; the tail's and those to come begin anew
+    if (a.block_weight)
+      for (int64_t j = nb + (int64_t)blockIdx.x * kThreads + tid; j < list; j += (int64_t)gridDim.x * kThreads) a.block_weight[to + j] = 0.f;
   }
   __threadfence();
 }
@@ -577,6 +589,25 @@ cudaError_t launch_seq_fork(const ForkArgs& a, unsigned* err, cudaStream_t strea
   prof_after(kKFork, stream);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
+}
+
+// A CTA a sequence: the weights of the entries behind its blocks.
+__global__ void __launch_bounds__(kThreads) k_weight_trim(const int32_t* seq_len, const int64_t* seq_blk_off, int r, int64_t n_list,
+                                                          float* block_weight, unsigned* err) {
+  grid_dep_wait();
+  const int s = blockIdx.x, len = seq_len[s];
+  const int64_t off = seq_blk_off[s], end = seq_blk_off[s + 1];
+  if (off < 0 || end < off || end > n_list) {
+    if (threadIdx.x == 0) atomicOr(err, kErrBlockList);
+    return;
+  }
+  const int64_t held = len > 0 ? ((int64_t)len + r - 1) / r : 0;
+  for (int64_t j = off + held + threadIdx.x; j < end; j += kThreads) block_weight[j] = 0.f;
+}
+cudaError_t launch_weight_trim(const int32_t* seq_len, const int64_t* seq_blk_off, int n_seq, int r, int64_t n_list, float* block_weight,
+                               unsigned* err, cudaStream_t stream) {
+  return launch_pdl(k_weight_trim, dim3((unsigned)n_seq), dim3(kThreads), 0, stream, 1, seq_len, seq_blk_off, r, n_list, block_weight,
+                    err);
 }
 
 // Workspace: the cells' bits and the slots', in whole tiles, then the tiles' sums.

@@ -102,4 +102,8 @@ struct EvictArgs {
 constexpr int64_t evict_max_blocks() { return 1 << 20; }   // entries of one sequence's list
 cudaError_t launch_cache_evict(const EvictArgs& a, unsigned* err, cudaStream_t stream);
 
+// Weights of entries behind the sequences' blocks to zero (cache_ops.cu).
+cudaError_t launch_weight_trim(const int32_t* seq_len, const int64_t* seq_blk_off, int n_seq, int r, int64_t n_list, float* block_weight,
+                               unsigned* err, cudaStream_t stream);
+
 }  // namespace qsa

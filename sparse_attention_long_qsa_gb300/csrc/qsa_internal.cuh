@@ -393,6 +393,7 @@ struct ForkArgs {
   int64_t max_blocks;
   int32_t* copy_src;
   int32_t* copy_dst;
+  float* block_weight;      // may be null
 };
 cudaError_t launch_seq_fork(const ForkArgs& a, unsigned* err, cudaStream_t stream);
 

@@ -238,21 +238,23 @@ class QSALayer:
         """Sequence dst_seq[f] becomes the first n_pos[f] positions of
         src_seq[f] (int32 CUDA tensors; tail_cells [n_fork][r]; at most the
         layer's max_blocks whole blocks, as for the steps): the block lists and
-        tables, and this layer's rows of the private tail cells.
+        tables, the shared blocks' weights (of the others of dst's list: 0), and
+        this layer's rows of the private tail cells.
         Returns the (source, destination) cell pairs, for other layers."""
         n, r = int(src_seq.numel()), self.cfgd["compress_ratio"]
         with _on(stream):
             pairs = torch.empty((2, n, r), dtype=torch.int32, device=self.device)
         qsa.seq_fork(self.cfg, src_seq, dst_seq, n_pos, tail_slot, tail_cells, self.seq_blk_off, self.seq_blk_slots,
-                     self.blk_cells, self.slot_block_idx, self.max_blocks, pairs[0], pairs[1], self.n_cells, stream)
+                     self.blk_cells, self.slot_block_idx, self.max_blocks, pairs[0], pairs[1], self.n_cells, stream,
+                     self.block_weight)
         qsa.cells_copy(self.cfg, pairs[0], pairs[1], self.k_cache, self.v_cache, self.idx_k, self.n_cells,
                        stream=stream)
         return pairs[0], pairs[1]
 
     def release(self, seq_len, compact=False, stream=None):
         """Free what the sequences no longer hold (seq_len: int32 CUDA tensor,
-        positions each one keeps); compact: also move the held cells to the
-        front, this layer's rows with them.  Returns a dict of the sweep's
+        positions each one keeps), their blocks' weights with it; compact: also
+        move the held cells to the front, this layer's rows with them.  Returns a dict of the sweep's
         outputs (counts, cell_map, free_cells, free_slots, move_src, move_dst):
         the layer's own tensors, which the next call writes again."""
         n, dev = self.n_cells, self.device
@@ -268,6 +270,8 @@ class QSALayer:
         qsa.cache_sweep(self.cfg, seq_len, self.seq_blk_off, self.seq_blk_slots, self.blk_cells, self.blk_cells, n,
                         s["counts"], self._ws_sweep, compact, s["cell_map"], s["free_cells"], s["free_slots"],
                         s["move_src"], s["move_dst"], stream)
+        if self.block_weight is not None:
+            qsa.weight_trim(self.cfg, seq_len, self.seq_blk_off, self.block_weight, stream)
         if compact:
             qsa.cells_copy(self.cfg, s["move_src"], s["move_dst"], self.k_cache, self.v_cache, self.idx_k, n,
                            s["counts"][3:], stream)

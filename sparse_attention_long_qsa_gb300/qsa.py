@@ -35,7 +35,7 @@ EXPORTS = ("qsa_config_init", "qsa_cells_per_token", "qsa_pool_update", "qsa_ind
            "qsa_sparse_attn", "qsa_sparse_attn_union", "qsa_index_attn", "qsa_index_attn_kernels", "qsa_kv_append", "qsa_blocks_dirty",
            "qsa_rope_init", "qsa_qk_norm_rope", "qsa_kv_read", "qsa_cells_copy", "qsa_seq_fork",
            "qsa_cache_sweep_workspace_size", "qsa_cache_sweep",
-           "qsa_paged_attn_workspace_size", "qsa_paged_attn", "qsa_cache_evict",
+           "qsa_paged_attn_workspace_size", "qsa_paged_attn", "qsa_cache_evict", "qsa_weight_trim", "qsa_seq_fork_weighed",
            "qsa_debug_check", "qsa_profile_kernel", "qsa_index_topk_kernels", "qsa_status_string")
 
 # Kernel ids of qsa_profile_kernel.
@@ -132,6 +132,8 @@ def _load():
     L.qsa_cells_copy.restype = _I32
     L.qsa_seq_fork.argtypes = [CP, _I32, _P, _P, _P, _P, _P, _P, _P, _I32, _I64, _P, _P, _I64, _I64, _I64, _P, _P, _P]
     L.qsa_seq_fork.restype = _I32
+    L.qsa_seq_fork_weighed.argtypes = [CP, _I32, _P, _P, _P, _P, _P, _P, _P, _I32, _I64, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P]
+    L.qsa_seq_fork_weighed.restype = _I32
     L.qsa_cache_sweep_workspace_size.argtypes = [CP, _I64, _I64]
     L.qsa_cache_sweep_workspace_size.restype = _SZ
     L.qsa_cache_sweep.argtypes = [CP, ctypes.c_uint32, _P, _P, _P, _I32, _I64, _P, _P, _I64, _I64,
@@ -144,6 +146,8 @@ def _load():
     L.qsa_paged_attn.restype = _I32
     L.qsa_cache_evict.argtypes = [CP, _I32, _I32, _I32, _P, _P, _P, _I32, _I64, _P, _I64, _P, _P, _P, _P, _P]
     L.qsa_cache_evict.restype = _I32
+    L.qsa_weight_trim.argtypes = [CP, _P, _P, _I32, _I64, _P, _P]
+    L.qsa_weight_trim.restype = _I32
     L.qsa_blocks_dirty.argtypes = [_P, _P, _I64, _I32, _P, _I32, ctypes.POINTER(_I32), _I32]
     L.qsa_blocks_dirty.restype = _I32
     L.qsa_debug_check.argtypes = [_P, ctypes.POINTER(ctypes.c_uint32)]
@@ -530,12 +534,15 @@ def cells_copy(cfg, src, dst, k_cache, v_cache, idx_k, n_cells: int, n_pairs=Non
 
 
 def seq_fork(cfg, src_seq, dst_seq, n_pos, tail_slot, tail_cells, seq_blk_off, seq_blk_slots, blk_cells,
-             slot_block_idx, max_blocks: int, copy_src, copy_dst, n_cells: int = 2**31 - 1, stream=None):
+             slot_block_idx, max_blocks: int, copy_src, copy_dst, n_cells: int = 2**31 - 1, stream=None,
+             block_weight=None):
     """Sequence dst_seq[f] becomes the first n_pos[f] positions of src_seq[f]:
     whole blocks shared, a partial last block private (tail_slot[f],
     tail_cells[f]); copy_src / copy_dst [n_fork][r] get the pairs for
     cells_copy.  n_cells: the cache's cells; tail cells at or past it are
-    flagged here (without it only by the calls that use them)."""
+    flagged here (without it only by the calls that use them).  block_weight
+    (as paged_attn's): the shared blocks' values go along, all others of
+    dst's list become 0."""
     torch, dev, i32 = _torch_dev()
     n, r, n_slots = src_seq.numel(), cfg.compress_ratio, blk_cells.shape[0]
     if not (dst_seq.numel() == n_pos.numel() == tail_slot.numel() == n
@@ -543,14 +550,17 @@ def seq_fork(cfg, src_seq, dst_seq, n_pos, tail_slot, tail_cells, seq_blk_off, s
         raise ValueError(f"dst_seq, n_pos and tail_slot must hold {n} values, tail_cells, copy_src and copy_dst {n * r}")
     if blk_cells.numel() != n_slots * r or slot_block_idx.numel() < n_slots:
         raise ValueError("blk_cells must be [n_slots][r] and slot_block_idx hold n_slots values")
-    st = lib().qsa_seq_fork(
+    if block_weight is not None and block_weight.numel() != seq_blk_slots.numel():
+        raise ValueError(f"block_weight must hold {seq_blk_slots.numel()} values, got {block_weight.numel()}")
+    st = lib().qsa_seq_fork_weighed(
         ctypes.byref(cfg), n, _at(src_seq, i32, dev, "src_seq"), _at(dst_seq, i32, dev, "dst_seq"),
         _at(n_pos, i32, dev, "n_pos"), _at(tail_slot, i32, dev, "tail_slot"),
         _at(tail_cells, i32, dev, "tail_cells"), _at(seq_blk_off, torch.int64, dev, "seq_blk_off"),
         _at(seq_blk_slots, i32, dev, "seq_blk_slots"), seq_blk_off.numel() - 1, seq_blk_slots.numel(),
         _at(blk_cells, i32, dev, "blk_cells"), _at(slot_block_idx, i32, dev, "slot_block_idx"),
         n_slots, int(n_cells), int(max_blocks),
-        _at(copy_src, i32, dev, "copy_src"), _at(copy_dst, i32, dev, "copy_dst"), _stream(stream))
+        _at(copy_src, i32, dev, "copy_src"), _at(copy_dst, i32, dev, "copy_dst"),
+        None if block_weight is None else _at(block_weight, torch.float32, dev, "block_weight"), _stream(stream))
     _check(st, "qsa_seq_fork")
 
 
@@ -645,6 +655,21 @@ def cache_evict(cfg, keep: int, n_sink: int, n_recent: int, seq_len, seq_blk_off
         _at(seq_blk_slots_out, i32, dev, "seq_blk_slots_out"), _at(block_weight_out, torch.float32, dev, "block_weight_out"),
         None if n_evicted is None else _at(n_evicted, i32, dev, "n_evicted"), _stream(stream))
     _check(st, "qsa_cache_evict")
+
+
+def weight_trim(cfg, seq_len, seq_blk_off, block_weight, stream=None):
+    """block_weight of the entries behind the blocks that seq_len positions of
+    each sequence take becomes 0: the blocks that enter there begin anew."""
+    torch, dev, i32 = _torch_dev()
+    if seq_len is None or block_weight is None:
+        raise ValueError("seq_len and block_weight are required")
+    n_seq = seq_blk_off.numel() - 1
+    if seq_len.numel() != n_seq:
+        raise ValueError(f"seq_len must hold {n_seq} values, got {seq_len.numel()}")
+    st = lib().qsa_weight_trim(
+        ctypes.byref(cfg), _at(seq_len, i32, dev, "seq_len"), _at(seq_blk_off, torch.int64, dev, "seq_blk_off"), n_seq,
+        block_weight.numel(), _at(block_weight, torch.float32, dev, "block_weight"), _stream(stream))
+    _check(st, "qsa_weight_trim")
 
 
 def blocks_dirty(old_tbl: np.ndarray, new_tbl: np.ndarray, pad_pow2_min: int = 4) -> np.ndarray:
