@@ -558,6 +558,7 @@ __global__ void __launch_bounds__(Row<KV>::kWarps * 32, 1) k_paged_one(const Pag
     const int64_t ps = ((int64_t)(2 * part + (run.first == 0 ? 1 : 0)) * G + g) * kGqa;   // the run's rows in the workspace
     float* out = whole ? a.out + ((int64_t)t0 * G + g) * kGqa * kHeadDim : a.part_o + ps * kHeadDim;
     const bool wide = (reinterpret_cast<uintptr_t>(out) & 15u) == 0u;
+    float odd = 0.f;   // zero, or NaN
     for (int i = tid; i < kGqa * kHeadDim / 4; i += kThreads) {
       const int h = i >> 6, d = (i & 63) * 4;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -566,31 +567,35 @@ __global__ void __launch_bounds__(Row<KV>::kWarps * 32, 1) k_paged_one(const Pag
         const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm.stage[w]) + h * kPitchO + d);
         x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
       }
-      if constexpr (kF16) {   // an infinite value times a weight's second part, of zero or below it, was NaN
-        const bool odd = !(isfinite(x.x) && isfinite(x.y) && isfinite(x.z) && isfinite(x.w)) && isfinite(sm.ml[1][h]);
-        if (__any_sync(kFull, odd)) {
-          float y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-          for (int v = run.first * kChunk; v < v_end; v += 32) {
-            const int mine = checked_cell(a, cell_at(a, run, v + lane, slot_at(a, run, v + lane, v_end, false, err), false, err), false, err);
-#pragma unroll 8
-            for (int j = 0; j < 32; ++j) {
-              const int c = __shfl_sync(kFull, mine, j);
-              const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __half*>(a.v_cache) + ((int64_t)max(c, 0) * G + g) * kHeadDim + d);
-              if (c >= 0) add_not_finite(y[0], y[1], w.x), add_not_finite(y[2], y[3], w.y);
-            }
-          }
-          if (odd) {
-            x.x = y[0] != 0.f ? y[0] : x.x, x.y = y[1] != 0.f ? y[1] : x.y;
-            x.z = y[2] != 0.f ? y[2] : x.z, x.w = y[3] != 0.f ? y[3] : x.w;
-          }
-        }
-      }
+      if constexpr (kF16) odd = fmaf((x.x + x.y) + (x.z + x.w), 0.f, odd);
       const float l = sm.ml[1][h], s = whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
       if (wide) {
         *reinterpret_cast<float4*>(out + 4 * i) = make_float4(x.x * s, x.y * s, x.z * s, x.w * s);
       } else {
         out[4 * i] = x.x * s, out[4 * i + 1] = x.y * s, out[4 * i + 2] = x.z * s, out[4 * i + 3] = x.w * s;
+      }
+    }
+    // infinite values of V and NaN make the sum of their dim (times a weight's second part, of zero or below it, infinity was
+    // NaN): those of the run's cells, added up, take its place
+    if (kF16 && __any_sync(kFull, odd != 0.f)) {
+#pragma unroll 1
+      for (int i = tid; i < kGqa * kHeadDim / 4; i += kThreads) {
+        const int h = i >> 6, d = (i & 63) * 4;   // (one head for a warp)
+        if (!isfinite(sm.ml[1][h])) continue;
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int v = run.first * kChunk; v < v_end; v += 32) {
+          const int mine = checked_cell(a, cell_at(a, run, v + lane, slot_at(a, run, v + lane, v_end, false, err), false, err), false, err);
+#pragma unroll 8
+          for (int j = 0; j < 32; ++j) {
+            const int c = __shfl_sync(kFull, mine, j);
+            const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __half*>(a.v_cache) + ((int64_t)max(c, 0) * G + g) * kHeadDim + d);
+            if (c >= 0) add_not_finite(y[0], y[1], w.x), add_not_finite(y[2], y[3], w.y);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (y[j] != 0.f) out[4 * i + j] = y[j];
       }
     }
     if (tid < kGqa) {
