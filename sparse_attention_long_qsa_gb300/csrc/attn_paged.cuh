@@ -66,20 +66,21 @@ struct Plan {
   int t0, first;       // the group of tile u0, and which of the group's tiles it is
 };
 
-// all * part / parts (a division of 64 bits takes some four times as long as one of 32).
+// all * part / parts, in 32 bits (part <= parts <= 2^15).
 __device__ __forceinline__ int share_of(int all, int part, int parts) {
-  const uint64_t x = (uint64_t)(unsigned)all * (unsigned)part;
-  return (int)(x >> 32 ? x / (unsigned)parts : (unsigned)x / (unsigned)parts);
+  const unsigned each = (unsigned)all / (unsigned)parts, rest = (unsigned)all % (unsigned)parts;
+  return (int)(each * (unsigned)part + rest * (unsigned)part / (unsigned)parts);
 }
 // By all threads of a CTA.  `least`: tiles of a part, where that leaves a part a token.  `uncut`: groups of no more tiles
 // are not shared by parts, as their join would take longer than their tiles (223 fp16 tokens of 255 positions 33 -> 19 us).
-// Nor is any group where the largest is hardly longer than a part's share, so that nothing has to be joined (420 fp16 tokens
-// of 700 43 -> 27 us, 3 x 900 of 1,000 110 -> 89, 35 x 8 of 500 q8_0 35 -> 29); with some of the groups cut all the same,
-// whole ones only cost (505 of 1,073 q8_0: 52 -> 63).
+// Nor is any group where no part gets much more than its share for that (`more` tiles, what the join would take, which for
+// more tokens than parts grows with them), so that nothing has to be joined (420 fp16 tokens of 700 43 -> 27 us, 3 x 900 of
+// 1,000 110 -> 77, 35 x 8 of 500 q8_0 35 -> 29; whole all the same: 24 x 5 of 1,000 33 -> 42, 2 x 300 of 4,000 72 -> 79, 80
+// tokens of 20,000 each 536 -> 782, of which some parts would have two).
 // A warp takes 32 tokens at a time (a word of flags: which of them start a run); what crosses words is scanned by one warp.
 // (4,096 tokens: 10 us, 512: 3, one: 1.)
 template <int NT, int kCells>
-__device__ __forceinline__ Plan plan(const PagedArgs& a, int* scratch, int tid, int part, int max_parts, int least, int uncut) {
+__device__ __forceinline__ void plan(const PagedArgs& a, int* scratch, Plan* out, int tid, int part, int max_parts, int least, int uncut, int more) {
   const int lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, n = a.n_tokens, words = (n + 31) >> 5;
   int* seq = scratch;
   int* pos = seq + kPagedPlan;
@@ -201,10 +202,29 @@ __device__ __forceinline__ Plan plan(const PagedArgs& a, int* scratch, int tid, 
   }
   // each has a tile; no fewer than tokens, whose runs would each wait for memory (12 tokens of 4 positions 24 -> 13 us)
   p.parts = min(max_parts, max(p.all / least, min(n, p.all)));
+  const int enough = p.all / p.parts + more;
+  if (longest <= more) {   // (a part gets less than a group more than its share)
+    uncut = max(uncut, longest);
+  } else if (longest > uncut && longest <= enough) {   // what the parts would have if each began with a group: a thread each
+    int* begins = seq;                                 // (free by now)
+    for (int i = tid; i <= p.parts; i += blockDim.x) {
+      const int u = share_of(p.all, i, p.parts);
+      int w = 0, l = 0;   // the last token with no more than u tiles before it
+#pragma unroll
+      for (int s = kPlanWords / 2; s >= 1; s >>= 1)
+        if (w + s < words && sum[w + s] <= u) w += s;
+#pragma unroll
+      for (int s = 16; s >= 1; s >>= 1)
+        if (32 * w + l + s < n && sum[w] + pre[32 * w + l + s - 1] <= u) l += s;
+      begins[i] = i == p.parts ? u : sum[w] + (l > 0 ? pre[32 * w + l - 1] : 0);
+    }
+    __syncthreads();
+    int largest = 0;
+    for (int i = lane; i < p.parts; i += 32) largest = max(largest, begins[i + 1] - begins[i]);
+    if ((int)__reduce_max_sync(kFull, largest) <= enough) uncut = longest;
+  }
   p.u0 = p.u1 = p.first = 0;
-  // (the join of more tokens than parts takes longer)
-  if (longest <= (int)((int64_t)p.all / p.parts) + (n > max_parts ? max(uncut, 6) : uncut)) uncut = max(uncut, longest);
-  if (part < p.parts) {
+  if (warp == 0 && part < p.parts) {
     // tile u's group: its first token, its first tile, its tiles
     auto group_of = [&](int u, int& begin, int& tiles) {
       begin = 0;
@@ -232,8 +252,8 @@ __device__ __forceinline__ Plan plan(const PagedArgs& a, int* scratch, int tid, 
     if (p.u0 < p.u1) p.t0 = group_of(p.u0, begin, tiles);
     p.first = p.u0 - begin;
   }
+  if (tid == 0) *out = p;
   __syncthreads();   // the scratch is free
-  return p;
 }
 
 // A run of tiles of one group.
@@ -284,7 +304,7 @@ __device__ __forceinline__ void announce(const PagedArgs& a, const Plan& p, cons
     return;
   }
   auto part_of = [&](int64_t tile) {
-    int x = (int)(tile * p.parts / p.all);
+    int x = min((int)((float)tile * (float)p.parts / (float)p.all), p.parts - 1);   // off by one at most
     while (share_of(p.all, x + 1, p.parts) <= tile) ++x;
     while (share_of(p.all, x, p.parts) > tile) --x;
     return x;

@@ -87,6 +87,7 @@ struct Smem {
   uint32_t ok[8][kSuper / 32];               // which of them exist
   uint64_t landed[kAhead], taken[kAhead], full[kStages], empty[kStages], s_full[2], p_full[2], pv_done[2], q_full;
   uint32_t tmem;
+  Plan plan;
   unsigned stray[8];                         // of a run: V values that are not finite were met
 };
 template <int KV>
@@ -199,7 +200,9 @@ __global__ void __launch_bounds__(KV == QSA_KV_F16 ? 896 : 768, 1) k_paged_few(c
   }
   grid_dep_wait();
   grid_dep_launch();
-  const Plan pl = plan<kNT, kCells>(a, reinterpret_cast<int*>(sm.stage[0]), tid, part, gridDim.x / G, 1, kUncut);
+  plan<kNT, kCells>(a, reinterpret_cast<int*>(sm.stage[0]), &sm.plan, tid, part, gridDim.x / G, 1, kUncut,
+                    a.n_tokens > (int)gridDim.x / G ? 6 + a.n_tokens / 64 : kUncut);
+  const Plan& pl = sm.plan;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

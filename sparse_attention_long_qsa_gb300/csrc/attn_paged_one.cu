@@ -58,6 +58,7 @@ struct Smem {
   uint2 vd[R::kWarps][kBlocks][4];               // a chunk's V scales: block, l4 -> cells 2 l4 + {0, 1, 8, 9}
   float m[R::kWarps][kGqa], l[R::kWarps][kGqa];
   float ml[2][kGqa];                             // the run's (max, sum)
+  Plan plan;
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -146,7 +147,8 @@ __global__ void __launch_bounds__(Row<KV>::kWarps * 32, 1) k_paged_one(const Pag
 
   grid_dep_wait();
   grid_dep_launch();
-  const Plan pl = plan<1, kChunk>(a, reinterpret_cast<int*>(sm.stage), tid, part, gridDim.x / G, kMinChunks, kWarps);   // (a chunk a warp)
+  plan<1, kChunk>(a, reinterpret_cast<int*>(sm.stage), &sm.plan, tid, part, gridDim.x / G, kMinChunks, kWarps, 2 * kWarps);   // (a chunk a warp)
+  const Plan& pl = sm.plan;
   if (tid == 0 && g == 0 && !a.span_by_token) a.span[part] = make_int4(0, 0, 0, 0);
 
   const unsigned char* kc = static_cast<const unsigned char*>(a.k_cache) + g * kCodes;

@@ -66,6 +66,7 @@ struct Smem {
   uint32_t ok[4][kSuper / 32];               // which of them exist
   uint64_t landed[kStages], full[kStages], s_full[2], p_full[2], pv_done[2], q_full;
   uint32_t tmem;
+  Plan plan;
   unsigned stray[4];                         // of a run: such V values were met (see above)
 };
 static_assert(kStages * kStageBytes >= kPlanScratch, "the plan's scratch");
@@ -156,7 +157,9 @@ __global__ void __launch_bounds__(640, 1) k_paged_prompt(const PagedArgs a, unsi
   }
   grid_dep_wait();
   grid_dep_launch();
-  const Plan pl = plan<kNT, kCells>(a, reinterpret_cast<int*>(sm.stage[0]), tid, part, (int)(gridDim.x >> 1) / G, 1, kUncut);
+  plan<kNT, kCells>(a, reinterpret_cast<int*>(sm.stage[0]), &sm.plan, tid, part, (int)(gridDim.x >> 1) / G, 1, kUncut,
+                    a.n_tokens > (int)(gridDim.x >> 1) / G ? 6 + a.n_tokens / 128 : kUncut);
+  const Plan& pl = sm.plan;
   tc_fence_before();
   __syncthreads();
   cluster_sync();   // both CTAs' barriers exist
