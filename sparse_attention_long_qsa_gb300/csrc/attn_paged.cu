@@ -25,6 +25,130 @@
 namespace qsa {
 namespace {
 
+// Adds the runs of a group that is spread over several parts.  Entries per token: a
+// block is a token and head; four dims a thread, every eighth part, the first of these
+// loaded with the parts' (max, sum), so that a row costs one wait for memory.  Entries
+// per part (more tokens than parts): four blocks of each of the group's parts share
+// its rows; 64 threads take a row, eight parts at a time.
+constexpr int kJoinThreads = 512, kJoinBlocks = 4;
+static_assert(kPagedMaxParts <= kJoinThreads, "a thread a part");
+__global__ void __launch_bounds__(kJoinThreads, 2) k_paged_join(const PagedArgs a) {
+  __shared__ float w[kPagedMaxParts];
+  __shared__ float4 o[7][64];
+  __shared__ float red[2][kJoinThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = blockIdx.y, G = a.n_kv_heads;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int4 sp = a.span[blockIdx.x];
+  if (sp.y == 0) return;
+  const int first = sp.z, np = sp.w - first + 1;   // the group's parts
+  auto row_of = [&](int i, int t, int h) -> int64_t {
+    return ((int64_t)(2 * (first + i) + (i == 0 ? 1 : 0)) * G + g) * (a.part_tokens * kGqa) + t * kGqa + h;
+  };
+  const int d = tid & 63, slice = tid >> 6;
+  auto add = [](float4& s, float c, const float4& y) {
+    s.x = fmaf(c, y.x, s.x), s.y = fmaf(c, y.y, s.y), s.z = fmaf(c, y.z, s.z), s.w = fmaf(c, y.w, s.w);
+  };
+  auto write = [&](int64_t row, const float4& s, float l) {
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    float* out = a.out + row * kHeadDim + 4 * d;
+    out[0] = s.x * inv, out[1] = s.y * inv, out[2] = s.z * inv, out[3] = s.w * inv;
+  };
+  constexpr int kBatch = 8, kEarly = 6;
+  if (!a.span_by_token) {
+    const int share = (blockIdx.x - first) * kJoinBlocks + blockIdx.z, shares = (np - 1) * kJoinBlocks;
+    for (int r = share * 8 + slice; r < sp.y * kGqa; r += shares * 8) {   // rows: token, head
+      const int t = r / kGqa, hr = r % kGqa;
+      float m = kNoMax, l = 0.f;
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i0 = 0; i0 < np; i0 += kBatch) {
+        float2 ml[kBatch];
+        float4 x[kBatch];
+        float nm = m, nan = 0.f;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          ml[i] = make_float2(kNoMax, 0.f);
+          x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i0 + i < np) {
+            ml[i] = *reinterpret_cast<const float2*>(a.part_ml + 2 * row_of(i0 + i, t, hr));
+            x[i] = *reinterpret_cast<const float4*>(a.part_o + row_of(i0 + i, t, hr) * kHeadDim + 4 * d);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          nm = fmaxf(nm, ml[i].x);
+          nan = fmaf(0.f, ml[i].x, nan);   // (fmaxf drops NaN)
+        }
+        nm += nan;
+        const float f0 = ex2(m - nm);
+        l *= f0;
+        s.x *= f0, s.y *= f0, s.z *= f0, s.w *= f0;
+        m = nm;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          if (i0 + i >= np) continue;
+          const float f = ex2(ml[i].x - m);
+          l = fmaf(f, ml[i].y, l);
+          add(s, f, x[i]);
+        }
+      }
+      const int64_t row = ((int64_t)(sp.x + t) * G + g) * kGqa + hr;
+      if (d == 0 && a.weigh) a.lse[row] = make_float2(m, l != 0.f ? 1.f / l : 0.f);
+      write(row, s, l);
+    }
+    return;
+  }
+  {
+    const int h = blockIdx.z, t = blockIdx.x - sp.x;
+    const float2 ml = tid < np ? *reinterpret_cast<const float2*>(a.part_ml + 2 * row_of(tid, t, h)) : make_float2(kNoMax, 0.f);
+    float4 x[kEarly];
+#pragma unroll
+    for (int k = 0; k < kEarly; ++k) {
+      const int i = slice + 8 * k;
+      if (i < np) x[k] = *reinterpret_cast<const float4*>(a.part_o + row_of(i, t, h) * kHeadDim + 4 * d);
+    }
+    float m = ml.x;
+#pragma unroll
+    for (int s = 16; s >= 1; s >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, s));
+    if (lane == 0) red[0][warp] = m;
+    __syncthreads();
+    m = red[0][lane & 15];
+#pragma unroll
+    for (int s = 8; s >= 1; s >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, s));
+    if (ml.x != ml.x) m = ml.x;   // (fmaxf drops NaN)
+    const float f = ex2(ml.x - m);
+    float l = f * ml.y;
+    if (tid < np) w[tid] = f;
+#pragma unroll
+    for (int s = 16; s >= 1; s >>= 1) l += __shfl_xor_sync(kFull, l, s);
+    if (lane == 0) red[1][warp] = l;
+    __syncthreads();
+    l = red[1][lane & 15];
+#pragma unroll
+    for (int s = 8; s >= 1; s >>= 1) l += __shfl_xor_sync(kFull, l, s);
+    const int64_t row = ((int64_t)(sp.x + t) * G + g) * kGqa + h;
+    if (tid == 0 && a.weigh) a.lse[row] = make_float2(m, l != 0.f ? 1.f / l : 0.f);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kEarly; ++k)
+      if (slice + 8 * k < np) add(s, w[slice + 8 * k], x[k]);
+#pragma unroll 8
+    for (int i = slice + 8 * kEarly; i < np; i += 8)
+      add(s, w[i], *reinterpret_cast<const float4*>(a.part_o + row_of(i, t, h) * kHeadDim + 4 * d));
+    if (slice > 0) o[slice - 1][d] = s;
+    __syncthreads();
+    if (slice == 0) {
+#pragma unroll
+      for (int i = 0; i < 7; ++i) {
+        const float4 y = o[i][d];
+        s.x += y.x, s.y += y.y, s.z += y.z, s.w += y.w;
+      }
+      write(row, s, l);
+    }
+  }
+}
+
 // block_weight[entry] += the probabilities of the entry's block, over the call's
 // tokens of its sequence and their heads.  A block takes every gridDim.x-th 64 entries of
 // the sequences that start at its share of the tokens.  A lane holds two entries; the warps
@@ -108,6 +232,11 @@ __global__ void __launch_bounds__(kWeighThreads) k_paged_weigh(const PagedArgs a
 }
 
 }  // namespace
+
+cudaError_t launch_paged_join(const PagedArgs& a, int64_t parts, cudaStream_t stream) {
+  const unsigned entries = (unsigned)(a.span_by_token ? a.n_tokens : parts), z = a.span_by_token ? kGqa : kJoinBlocks;
+  return launch_pdl(k_paged_join, dim3(entries, (unsigned)a.n_kv_heads, z), dim3(kJoinThreads), 0, stream, 1, a);
+}
 
 // Measured, us, one by one / groups of 16 / pairs' groups of 32:
 //   2 tokens of 50k f16 37 / 40 / 42, q8_0 32 / 37, q4_0 29 / 37; 24 x 2 tokens of 3,000 f16 42 / 50 / 52, q8_0 41 / 49

@@ -678,7 +678,7 @@ cudaError_t launch(PagedArgs a, unsigned* err, cudaStream_t stream) {
   a.span_by_token = a.n_tokens <= parts;
   a.part_tokens = a.n_tokens < kNT ? a.n_tokens : kNT;
   e = launch_pdl(k_paged_few<KV, kWeigh>, dim3((unsigned)(parts * a.n_kv_heads)), dim3(kThreads<KV>), kSmemBytes<KV>, stream, 1, a, err);
-  if (e == cudaSuccess && parts > 1) e = launch_join(a, parts, stream);
+  if (e == cudaSuccess && parts > 1) e = launch_paged_join(a, parts, stream);
   return e;
 }
 

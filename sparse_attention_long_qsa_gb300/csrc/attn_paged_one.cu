@@ -632,7 +632,7 @@ cudaError_t launch(PagedArgs a, unsigned* err, cudaStream_t stream) {
   a.part_tokens = 1;
   e = launch_pdl(k_paged_one<KV>, dim3((unsigned)(parts * a.n_kv_heads)), dim3(Row<KV>::kWarps * 32), sizeof(Smem<KV>), stream, 1, a,
                  err);
-  if (e == cudaSuccess && parts > 1) e = launch_join(a, parts, stream);
+  if (e == cudaSuccess && parts > 1) e = launch_paged_join(a, parts, stream);
   return e;
 }
 

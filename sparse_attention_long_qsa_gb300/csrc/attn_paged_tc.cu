@@ -533,7 +533,7 @@ cudaError_t launch_paged_prompt(PagedArgs a, unsigned* err, cudaStream_t stream)
   a.span_by_token = a.n_tokens <= parts;
   a.part_tokens = kNT;
   e = launch_pdl(k_paged_prompt, dim3((unsigned)(2 * parts * a.n_kv_heads)), dim3(kThreads), kSmemBytes, stream, 2, a, err);
-  if (e == cudaSuccess && parts > 1) e = launch_join(a, parts, stream);
+  if (e == cudaSuccess && parts > 1) e = launch_paged_join(a, parts, stream);
   return e;
 }
 

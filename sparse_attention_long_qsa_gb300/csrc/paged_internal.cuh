@@ -72,6 +72,8 @@ int paged_group(const PagedArgs& a, int kv_type);
 // Runs that each KV head's tiles of so many cells are dealt in, by `ctas` CTAs (or pairs), at most
 // most_ctas of them.
 int64_t paged_launch_parts(const PagedArgs& a, int64_t ctas, int64_t most_ctas, int cells);
+// Adds the partial results of groups that several of the parts share (attn_paged.cu).
+cudaError_t launch_paged_join(const PagedArgs& a, int64_t parts, cudaStream_t stream);
 // One token of a sequence (attn_paged_one.cu).
 cudaError_t launch_paged_one(const PagedArgs& a, int kv_type, unsigned* err, cudaStream_t stream);
 // Two tokens and more (attn_paged_few.cu).
