@@ -560,7 +560,9 @@ qsa_status qsa_cache_sweep(const qsa_config* cfg, uint32_t flags, const int32_t*
  * that sees nothing gets zeros.  What a token does not see does not reach its
  * output, were it NaN.  Any number of tokens from one on, of any sequences;
  * neighbouring tokens of one sequence at neighbouring positions (drafted tokens, a
- * prompt) share the reading of its cells.
+ * prompt) share the reading of its cells, also beside single tokens and in a table of
+ * many sequences.  (Where max_len bounds the call to less than about 1 GB of rows one
+ * way of reading is chosen for the whole call, by n_tokens / n_seq.)
  * Sums and the softmax are fp32; values of a row enter the products as stored
  * (kv_type f16, q8_0, q4_0: code times scale, exactly).  A weight has 22 bits, or, of
  * 16 to 128 cells that are read together, 2^-39 of the largest where that stands out;

@@ -23,7 +23,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build", "qsa")
 LIB = os.path.join(PKG, "libqsa.so")
 SOURCES = ["api.cu", "pool.cu", "index.cu", "attn.cu", "attn_pf.cu", "attn_union.cu", "append.cu",
-           "attn_q4.cu", "norm_rope.cu", "cache_ops.cu", "attn_paged.cu", "attn_paged_tc.cu", "attn_paged_few.cu", "attn_paged_one.cu", "evict.cu"]
+           "attn_q4.cu", "norm_rope.cu", "cache_ops.cu", "attn_paged.cu", "attn_paged_tc.cu", 
+           "attn_paged_few.cu", "attn_paged_few_mixed.cu", "attn_paged_one.cu", "evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -19,6 +19,7 @@
 // codes times scales in parts that hold them exactly; probabilities go in as two fp16
 // parts (22 bits).
 #include <algorithm>
+#include <atomic>
 
 #include "attn_paged.cuh"
 
@@ -32,6 +33,7 @@ namespace {
 // its rows; 64 threads take a row, eight parts at a time.
 constexpr int kJoinThreads = 512, kJoinBlocks = 4;
 static_assert(kPagedMaxParts <= kJoinThreads, "a thread a part");
+template <bool kMixed>
 __global__ void __launch_bounds__(kJoinThreads, 2) k_paged_join(const PagedArgs a) {
   __shared__ float w[kPagedMaxParts];
   __shared__ float4 o[7][64];
@@ -43,8 +45,13 @@ __global__ void __launch_bounds__(kJoinThreads, 2) k_paged_join(const PagedArgs 
   const int4 sp = a.span[blockIdx.x];
   if (sp.y == 0) return;
   const int first = sp.z, np = sp.w - first + 1;   // the group's parts
+  const bool groups = kMixed && (sp.y >> 8) != 0;
+  const int tokens = sp.y & 255, nth = blockIdx.x - (groups ? a.kinds[0].parts : 0) - first;   // (an entry a part: which of them)
+  const float* part_ml = !kMixed ? a.of.ml : groups ? a.kinds[1].ml : a.kinds[0].ml;
+  const float* part_o = !kMixed ? a.of.o : groups ? a.kinds[1].o : a.kinds[0].o;
+  const int part_tokens = !kMixed ? a.of.tokens : groups ? a.kinds[1].tokens : 1;
   auto row_of = [&](int i, int t, int h) -> int64_t {
-    return ((int64_t)(2 * (first + i) + (i == 0 ? 1 : 0)) * G + g) * (a.part_tokens * kGqa) + t * kGqa + h;
+    return ((int64_t)(2 * (first + i) + (i == 0 ? 1 : 0)) * G + g) * (part_tokens * kGqa) + t * kGqa + h;
   };
   const int d = tid & 63, slice = tid >> 6;
   auto add = [](float4& s, float c, const float4& y) {
@@ -57,8 +64,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) k_paged_join(const PagedArgs 
   };
   constexpr int kBatch = 8, kEarly = 6;
   if (!a.span_by_token) {
-    const int share = (blockIdx.x - first) * kJoinBlocks + blockIdx.z, shares = (np - 1) * kJoinBlocks;
-    for (int r = share * 8 + slice; r < sp.y * kGqa; r += shares * 8) {   // rows: token, head
+    const int share = nth * kJoinBlocks + blockIdx.z, shares = (np - 1) * kJoinBlocks;
+    for (int r = share * 8 + slice; r < tokens * kGqa; r += shares * 8) {   // rows: token, head
       const int t = r / kGqa, hr = r % kGqa;
       float m = kNoMax, l = 0.f;
       float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -71,8 +78,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) k_paged_join(const PagedArgs 
           ml[i] = make_float2(kNoMax, 0.f);
           x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (i0 + i < np) {
-            ml[i] = *reinterpret_cast<const float2*>(a.part_ml + 2 * row_of(i0 + i, t, hr));
-            x[i] = *reinterpret_cast<const float4*>(a.part_o + row_of(i0 + i, t, hr) * kHeadDim + 4 * d);
+            ml[i] = *reinterpret_cast<const float2*>(part_ml + 2 * row_of(i0 + i, t, hr));
+            x[i] = *reinterpret_cast<const float4*>(part_o + row_of(i0 + i, t, hr) * kHeadDim + 4 * d);
           }
         }
 #pragma unroll
@@ -101,12 +108,12 @@ __global__ void __launch_bounds__(kJoinThreads, 2) k_paged_join(const PagedArgs 
   }
   {
     const int h = blockIdx.z, t = blockIdx.x - sp.x;
-    const float2 ml = tid < np ? *reinterpret_cast<const float2*>(a.part_ml + 2 * row_of(tid, t, h)) : make_float2(kNoMax, 0.f);
+    const float2 ml = tid < np ? *reinterpret_cast<const float2*>(part_ml + 2 * row_of(tid, t, h)) : make_float2(kNoMax, 0.f);
     float4 x[kEarly];
 #pragma unroll
     for (int k = 0; k < kEarly; ++k) {
       const int i = slice + 8 * k;
-      if (i < np) x[k] = *reinterpret_cast<const float4*>(a.part_o + row_of(i, t, h) * kHeadDim + 4 * d);
+      if (i < np) x[k] = *reinterpret_cast<const float4*>(part_o + row_of(i, t, h) * kHeadDim + 4 * d);
     }
     float m = ml.x;
 #pragma unroll
@@ -135,7 +142,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) k_paged_join(const PagedArgs 
       if (slice + 8 * k < np) add(s, w[slice + 8 * k], x[k]);
 #pragma unroll 8
     for (int i = slice + 8 * kEarly; i < np; i += 8)
-      add(s, w[i], *reinterpret_cast<const float4*>(a.part_o + row_of(i, t, h) * kHeadDim + 4 * d));
+      add(s, w[i], *reinterpret_cast<const float4*>(part_o + row_of(i, t, h) * kHeadDim + 4 * d));
     if (slice > 0) o[slice - 1][d] = s;
     __syncthreads();
     if (slice == 0) {
@@ -161,7 +168,6 @@ __global__ void __launch_bounds__(kWeighThreads) k_paged_weigh(const PagedArgs a
   __shared__ int seq_of[kPagedWeigh], tok[kPagedWeigh];   // of all tokens; the sequence's
   __shared__ int4 geo[kPagedWeigh];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = a.n_kv_heads, heads = G * kGqa;
-  const int to_tile = 31 - __clz(a.e_cells) - a.r_shift;   // (blocks of a tile: a power of two)
   grid_dep_wait();
   grid_dep_launch();
   if (tid < kPagedWeigh) {
@@ -198,6 +204,7 @@ __global__ void __launch_bounds__(kWeighThreads) k_paged_weigh(const PagedArgs a
           const int t = tok[row_there ? k : 0];
           const int4 at = geo[t];
           const int ns = at.x >> a.r_shift, lo = at.y >> a.r_shift;
+          const int to_tile = 31 - __clz(at.w) - a.r_shift;   // (blocks of a tile: a power of two)
           const int64_t row = (int64_t)t * heads + h * kWeighWarps + warp;
           l[i] = a.lse[row];
 #pragma unroll
@@ -231,36 +238,130 @@ __global__ void __launch_bounds__(kWeighThreads) k_paged_weigh(const PagedArgs a
   }
 }
 
-}  // namespace
-
-cudaError_t launch_paged_join(const PagedArgs& a, int64_t parts, cudaStream_t stream) {
-  const unsigned entries = (unsigned)(a.span_by_token ? a.n_tokens : parts), z = a.span_by_token ? kGqa : kJoinBlocks;
-  return launch_pdl(k_paged_join, dim3(entries, (unsigned)a.n_kv_heads, z), dim3(kJoinThreads), 0, stream, 1, a);
-}
-
-// Measured, us, one by one / groups of 16 / pairs' groups of 32:
+// Which kernels a launch's tokens go to.  Tokens one by one read their rows once each; groups of 16, or on pairs of CTAs of
+// 32, share them.  Measured, us, one by one / groups of 16 / pairs' groups of 32:
 //   2 tokens of 50k f16 37 / 40 / 42, q8_0 32 / 37, q4_0 29 / 37; 24 x 2 tokens of 3,000 f16 42 / 50 / 52, q8_0 41 / 49
 //   3 tokens of 50k f16 51 / 41 / 43, q8_0 47 / 39, q4_0 42 / 39
-//   16 tokens of 50k f16 - / 46 / 45; 24 x 12 tokens of 3,000 - / 54 / 56; 24 x 24 - / 78 / 63
+//   16 tokens of 50k f16 - / 46 / 45; 24 x 12 tokens of 3,000 - / 54 / 56; 24 x 24 - / 78 / 63; 48 x 8 of 1,000 - / 42 / 72
 // Two tokens one by one read their rows twice, which pays as long as the second reading is L2's.
-int paged_group(const PagedArgs& a, int kv_type) {
-  const int64_t per = ceil_div(a.n_tokens, a.n_seq > 0 ? a.n_seq : 1);
-  const int64_t reach = a.window > 0 && a.window + a.n_sink < a.max_len ? a.window + a.n_sink : a.max_len;
-  const int row = kv_type == QSA_KV_F16 ? 512 : kv_type == QSA_KV_Q8_0 ? 272 : 144;
-  const bool cached = 2 * reach * a.n_kv_heads * row <= INT64_C(100) << 20;
-  return per <= 1 || (per == 2 && cached) ? 1 : per <= 16 || kv_type != QSA_KV_F16 || a.weigh ? 16 : 32;
+//
+// What the call's tokens come to for each list on average says which; how many are neighbours only the device sees.  Where
+// there are several lists the average may be far out: drafted tokens or a chunk of a prompt in a table of many lists, or
+// beside single tokens (us, by the average / by both kinds: 5 of 250k q8_0 in 64 lists 246 / 145, and 63 single tokens
+// beside them 413 / 173; 64 of 50k f16 634 / 88; 512 of 50k f16 in 64 lists 628 / 426, in 512 5,070 / 421).  So two kernels
+// are launched, one for short runs of neighbours and one for long ones, of which either may find nothing to do.  That takes
+// 2 to 3 us (64 single tokens of 300 in room for 100k f16 16.4 / 19.2, q8_0 15.8 / 18.5; of 11,000 254 / 251; with groups of
+// 16 and 32, which have a join each, 5 to 8: 64 x 5 of 11,000 292 / 300).  So it is done where, by its lists' bound, the
+// call takes a quarter of a millisecond if it is what its average says: tokens one by one read 5 TB/s, groups 3.
+struct Route {
+  enum Kernel { kOne, kFew, kPairs } kernel, high;   // `high` where `mixed`: for runs of more than `split` tokens
+  bool mixed, high_first;
+  int split;
+};
+Route route(const PagedArgs& a, int64_t call_tokens, int kv_type) {
+  const int64_t per = ceil_div(call_tokens, a.n_seq > 0 ? a.n_seq : 1), seen = (int64_t)a.window + a.n_sink;
+  const int64_t reach = a.window > 0 && seen < a.max_len ? seen : a.max_len;
+  const int64_t row = kv_type == QSA_KV_F16 ? 512 : kv_type == QSA_KV_Q8_0 ? 272 : 144;
+  const int64_t rows = 2 * reach * a.n_kv_heads * row;   // of a token
+  const bool cached = rows <= INT64_C(100) << 20, pairs = kv_type == QSA_KV_F16 && !a.weigh;
+  Route r{};
+  r.kernel = per <= 1 || (per == 2 && cached) || a.n_tokens == 1 ? Route::kOne : per <= 16 || !pairs ? Route::kFew : Route::kPairs;
+  const double bytes = (double)rows * (a.n_seq < a.n_tokens ? a.n_seq : a.n_tokens);
+  r.mixed = a.n_seq > 1 && a.n_tokens > 2 && bytes >= (r.kernel == Route::kOne ? 1.25e9 : 0.75e9);
+  const Route::Kernel groups = pairs && a.n_tokens > 16 ? Route::kPairs : Route::kFew;
+  // (single tokens among groups of 16 cost much only where they are most)
+  if (!r.mixed || (r.kernel == groups && groups == Route::kFew && per > 2)) {
+    r.mixed = false;
+    return r;
+  }
+  r.high = groups;
+  r.high_first = r.kernel == groups;
+  r.split = cached ? 2 : 1;
+  if (r.kernel == Route::kFew && groups == Route::kPairs) r.split = 16;
+  else r.kernel = Route::kOne;
+  return r;
 }
 
-int64_t paged_launch_parts(const PagedArgs& a, int64_t ctas, int64_t most_ctas, int cells) {
-  // no more parts than there can be tiles
+// Parts that each KV head's tiles are dealt in: by `ctas` CTAs (or pairs), at most most_ctas of them, no more than there can
+// be tiles of so many cells.
+int launch_parts(const PagedArgs& a, int64_t ctas, int64_t most_ctas, int cells) {
   const int64_t reach = a.window > 0 && a.window < a.max_len ? a.window : a.max_len;
   const int64_t most = (int64_t)a.n_tokens * ceil_div((reach < a.max_len - a.n_sink ? reach + a.n_sink : a.max_len) + cells, cells);
-  int64_t parts = (ctas < most_ctas ? ctas : most_ctas) / a.n_kv_heads;
-  parts = parts < 1 ? 1 : parts;
-  return parts > most ? most : parts;
+  return (int)std::min(std::max<int64_t>(std::min(ctas, most_ctas) / a.n_kv_heads, 1), most);
 }
 
-// The workspace: spans, partials of two runs a part, and for block weights the
+// The current device's.
+cudaError_t multiprocessors(int* n) {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> known[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  *n = known[dev].load(std::memory_order_relaxed);
+  if (*n == 0) {
+    e = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) known[dev].store(*n, std::memory_order_relaxed);
+  }
+  return e;
+}
+
+// One of the kernels, without its join.
+cudaError_t launch_kernel(const PagedArgs& a, Route::Kernel k, bool mixed, int kv_type, unsigned* err, cudaStream_t stream) {
+  return k == Route::kOne     ? launch_paged_one(a, kv_type, mixed, err, stream)
+         : k == Route::kPairs ? launch_paged_prompt(a, mixed, err, stream)
+         : mixed              ? launch_paged_few_mixed(a, kv_type, err, stream)
+                              : launch_paged_few(a, kv_type, err, stream);
+}
+// Adds the partial results of groups that several parts share.
+cudaError_t launch_join(const PagedArgs& a, int parts, bool mixed, cudaStream_t stream) {
+  const unsigned entries = (unsigned)(a.span_by_token ? a.n_tokens : parts), z = a.span_by_token ? kGqa : kJoinBlocks;
+  const dim3 grid(entries, (unsigned)a.n_kv_heads, z);
+  return mixed ? launch_pdl(k_paged_join<true>, grid, dim3(kJoinThreads), 0, stream, 1, a)
+               : launch_pdl(k_paged_join<false>, grid, dim3(kJoinThreads), 0, stream, 1, a);
+}
+
+cudaError_t launch_tokens(PagedArgs a, const Route& r, int kv_type, int sms, unsigned* err, cudaStream_t stream) {
+  auto partials = [&](Route::Kernel k) {
+    PagedPartials x = a.kinds[k != Route::kOne];
+    x.tokens = k == Route::kOne ? 1 : k == Route::kPairs ? 32 : a.n_tokens < 16 ? a.n_tokens : 16;
+    x.parts = k == Route::kOne     ? launch_parts(a, sms, kPagedMaxParts, kPagedOneCells)
+              : k == Route::kPairs ? launch_parts(a, sms / 2, kPagedMaxPairs, kPagedPromptCells)
+                                   : launch_parts(a, sms, kPagedMaxFew, kPagedFewCells);
+    return x;
+  };
+  cudaError_t e = cudaSuccess;
+  if (!r.mixed) {
+    a.of = partials(r.kernel);
+    a.span_by_token = a.n_tokens <= a.of.parts;
+    e = launch_kernel(a, r.kernel, false, kv_type, err, stream);
+    return e == cudaSuccess && a.of.parts > 1 ? launch_join(a, a.of.parts, false, stream) : e;
+  }
+  // one by one and in groups: one join for both; groups of 16 and of 32 (whose partials take the same place): one each
+  const bool joint = r.kernel == Route::kOne;
+  a.kinds[0] = partials(r.kernel);
+  a.kinds[1] = partials(r.high);
+  a.span_by_token = joint && a.n_tokens <= std::min(a.kinds[0].parts, a.kinds[1].parts);
+  for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
+    const bool high = (i == 0) == r.high_first;
+    PagedArgs b = a;
+    b.second = i;
+    b.run_lo = high ? r.split : 0;
+    b.run_hi = high ? a.n_tokens : r.split;
+    b.of = a.kinds[high];
+    b.kind = joint && high;
+    if (joint && high && !a.span_by_token) b.span += a.kinds[0].parts;
+    e = launch_kernel(b, high ? r.high : r.kernel, true, kv_type, err, stream);
+    if (e == cudaSuccess && !joint && b.of.parts > 1) e = launch_join(b, b.of.parts, false, stream);
+  }
+  if (e == cudaSuccess && joint && std::max(a.kinds[0].parts, a.kinds[1].parts) > 1)
+    e = launch_join(a, a.kinds[0].parts + a.kinds[1].parts, true, stream);
+  return e;
+}
+
+}  // namespace
+
+// The workspace: spans, partials of two runs a part of either kind, and for block weights the
 // tokens' geometry, rows' (max, 1 / sum) and block sums.
 size_t paged_workspace_bytes(int n_tokens, int n_kv_heads, int64_t max_len, int r_shift, bool weigh, PagedArgs* a, void* ws) {
   unsigned char* base = static_cast<unsigned char*>(ws);
@@ -277,13 +378,16 @@ size_t paged_workspace_bytes(int n_tokens, int n_kv_heads, int64_t max_len, int 
     const int64_t parts = ctas / n_kv_heads;
     return 2 * (parts > 0 ? parts : 1) * n_kv_heads * group * kGqa;
   };
-  int64_t rows = rows_of(kPagedMaxParts, 1);
-  if (tokens > 1) rows = std::max(rows, rows_of(kPagedMaxFew, tokens < 16 ? tokens : 16));
-  if (tokens > 16 && !weigh) rows = std::max(rows, rows_of(kPagedMaxPairs, 32));
+  int64_t rows[2] = {rows_of(kPagedMaxParts, 1), 0};
+  if (tokens > 1) rows[1] = rows_of(kPagedMaxFew, tokens < 16 ? tokens : 16);
+  if (tokens > 16 && !weigh) rows[1] = std::max(rows[1], rows_of(kPagedMaxPairs, 32));
   PagedArgs x{};
-  x.span = reinterpret_cast<int4*>(take(sizeof(int4) * kPagedMaxParts));
-  x.part_ml = reinterpret_cast<float*>(take(sizeof(float) * 2 * rows));
-  x.part_o = reinterpret_cast<float*>(take(sizeof(float) * kHeadDim * rows));
+  x.span = reinterpret_cast<int4*>(take(sizeof(int4) * (kPagedMaxParts + kPagedMaxFew)));
+  x.left = reinterpret_cast<int*>(take(sizeof(int)));
+  for (int i = 0; i < 2; ++i) {
+    x.kinds[i].ml = reinterpret_cast<float*>(take(sizeof(float) * 2 * rows[i]));
+    x.kinds[i].o = reinterpret_cast<float*>(take(sizeof(float) * kHeadDim * rows[i]));
+  }
   if (weigh) {
     const int64_t tiles = ceil_div(max_len, 128) + 2, small = ceil_div(max_len, 16) + 2;
     x.geo = reinterpret_cast<int4*>(take(sizeof(int4) * tokens));
@@ -294,7 +398,7 @@ size_t paged_workspace_bytes(int n_tokens, int n_kv_heads, int64_t max_len, int 
     x.e_blocks = tiles * (128 >> r_shift);
   }
   if (a != nullptr) {
-    a->span = x.span, a->part_ml = x.part_ml, a->part_o = x.part_o;
+    a->span = x.span, a->left = x.left, a->kinds[0] = x.kinds[0], a->kinds[1] = x.kinds[1];
     a->geo = x.geo, a->lse = x.lse, a->em = x.em, a->e = x.e, a->e_tiles = x.e_tiles, a->e_blocks = x.e_blocks;
   }
   return at;
@@ -304,6 +408,9 @@ cudaError_t launch_paged_attn(const PagedArgs& args, int kv_type, unsigned* err,
   // the plan of a launch is held in shared memory, its tiles are counted in 31 bits
   const int64_t most = (INT64_C(1) << 31) / (ceil_div(args.max_len, 16) + 2) - 1, cap = args.weigh ? kPagedWeigh : kPagedPlan;
   const int chunk = (int)(most < cap ? most : cap);
+  int sms = 0;
+  cudaError_t e = multiprocessors(&sms);
+  if (e != cudaSuccess) return e;
   for (int t = 0; t < args.n_tokens; t += chunk) {
     PagedArgs a = args;
     a.n_tokens = args.n_tokens - t < chunk ? args.n_tokens - t : chunk;
@@ -312,12 +419,8 @@ cudaError_t launch_paged_attn(const PagedArgs& args, int kv_type, unsigned* err,
     a.q += (int64_t)t * a.n_kv_heads * kGqa * kHeadDim;
     a.out += (int64_t)t * a.n_kv_heads * kGqa * kHeadDim;
     prof_before(kKPaged, stream);
-    const int group = paged_group(a, kv_type);
-    cudaError_t e = group == 1    ? launch_paged_one(a, kv_type, err, stream)
-                    : group == 16 ? launch_paged_few(a, kv_type, err, stream)
-                                  : launch_paged_prompt(a, err, stream);
+    e = launch_tokens(a, route(a, args.n_tokens, kv_type), kv_type, sms, err, stream);
     if (e == cudaSuccess && a.weigh) {
-      a.e_cells = group == 1 ? 16 : 64;
       const int64_t blocks = std::max<int64_t>(ceil_div(ceil_div(a.max_len, (int64_t)1 << a.r_shift), kWeighEntries), 1);
       // a block a token while they are few: most start no sequence, and each sequence is a chain of loads
       const int64_t shares = std::max<int64_t>(std::min<int64_t>(a.n_tokens, kWeighBlocks / blocks), ceil_div(a.n_tokens, 8));

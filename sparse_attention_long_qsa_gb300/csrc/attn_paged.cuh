@@ -59,12 +59,33 @@ __device__ __forceinline__ int pos_of(const Group& g, int v) { return v < g.ns_a
 // Shared memory that the plan takes while it is made, and where it leaves its parts.
 constexpr int kPlanWords = kPagedPlan / 32;
 constexpr int kPlanScratch = (3 * kPagedPlan + 3 * kPlanWords + 4) * 4;
+constexpr int kLeaves = 1 << 30;   // beside a word's largest group: some tokens are the other launch's
 // The tiles of a launch dealt to `parts` runs of them; what this CTA starts with.
 struct Plan {
   int all, parts;      // tiles; parts that have any
   int u0, u1;          // this part's tiles
   int t0, first;       // the group of tile u0, and which of the group's tiles it is
 };
+template <bool kMixed>
+struct PlanOf : Plan {};
+template <>
+struct PlanOf<true> : Plan {
+  unsigned firsts[kPlanWords];   // the first tokens of this launch's groups
+};
+// The launch's group at token t or behind it.
+template <bool kMixed>
+__device__ __forceinline__ int next_group(const PagedArgs& a, const PlanOf<kMixed>& p, int t) {
+  if constexpr (kMixed) {
+    const int words = (a.n_tokens + 31) >> 5;
+    int w = t >> 5;
+    if (w >= words) return t;
+    unsigned x = p.firsts[w] & (~0u << (t & 31));
+    while (x == 0u && ++w < words) x = p.firsts[w];
+    return x ? 32 * w + __ffs((int)x) - 1 : a.n_tokens;
+  } else {
+    return t;
+  }
+}
 
 // all * part / parts, in 32 bits (part <= parts <= 2^15).
 __device__ __forceinline__ int share_of(int all, int part, int parts) {
@@ -79,8 +100,10 @@ __device__ __forceinline__ int share_of(int all, int part, int parts) {
 // tokens of 20,000 each 536 -> 782, of which some parts would have two).
 // A warp takes 32 tokens at a time (a word of flags: which of them start a run); what crosses words is scanned by one warp.
 // (4,096 tokens: 10 us, 512: 3, one: 1.)
-template <int NT, int kCells>
-__device__ __forceinline__ void plan(const PagedArgs& a, int* scratch, Plan* out, int tid, int part, int max_parts, int least, int uncut, int more) {
+// kMixed: of the runs in [run_lo + 1, run_hi] only.
+template <int NT, int kCells, bool kMixed>
+__device__ __forceinline__ void plan(const PagedArgs& a, int* scratch, PlanOf<kMixed>* out, int tid, int part, int max_parts, int least, int uncut,
+                                     int more) {
   const int lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, n = a.n_tokens, words = (n + 31) >> 5;
   int* seq = scratch;
   int* pos = seq + kPagedPlan;
@@ -88,6 +111,11 @@ __device__ __forceinline__ void plan(const PagedArgs& a, int* scratch, Plan* out
   unsigned* starts = reinterpret_cast<unsigned*>(pre + kPagedPlan);
   int* last = reinterpret_cast<int*>(starts + kPlanWords);   // the last start before each word
   int* sum = last + kPlanWords;             // tiles before each word, then all, and the largest group's
+  if (kMixed && a.second && !*a.left) {   // nothing to do
+    if (tid == 0) out->u0 = out->u1 = 0;
+    __syncthreads();
+    return;
+  }
   Plan p;
   p.t0 = 0;
   int longest = 0;
@@ -108,10 +136,21 @@ __device__ __forceinline__ void plan(const PagedArgs& a, int* scratch, Plan* out
     __syncthreads();
     for (int w = warp; w < words; w += warps) {
       const int t = 32 * w + lane;
-      const unsigned f = __ballot_sync(kFull, t < n && (t == 0 || new_run(seq[t], pos[t], seq[t - 1], pos[t - 1])));
+      const unsigned f = __ballot_sync(kFull, (kMixed && t >= n) || (t < n && (t == 0 || new_run(seq[t], pos[t], seq[t - 1], pos[t - 1]))));
       if (lane == 0) starts[w] = f;
     }
     __syncthreads();
+    // the 32 tokens from t on: which start a run
+    auto starts_from = [&](int t) {
+      const int w = t >> 5;
+      return __funnelshift_r(w < words ? starts[w] : ~0u, w + 1 < words ? starts[w + 1] : ~0u, t & 31);
+    };
+    // whether a run that starts at t is this launch's
+    auto takes = [&](int t) {
+      const unsigned f = starts_from(t + 1);
+      const int len = f ? __ffs((int)f) : 33;   // (or more)
+      return len > a.run_lo && len <= a.run_hi;
+    };
     constexpr int kEach = kPlanWords / 32;   // words of a lane
     if (warp == 0) {
       int at[kEach], x = -1;
@@ -136,9 +175,12 @@ __device__ __forceinline__ void plan(const PagedArgs& a, int* scratch, Plan* out
     for (int w = warp; w < words; w += warps) {
       const int t = 32 * w + lane;
       int m = 0;
+      bool left = false;   // to the other launch
       Group g;
       if constexpr (NT == 1) {
-        if (t < n) {
+        if (kMixed && t < n)   // (runs of at most two tokens: the first, or the second)
+          left = starts[w] >> lane & 1u ? !takes(t) : a.run_hi < 2 || (starts_from(t - 1) & 7u) != 5u;
+        if (t < n && !left) {
           g.pmin = g.pmax = pos[t];
           g.seq = g.pmin < 0 ? -1 : seq[t];
           reach<kCells>(a, g);
@@ -153,6 +195,10 @@ __device__ __forceinline__ void plan(const PagedArgs& a, int* scratch, Plan* out
           groups &= groups - 1u;
           const unsigned cut = __ballot_sync(kFull, lane > 0 && (x >= n || (starts[x >> 5] >> (x & 31) & 1u)));
           const int len = min(cut ? __ffs((int)cut) - 1 : 32, NT), q = lane < len ? pos[x] : 0;
+          if (kMixed && (starts[w] >> b & 1u ? !takes(t0) : a.run_hi <= NT)) {   // (a group further on: a run of more than NT)
+            left = true;
+            continue;
+          }
           g.pmin = __reduce_min_sync(kFull, lane < len ? q : 0x7fffffff);
           g.pmax = __reduce_max_sync(kFull, lane < len ? q : -1);
           g.seq = g.pmin < 0 ? -1 : seq[t0];
@@ -161,6 +207,7 @@ __device__ __forceinline__ void plan(const PagedArgs& a, int* scratch, Plan* out
         }
       }
       const int top = __reduce_max_sync(kFull, m);
+      const unsigned firsts = kMixed ? __ballot_sync(kFull, m > 0) : 0u, leaves = kMixed ? __ballot_sync(kFull, left) : 0u;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(kFull, m, o);
@@ -169,19 +216,27 @@ __device__ __forceinline__ void plan(const PagedArgs& a, int* scratch, Plan* out
       if (t < n) pre[t] = m;
       if (lane == 31) {
         sum[w] = m;
-        last[w] = top;   // (by now this word's last start has been read)
+        last[w] = top | (kMixed && leaves ? kLeaves : 0);   // (by now this word's last start has been read)
+        if constexpr (kMixed) out->firsts[w] = firsts;
       }
     }
     __syncthreads();
     if (warp == 0) {
       int at[kEach], x = 0, top = 0;
+      unsigned leaves = 0u;
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
         at[i] = x;
         x += kEach * lane + i < words ? sum[kEach * lane + i] : 0;
-        top = max(top, kEach * lane + i < words ? last[kEach * lane + i] : 0);
+        const int y = kEach * lane + i < words ? last[kEach * lane + i] : 0;
+        top = max(top, kMixed ? y & (kLeaves - 1) : y);
+        if (kMixed) leaves |= y & kLeaves;
       }
       top = __reduce_max_sync(kFull, top);
+      if (kMixed && !a.second) {
+        leaves = __reduce_or_sync(kFull, leaves);
+        if (blockIdx.x == 0 && lane == 0) *a.left = leaves;
+      }
       const int own = x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -202,6 +257,7 @@ __device__ __forceinline__ void plan(const PagedArgs& a, int* scratch, Plan* out
   }
   // each has a tile; no fewer than tokens, whose runs would each wait for memory (12 tokens of 4 positions 24 -> 13 us)
   p.parts = min(max_parts, max(p.all / least, min(n, p.all)));
+  if (kMixed) p.parts = max(p.parts, 1);
   const int enough = p.all / p.parts + more;
   if (longest <= more) {   // (a part gets less than a group more than its share)
     uncut = max(uncut, longest);
@@ -252,7 +308,7 @@ __device__ __forceinline__ void plan(const PagedArgs& a, int* scratch, Plan* out
     if (p.u0 < p.u1) p.t0 = group_of(p.u0, begin, tiles);
     p.first = p.u0 - begin;
   }
-  if (tid == 0) *out = p;
+  if (tid == 0) static_cast<Plan&>(*out) = p;
   __syncthreads();   // the scratch is free
 }
 
@@ -310,7 +366,7 @@ __device__ __forceinline__ void announce(const PagedArgs& a, const Plan& p, cons
     return x;
   };
   const int64_t begin = (int64_t)u - r.first;
-  const int4 span = make_int4(r.g.t0, r.g.nt, r.first == 0 ? part : part_of(begin), part_of(begin + r.g.tiles - 1));
+  const int4 span = make_int4(r.g.t0, r.g.nt | (a.kind << 8), r.first == 0 ? part : part_of(begin), part_of(begin + r.g.tiles - 1));
   if (a.span_by_token ? lane < r.g.nt : lane == 0) a.span[a.span_by_token ? r.g.t0 + lane : part] = span;
 }
 // The slot of the block of the group's position v (in reading order), -1: not read.

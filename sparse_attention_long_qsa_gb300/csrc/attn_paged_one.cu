@@ -49,7 +49,7 @@ template <> struct Row<QSA_KV_F16> { static constexpr int kCodes = 512, kPitch =
 template <> struct Row<QSA_KV_Q8_0> { static constexpr int kCodes = 256, kPitch = 272, kWarps = 12; };
 template <> struct Row<QSA_KV_Q4_0> { static constexpr int kCodes = 128, kPitch = 144, kWarps = 16; };
 
-template <int KV>
+template <int KV, bool kMixed>
 struct Smem {
   using R = Row<KV>;
   static constexpr int kHalf = kChunk * R::kPitch;
@@ -58,7 +58,7 @@ struct Smem {
   uint2 vd[R::kWarps][kBlocks][4];               // a chunk's V scales: block, l4 -> cells 2 l4 + {0, 1, 8, 9}
   float m[R::kWarps][kGqa], l[R::kWarps][kGqa];
   float ml[2][kGqa];                             // the run's (max, sum)
-  Plan plan;
+  PlanOf<kMixed> plan;
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -132,11 +132,11 @@ __device__ __forceinline__ __half2 pow2h(int k) {
   return half2_of(e | (e << 16));
 }
 
-template <int KV>
+template <int KV, bool kMixed>
 __global__ void __launch_bounds__(Row<KV>::kWarps * 32, 1) k_paged_one(const PagedArgs a, unsigned* err) {
   extern __shared__ unsigned char smem_raw[];
   using R = Row<KV>;
-  using S = Smem<KV>;
+  using S = Smem<KV, kMixed>;
   S& sm = *reinterpret_cast<S*>(smem_raw);
   constexpr int kWarps = R::kWarps, kThreads = 32 * kWarps, kCodes = R::kCodes, kPitch = R::kPitch;
   constexpr bool kF16 = KV == QSA_KV_F16;
@@ -147,8 +147,8 @@ __global__ void __launch_bounds__(Row<KV>::kWarps * 32, 1) k_paged_one(const Pag
 
   grid_dep_wait();
   grid_dep_launch();
-  plan<1, kChunk>(a, reinterpret_cast<int*>(sm.stage), &sm.plan, tid, part, gridDim.x / G, kMinChunks, kWarps, 2 * kWarps);   // (a chunk a warp)
-  const Plan& pl = sm.plan;
+  plan<1, kChunk, kMixed>(a, reinterpret_cast<int*>(sm.stage), &sm.plan, tid, part, gridDim.x / G, kMinChunks, kWarps, 2 * kWarps);   // (a chunk a warp)
+  const PlanOf<kMixed>& pl = sm.plan;
   if (tid == 0 && g == 0 && !a.span_by_token) a.span[part] = make_int4(0, 0, 0, 0);
 
   const unsigned char* kc = static_cast<const unsigned char*>(a.k_cache) + g * kCodes;
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(Row<KV>::kWarps * 32, 1) k_paged_one(const Pag
     const int t0 = gr.t0, n = run.n, v_end = min(gr.nv, (run.first + n) * kChunk);
     if (warp == 0 && g == 0) announce(a, pl, run, part, u, err);
     u += n;
-    t_next = t0 + 1;
+    t_next = next_group<kMixed>(a, pl, t0 + 1);
     first_next = 0;
 
     // ---- ids: position -> slot -> cell, a step of the warp's chunks apart; lanes i and i + 16 hold cell i
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(Row<KV>::kWarps * 32, 1) k_paged_one(const Pag
     __syncthreads();
     const bool whole = n == gr.tiles;
     const int64_t ps = ((int64_t)(2 * part + (run.first == 0 ? 1 : 0)) * G + g) * kGqa;   // the run's rows in the workspace
-    float* out = whole ? a.out + ((int64_t)t0 * G + g) * kGqa * kHeadDim : a.part_o + ps * kHeadDim;
+    float* out = whole ? a.out + ((int64_t)t0 * G + g) * kGqa * kHeadDim : a.of.o + ps * kHeadDim;
     const bool wide = (reinterpret_cast<uintptr_t>(out) & 15u) == 0u;
     float odd = 0.f;   // zero, or NaN
     for (int i = tid; i < kGqa * kHeadDim / 4; i += kThreads) {
@@ -602,46 +602,44 @@ __global__ void __launch_bounds__(Row<KV>::kWarps * 32, 1) k_paged_one(const Pag
     }
     if (tid < kGqa) {
       const float m = sm.ml[0][tid], l = sm.ml[1][tid];
-      if (!whole) *reinterpret_cast<float2*>(a.part_ml + 2 * (ps + tid)) = make_float2(m, l);
+      if (!whole) *reinterpret_cast<float2*>(a.of.ml + 2 * (ps + tid)) = make_float2(m, l);
       else if (a.weigh) a.lse[((int64_t)t0 * G + g) * kGqa + tid] = make_float2(m, l != 0.f ? 1.f / l : 0.f);
     }
-    if (a.weigh && tid == 0 && g == 0 && run.first == 0) a.geo[t0] = make_int4(gr.ns_al, gr.lo_al, gr.nv, gr.seq);
+    if (a.weigh && tid == 0 && g == 0 && run.first == 0) a.geo[t0] = make_int4(gr.ns_al, gr.lo_al, gr.nv, kChunk);
   }
 }
 
 constexpr int kMaxDevices = 64;
 
-template <int KV>
-cudaError_t launch(PagedArgs a, unsigned* err, cudaStream_t stream) {
-  static std::atomic<int> known[kMaxDevices];
+template <int KV, bool kMixed>
+cudaError_t launch(const PagedArgs& a, unsigned* err, cudaStream_t stream) {
+  static std::atomic<bool> known[kMaxDevices];
   static std::mutex mu;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  int sms = known[dev].load(std::memory_order_acquire);
-  if (sms == 0) {
+  if (!known[dev].load(std::memory_order_acquire)) {
     std::lock_guard<std::mutex> lock(mu);
-    e = cudaFuncSetAttribute(k_paged_one<KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<KV>));
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    e = cudaFuncSetAttribute(k_paged_one<KV, kMixed>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<KV, kMixed>));
     if (e != cudaSuccess) return e;
-    known[dev].store(sms, std::memory_order_release);
+    known[dev].store(true, std::memory_order_release);
   }
-  const int64_t parts = paged_launch_parts(a, sms, kPagedMaxParts, kChunk * kMinChunks);
-  a.span_by_token = a.n_tokens <= parts;
-  a.part_tokens = 1;
-  e = launch_pdl(k_paged_one<KV>, dim3((unsigned)(parts * a.n_kv_heads)), dim3(Row<KV>::kWarps * 32), sizeof(Smem<KV>), stream, 1, a,
-                 err);
-  if (e == cudaSuccess && parts > 1) e = launch_paged_join(a, parts, stream);
-  return e;
+  return launch_pdl(k_paged_one<KV, kMixed>, dim3((unsigned)(a.of.parts * a.n_kv_heads)), dim3(Row<KV>::kWarps * 32), sizeof(Smem<KV, kMixed>), stream, 1,
+                    a, err);
+}
+
+template <int KV>
+cudaError_t launch_kv(const PagedArgs& a, bool mixed, unsigned* err, cudaStream_t stream) {
+  return mixed ? launch<KV, true>(a, err, stream) : launch<KV, false>(a, err, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_one(const PagedArgs& a, int kv_type, unsigned* err, cudaStream_t stream) {
-  return kv_type == QSA_KV_F16    ? launch<QSA_KV_F16>(a, err, stream)
-         : kv_type == QSA_KV_Q8_0 ? launch<QSA_KV_Q8_0>(a, err, stream)
-                                  : launch<QSA_KV_Q4_0>(a, err, stream);
+cudaError_t launch_paged_one(const PagedArgs& a, int kv_type, bool mixed, unsigned* err, cudaStream_t stream) {
+  return kv_type == QSA_KV_F16    ? launch_kv<QSA_KV_F16>(a, mixed, err, stream)
+         : kv_type == QSA_KV_Q8_0 ? launch_kv<QSA_KV_Q8_0>(a, mixed, err, stream)
+                                  : launch_kv<QSA_KV_Q4_0>(a, mixed, err, stream);
 }
 
 }  // namespace qsa

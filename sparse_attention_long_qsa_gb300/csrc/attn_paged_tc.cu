@@ -56,6 +56,7 @@ constexpr int kSuper = 512;                  // cells whose ids are looked up to
 constexpr uint32_t kColS = 256;
 constexpr int kAdditions = 16;               // to O, of a tile
 
+template <bool kMixed>
 struct Smem {
   alignas(1024) unsigned char q[128 * 512];
   alignas(1024) unsigned char stage[kStages][kStageBytes];
@@ -66,12 +67,13 @@ struct Smem {
   uint32_t ok[4][kSuper / 32];               // which of them exist
   uint64_t landed[kStages], full[kStages], s_full[2], p_full[2], pv_done[2], q_full;
   uint32_t tmem;
-  Plan plan;
+  PlanOf<kMixed> plan;
   unsigned stray[4];                         // of a run: such V values were met (see above)
 };
 static_assert(kStages * kStageBytes >= kPlanScratch, "the plan's scratch");
-constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
-static_assert(kSmemBytes <= 227 * 1024, "shared memory of an SM");
+template <bool kMixed>
+constexpr size_t kSmemBytes = sizeof(Smem<kMixed>) + 1024;
+static_assert(kSmemBytes<true> <= 227 * 1024, "shared memory of an SM");
 
 // kind::f16, fp32 accumulators, M = 256 over the pair; B K-major (scores) or MN-major (P V)
 constexpr uint32_t kIdescS = (1u << 4) | (((uint32_t)kCells >> 3) << 17) | ((256u >> 4) << 24);
@@ -126,9 +128,10 @@ __device__ __forceinline__ bool edge_tile(const Group& g, int window, int v0) {
   return g.nt > 1 && (pos_of(g, v0 + kCells - 1) > g.pmin || (window > 0 && pos_of(g, max(v0, g.ns_al)) <= g.pmax - window));
 }
 // (bounds of 640 threads: 96 registers, so that the five warps of one sub-partition fit)
+template <bool kMixed>
 __global__ void __launch_bounds__(640, 1) k_paged_prompt(const PagedArgs a, unsigned* err) {
   extern __shared__ unsigned char raw[];
-  Smem& sm = *reinterpret_cast<Smem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
+  Smem<kMixed>& sm = *reinterpret_cast<Smem<kMixed>*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);
   const int G = a.n_kv_heads, rank = (int)cluster_rank(), g = (blockIdx.x >> 1) % G, part = (blockIdx.x >> 1) / G;
   const bool reports = g == 0 && rank == 0;
@@ -141,6 +144,15 @@ __global__ void __launch_bounds__(640, 1) k_paged_prompt(const PagedArgs a, unsi
   // the even CTA's, where the products are issued
   const uint32_t lfull = dsmem_addr(sm.full, 0), lp = dsmem_addr(sm.p_full, 0), lq = dsmem_addr(&sm.q_full, 0);
 
+  if constexpr (kMixed) {   // nothing to do: before anything is set up
+    if (a.second) {
+      grid_dep_wait();
+      if (!*a.left) {
+        if (tid == 0 && reports && !a.span_by_token) a.span[part] = make_int4(0, 0, 0, 0);
+        return;
+      }
+    }
+  }
   if (warp == 0) pair_alloc(smem_u32(&sm.tmem));
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -157,9 +169,9 @@ __global__ void __launch_bounds__(640, 1) k_paged_prompt(const PagedArgs a, unsi
   }
   grid_dep_wait();
   grid_dep_launch();
-  plan<kNT, kCells>(a, reinterpret_cast<int*>(sm.stage[0]), &sm.plan, tid, part, (int)(gridDim.x >> 1) / G, 1, kUncut,
+  plan<kNT, kCells, kMixed>(a, reinterpret_cast<int*>(sm.stage[0]), &sm.plan, tid, part, (int)(gridDim.x >> 1) / G, 1, kUncut,
                     a.n_tokens > (int)(gridDim.x >> 1) / G ? 6 + a.n_tokens / 128 : kUncut);
-  const Plan& pl = sm.plan;
+  const PlanOf<kMixed>& pl = sm.plan;
   tc_fence_before();
   __syncthreads();
   cluster_sync();   // both CTAs' barriers exist
@@ -177,7 +189,7 @@ __global__ void __launch_bounds__(640, 1) k_paged_prompt(const PagedArgs a, unsi
       u += run.n;
       base += run.n;
       chunks += (run.n + kSuper / kCells - 1) / (kSuper / kCells);
-      t0 = run.g.t0 + run.g.nt;
+      t0 = next_group<kMixed>(a, pl, run.g.t0 + run.g.nt);
       first = 0;
     }
   };
@@ -216,7 +228,7 @@ __global__ void __launch_bounds__(640, 1) k_paged_prompt(const PagedArgs a, unsi
       const int vsink = gr.lo_al == 0 || gr.ns_al > 0 ? min(min(a.n_sink, pos + 1), gr.nv) : 0;
       const bool whole = n == gr.tiles;
       const int64_t ps = ((int64_t)(2 * part + (run.first == 0 ? 1 : 0)) * G + g) * (kNT * kGqa);   // the run's rows
-      float* sums = a.part_o + ps * kHeadDim + 128 * half;
+      float* sums = a.of.o + ps * kHeadDim + 128 * half;
       const int stretch = stretch_of(n, kAdditions);
       int next = stretch;   // where the next one begins
       float fs = 0.f;       // of the stretches' sums so far
@@ -335,11 +347,11 @@ __global__ void __launch_bounds__(640, 1) k_paged_prompt(const PagedArgs a, unsi
       // ---- the run's result: a row of 256 values, 128 a thread
       if (!mbar_wait(bpv + 8 * ((base + n - 1) & 1), (uint32_t)((base + n - 1) >> 1) & 1u)) timed_out = true;
       tc_fence_after();
-      if (u + n < pl.u1) load_q(run_at<kNT, kCells>(a, gr.t0 + gr.nt, 0, 1).g);   // scores of the next run form meanwhile
+      if (u + n < pl.u1) load_q(run_at<kNT, kCells>(a, next_group<kMixed>(a, pl, gr.t0 + gr.nt), 0, 1).g);   // scores of the next run form meanwhile
       sm.sum[half][row] = l;
       bar_named(2 + quarter, 64);
       l = sm.sum[0][row] + sm.sum[1][row];
-      if (tok < gr.nt && !whole && half == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * (ps + tok * kGqa + head)) = make_float2(m, l);
+      if (tok < gr.nt && !whole && half == 0) *reinterpret_cast<float2*>(a.of.ml + 2 * (ps + tok * kGqa + head)) = make_float2(m, l);
       const float w = whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
       float* rows = whole ? a.out + ((int64_t)gr.t0 * G + g) * kGqa * kHeadDim + 128 * half : sums;
       const int64_t stride = (whole ? G : 1) * (kGqa * kHeadDim);
@@ -512,29 +524,28 @@ __global__ void __launch_bounds__(640, 1) k_paged_prompt(const PagedArgs a, unsi
 
 constexpr int kMaxDevices = 64;
 
-}  // namespace
-
-cudaError_t launch_paged_prompt(PagedArgs a, unsigned* err, cudaStream_t stream) {
-  static std::atomic<int> known[kMaxDevices];
+template <bool kMixed>
+cudaError_t launch(const PagedArgs& a, unsigned* err, cudaStream_t stream) {
+  static std::atomic<bool> known[kMaxDevices];
   static std::mutex mu;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  int sms = known[dev].load(std::memory_order_acquire);
-  if (sms == 0) {
+  if (!known[dev].load(std::memory_order_acquire)) {
     std::lock_guard<std::mutex> lock(mu);
-    e = cudaFuncSetAttribute(k_paged_prompt, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    e = cudaFuncSetAttribute(k_paged_prompt<kMixed>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<kMixed>);
     if (e != cudaSuccess) return e;
-    known[dev].store(sms, std::memory_order_release);
+    known[dev].store(true, std::memory_order_release);
   }
-  const int64_t parts = paged_launch_parts(a, sms / 2, kPagedMaxPairs, kCells);
-  a.span_by_token = a.n_tokens <= parts;
-  a.part_tokens = kNT;
-  e = launch_pdl(k_paged_prompt, dim3((unsigned)(2 * parts * a.n_kv_heads)), dim3(kThreads), kSmemBytes, stream, 2, a, err);
-  if (e == cudaSuccess && parts > 1) e = launch_paged_join(a, parts, stream);
-  return e;
+  return launch_pdl(k_paged_prompt<kMixed>, dim3((unsigned)(2 * a.of.parts * a.n_kv_heads)), dim3(kThreads), kSmemBytes<kMixed>, stream, 2,
+                    a, err);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_prompt(const PagedArgs& a, bool mixed, unsigned* err, cudaStream_t stream) {
+  return mixed ? launch<true>(a, err, stream) : launch<false>(a, err, stream);
 }
 
 }  // namespace qsa

@@ -27,8 +27,15 @@ constexpr int kPagedWeigh = 64;        // with block weights, whose workspace gr
 constexpr int kPagedMaxParts = 320;    // CTAs of one launch
 constexpr int kPagedMaxPairs = 80;     // pairs of CTAs
 constexpr int kPagedMaxFew = 160;      // CTAs that take an SM each
+constexpr int kPagedOneCells = 64, kPagedFewCells = 64, kPagedPromptCells = 128;   // cells of a part at least
 constexpr int kPagedNear = 8;          // neighbouring tokens further apart than this do not share a group
 constexpr int kPagedMaxLen = 1 << 30;  // positions of a sequence
+// Partial results, (max, sum) and sums: of each of a launch's parts two runs of `tokens` tokens.
+struct PagedPartials {
+  float* ml;
+  float* o;
+  int tokens, parts;
+};
 struct PagedArgs {
   int n_tokens;
   int n_kv_heads;
@@ -57,29 +64,24 @@ struct PagedArgs {
   // a launch has no more tokens than parts, else one per part (all of them but the last)
   int4* span;
   int span_by_token;
-  int part_tokens;          // tokens of a partial result
-  float* part_ml;
-  float* part_o;
-  int4* geo;                // per token: sinks, window start, positions read, sequence
+  PagedPartials of;         // of this launch's parts, at most
+  PagedPartials kinds[2];   // of both, for the join
+  int4* geo;                // per token: sinks, window start, positions read, cells of a tile
   float2* lse;              // per row: max, 1 / sum
   float* em;                // per row and tile: its largest score
   float* e;                 // per row and block: its sum relative to that
   int64_t e_tiles, e_blocks;
-  int e_cells;              // cells of a tile there
+  // Of two launches that share a call's tokens (kMixed) each takes runs of neighbouring tokens of more than run_lo and at
+  // most run_hi of them; the first leaves word in `left` whether there are others.  kind 0: tokens one by one, 1: groups.
+  int run_lo, run_hi, second, kind;
+  int* left;
 };
-// Tokens that share a group at most, by what a call's sequences have on average.
-int paged_group(const PagedArgs& a, int kv_type);
-// Runs that each KV head's tiles of so many cells are dealt in, by `ctas` CTAs (or pairs), at most
-// most_ctas of them.
-int64_t paged_launch_parts(const PagedArgs& a, int64_t ctas, int64_t most_ctas, int cells);
-// Adds the partial results of groups that several of the parts share (attn_paged.cu).
-cudaError_t launch_paged_join(const PagedArgs& a, int64_t parts, cudaStream_t stream);
-// One token of a sequence (attn_paged_one.cu).
-cudaError_t launch_paged_one(const PagedArgs& a, int kv_type, unsigned* err, cudaStream_t stream);
-// Two tokens and more (attn_paged_few.cu).
+// Tokens one by one (attn_paged_one.cu), in groups of 16 (attn_paged_few.cuh; kMixed: attn_paged_few_mixed.cu), in groups of
+// 32 on pairs of CTAs, fp16 rows (attn_paged_tc.cu): the kernel, in a.of.parts parts.
+cudaError_t launch_paged_one(const PagedArgs& a, int kv_type, bool mixed, unsigned* err, cudaStream_t stream);
 cudaError_t launch_paged_few(const PagedArgs& a, int kv_type, unsigned* err, cudaStream_t stream);
-// Many tokens of a sequence, fp16 rows (attn_paged_tc.cu).
-cudaError_t launch_paged_prompt(PagedArgs a, unsigned* err, cudaStream_t stream);
+cudaError_t launch_paged_few_mixed(const PagedArgs& a, int kv_type, unsigned* err, cudaStream_t stream);
+cudaError_t launch_paged_prompt(const PagedArgs& a, bool mixed, unsigned* err, cudaStream_t stream);
 size_t paged_workspace_bytes(int n_tokens, int n_kv_heads, int64_t max_len, int r_shift, bool weigh, PagedArgs* a, void* ws);
 cudaError_t launch_paged_attn(const PagedArgs& a, int kv_type, unsigned* err, cudaStream_t stream);
 
