@@ -163,17 +163,22 @@ __global__ void __launch_bounds__(kJoinThreads, 2) k_paged_join(const PagedArgs 
 // 250k: 20 MB of block sums, 14 us; with one entry a lane and its loads one after the
 // other it took 26.)
 constexpr int kWeighThreads = 256, kWeighWarps = kWeighThreads / 32, kWeighBlocks = 2048, kWeighEntries = 64;
-__global__ void __launch_bounds__(kWeighThreads) k_paged_weigh(const PagedArgs a) {
+template <bool kMixed>
+__global__ void __launch_bounds__(kWeighThreads) k_paged_weigh(const PagedArgs a, int tile_cells) {
   __shared__ float part[2][kWeighWarps][kWeighEntries];
   __shared__ int seq_of[kPagedWeigh], tok[kPagedWeigh];   // of all tokens; the sequence's
   __shared__ int4 geo[kPagedWeigh];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = a.n_kv_heads, heads = G * kGqa;
+  const int one_tile = 31 - __clz(tile_cells) - a.r_shift;   // (the same for all tokens)
   grid_dep_wait();
   grid_dep_launch();
   if (tid < kPagedWeigh) {
     const int s = tid < a.n_tokens ? a.tok_seq[tid] : -1;
     seq_of[tid] = tid < a.n_tokens && token_pos(a, tid) >= 0 ? s : -1;
-    if (tid < a.n_tokens) geo[tid] = a.geo[tid];
+    if (tid < a.n_tokens) {
+      geo[tid] = a.geo[tid];
+      if (kMixed) geo[tid].w = 31 - __clz(geo[tid].w) - a.r_shift;   // log2 of the blocks of a tile
+    }
   }
   __syncthreads();
   const int share = (a.n_tokens + gridDim.y - 1) / gridDim.y;
@@ -204,7 +209,6 @@ __global__ void __launch_bounds__(kWeighThreads) k_paged_weigh(const PagedArgs a
           const int t = tok[row_there ? k : 0];
           const int4 at = geo[t];
           const int ns = at.x >> a.r_shift, lo = at.y >> a.r_shift;
-          const int to_tile = 31 - __clz(at.w) - a.r_shift;   // (blocks of a tile: a power of two)
           const int64_t row = (int64_t)t * heads + h * kWeighWarps + warp;
           l[i] = a.lse[row];
 #pragma unroll
@@ -215,7 +219,7 @@ __global__ void __launch_bounds__(kWeighThreads) k_paged_weigh(const PagedArgs a
             if (there) have |= 1u << (2 * i + c);
             else b = 0;   // (read, and not used)
             e[i][c] = a.e[row * a.e_blocks + b];
-            m[i][c] = a.em[row * a.e_tiles + (b >> to_tile)];
+            m[i][c] = a.em[row * a.e_tiles + (b >> (kMixed ? at.w : one_tile))];
           }
           if (row_there && ++h == heads / kWeighWarps) h = 0, ++k;
         }
@@ -419,13 +423,15 @@ cudaError_t launch_paged_attn(const PagedArgs& args, int kv_type, unsigned* err,
     a.q += (int64_t)t * a.n_kv_heads * kGqa * kHeadDim;
     a.out += (int64_t)t * a.n_kv_heads * kGqa * kHeadDim;
     prof_before(kKPaged, stream);
-    e = launch_tokens(a, route(a, args.n_tokens, kv_type), kv_type, sms, err, stream);
+    const Route r = route(a, args.n_tokens, kv_type);
+    e = launch_tokens(a, r, kv_type, sms, err, stream);
     if (e == cudaSuccess && a.weigh) {
       const int64_t blocks = std::max<int64_t>(ceil_div(ceil_div(a.max_len, (int64_t)1 << a.r_shift), kWeighEntries), 1);
       // a block a token while they are few: most start no sequence, and each sequence is a chain of loads
       const int64_t shares = std::max<int64_t>(std::min<int64_t>(a.n_tokens, kWeighBlocks / blocks), ceil_div(a.n_tokens, 8));
-      e = launch_pdl(k_paged_weigh, dim3((unsigned)std::min<int64_t>(blocks, kWeighBlocks), (unsigned)shares), dim3(kWeighThreads), 0,
-                     stream, 1, a);
+      const dim3 grid((unsigned)std::min<int64_t>(blocks, kWeighBlocks), (unsigned)shares);
+      e = launch_pdl(r.mixed ? k_paged_weigh<true> : k_paged_weigh<false>, grid, dim3(kWeighThreads), 0, stream, 1, a,
+                     r.kernel == Route::kOne ? 16 : 64);
     }
     prof_after(kKPaged, stream);
     if (e != cudaSuccess) return e;

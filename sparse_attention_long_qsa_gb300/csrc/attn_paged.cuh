@@ -10,6 +10,21 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kNoMax = -3.0e38f;         // no cell seen yet (below every score, and finite)
 
+__device__ __forceinline__ uint32_t bits(__half2 h) {
+  uint32_t u;
+  memcpy(&u, &h, 4);
+  return u;
+}
+__device__ __forceinline__ __half2 half2_of(uint32_t u) {
+  __half2 h;
+  memcpy(&h, &u, 4);
+  return h;
+}
+// Bytes (i, j) of x as halves less `off` (bits of a half): a byte put under the exponent of 1024 is 1024 + it, exactly.
+template <int kSel>
+__device__ __forceinline__ __half2 bytes2(uint32_t x, uint32_t off) {
+  return __hsub2(half2_of(__byte_perm(x, 0x64646464u, kSel)), half2_of(off));
+}
 // 2^x; results below the normal range are zero
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -395,9 +410,7 @@ __device__ __forceinline__ int checked_cell(const PagedArgs& a, int c, bool repo
 
 // Adds those of two halves that are infinite or NaN to (x, y).
 __device__ __forceinline__ void add_not_finite(float& x, float& y, uint32_t w) {
-  __half2 h;
-  memcpy(&h, &w, 4);
-  const float2 v = __half22float2(h);
+  const float2 v = __half22float2(half2_of(w));
   if (!isfinite(v.x)) x += v.x;
   if (!isfinite(v.y)) y += v.y;
 }

@@ -121,24 +121,9 @@ __device__ __forceinline__ void commit(uint32_t bar) {
 __device__ __forceinline__ void arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ uint32_t bits(__half2 h) {
-  uint32_t u;
-  memcpy(&u, &h, 4);
-  return u;
-}
-__device__ __forceinline__ __half2 half2_of(uint32_t u) {
-  __half2 h;
-  memcpy(&h, &u, 4);
-  return h;
-}
 // The halves of x whose magnitude is limit (bits of a half) or more, or NaN: all their bits set.
 __device__ __forceinline__ uint32_t halves_from(uint32_t x, uint32_t limit) {
   return ((x & 0x7fffu) >= limit ? 0xffffu : 0u) | (((x >> 16) & 0x7fffu) >= limit ? 0xffff0000u : 0u);
-}
-// Bytes (i, j) of x as halves less `off` (bits of a half): a byte put under the exponent of 1024 is 1024 + it, exactly.
-template <int kSel>
-__device__ __forceinline__ __half2 bytes2(uint32_t x, uint32_t off) {
-  return __hsub2(half2_of(__byte_perm(x, 0x64646464u, kSel)), half2_of(off));
 }
 __device__ __forceinline__ uint4 ld_smem(uint32_t p) {
   uint4 x;

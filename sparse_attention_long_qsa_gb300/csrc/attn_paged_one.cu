@@ -90,31 +90,21 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   return y;
 }
 // (sx, sy) += (dx, dy) * (cx, cy)
-__device__ __forceinline__ void fma2(float& sx, float& sy, float dx, float dy, float cx, float cy) {
+__device__ __forceinline__ void add_products2(float& sx, float& sy, float dx, float dy, float cx, float cy) {
   asm("{\n .reg .b64 s, d, c;\n mov.b64 s, {%0, %1};\n mov.b64 d, {%2, %3};\n mov.b64 c, {%4, %5};\n"
       " fma.rn.f32x2 s, d, c, s;\n mov.b64 {%0, %1}, s;\n}\n"
       : "+f"(sx), "+f"(sy)
       : "f"(dx), "f"(dy), "f"(cx), "f"(cy));
-}
-__device__ __forceinline__ uint32_t bits(__half2 h) {
-  uint32_t u;
-  memcpy(&u, &h, 4);
-  return u;
-}
-__device__ __forceinline__ __half2 half2_of(uint32_t u) {
-  __half2 h;
-  memcpy(&h, &u, 4);
-  return h;
 }
 __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t o) {
   uint32_t r;
   asm("lop3.b32 %0, %1, %2, %3, 0xea;\n" : "=r"(r) : "r"(x), "r"(m), "r"(o));
   return r;
 }
-// Signed bytes (i, j) of x ^ 0x80808080 as halves: a byte put under the exponent of 1024 is 1024 + it, exactly.
+// Signed bytes (i, j) of x ^ 0x80808080 as halves.
 template <int kSel>
-__device__ __forceinline__ uint32_t bytes2(uint32_t x) {
-  return bits(__hsub2(half2_of(__byte_perm(x, 0x64646464u, kSel)), half2_of(0x64806480u)));
+__device__ __forceinline__ uint32_t signed2(uint32_t x) {
+  return bits(bytes2<kSel>(x, 0x64806480u));
 }
 // Codes less 8 in bits 0..3 of x's two halves.
 __device__ __forceinline__ uint32_t nibbles2(uint32_t x) {
@@ -298,8 +288,8 @@ __global__ void __launch_bounds__(Row<KV>::kWarps * 32, 1) k_paged_one(const Pag
             ldsm4(arow + 32 * b, w);
 #pragma unroll
             for (int j = 0; j < 4; ++j) w[j] ^= 0x80808080u;
-            x0[0] = bytes2<0x4140>(w[0]), x0[1] = bytes2<0x4140>(w[1]), x0[2] = bytes2<0x4342>(w[0]), x0[3] = bytes2<0x4342>(w[1]);
-            x1[0] = bytes2<0x4140>(w[2]), x1[1] = bytes2<0x4140>(w[3]), x1[2] = bytes2<0x4342>(w[2]), x1[3] = bytes2<0x4342>(w[3]);
+            x0[0] = signed2<0x4140>(w[0]), x0[1] = signed2<0x4140>(w[1]), x0[2] = signed2<0x4342>(w[0]), x0[3] = signed2<0x4342>(w[1]);
+            x1[0] = signed2<0x4140>(w[2]), x1[1] = signed2<0x4140>(w[3]), x1[2] = signed2<0x4342>(w[2]), x1[3] = signed2<0x4342>(w[3]);
           } else {
             if ((b & 1) == 0) ldsm4(arow + 16 * b, w);
             const uint32_t w0 = w[2 * (b & 1)], w1 = w[2 * (b & 1) + 1];
@@ -395,8 +385,8 @@ __global__ void __launch_bounds__(Row<KV>::kWarps * 32, 1) k_paged_one(const Pag
             ldsm4t(vrow + 64 * b + 32 * i, x);
             mma0(c, x, ph[0], ph[1]);
             mma(c, x, pw[0], pw[1]);
-            fma2(acc[b][i][0], acc[b][i][1], fac[0], fac[1], c[0], c[1]);
-            fma2(acc[b][i][2], acc[b][i][3], fac[0], fac[1], c[2], c[3]);
+            add_products2(acc[b][i][0], acc[b][i][1], fac[0], fac[1], c[0], c[1]);
+            add_products2(acc[b][i][2], acc[b][i][3], fac[0], fac[1], c[2], c[3]);
           }
       } else {
         // the chunk's scales: this lane those of cells 2 l4 + {0, 1, 8, 9} in block gid
@@ -442,7 +432,7 @@ __global__ void __launch_bounds__(Row<KV>::kWarps * 32, 1) k_paged_one(const Pag
             uint32_t x[4];
             if constexpr (KV == QSA_KV_Q8_0) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) x[j] = i == 0 ? bytes2<0x4240>(w[j]) : bytes2<0x4341>(w[j]);
+              for (int j = 0; j < 4; ++j) x[j] = i == 0 ? signed2<0x4240>(w[j]) : signed2<0x4341>(w[j]);
             } else {   // w[0], w[1]: the block's bytes of cells 0-7, 8-15
               const uint32_t v0 = w[0] >> (8 * i), v1 = w[1] >> (8 * i);
               x[0] = nibbles2(v0), x[1] = high_nibbles2(v0), x[2] = nibbles2(v1), x[3] = high_nibbles2(v1);
@@ -450,8 +440,8 @@ __global__ void __launch_bounds__(Row<KV>::kWarps * 32, 1) k_paged_one(const Pag
             float c[4];
             mma0(c, x, bits(x0), bits(x1));
             mma(c, x, y0, y1);
-            fma2(acc[b][i][0], acc[b][i][1], f0, f1, c[0], c[1]);
-            fma2(acc[b][i][2], acc[b][i][3], f0, f1, c[2], c[3]);
+            add_products2(acc[b][i][0], acc[b][i][1], f0, f1, c[0], c[1]);
+            add_products2(acc[b][i][2], acc[b][i][3], f0, f1, c[2], c[3]);
           }
         };
         // the block's codes: q8_0 four pieces (dims 0-15, 16-31 of cells 0-7, then 8-15); q4_0 two blocks at a time

@@ -114,11 +114,6 @@ __device__ __forceinline__ void pair_commit(uint32_t bar) {
 __device__ __forceinline__ void lead_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ uint32_t half_bits(__half2 h) {
-  uint32_t u;
-  memcpy(&u, &h, 4);
-  return u;
-}
 // The halves of x that are infinite or NaN, all their bits set.
 __device__ __forceinline__ uint32_t stray_halves(uint32_t x) {
   return ((x & 0x7c00u) == 0x7c00u ? 0xffffu : 0u) | ((x & 0x7c000000u) == 0x7c000000u ? 0xffff0000u : 0u);
@@ -301,7 +296,7 @@ __global__ void __launch_bounds__(640, 1) k_paged_prompt(const PagedArgs a, unsi
             float2 h;
             hi[j] = first_part(x, y, h);
             add2(x, y, -h.x, -h.y);
-            lo[j] = half_bits(__floats2half2_rn(x, y));
+            lo[j] = bits(__floats2half2_rn(x, y));
           }
           tmem_st16(ts + 32 * k, hi);
           tmem_st16(ts + 32 * k + 16, lo);

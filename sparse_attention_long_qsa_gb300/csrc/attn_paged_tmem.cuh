@@ -67,9 +67,7 @@ __device__ __forceinline__ float next_reference(float m, float& high, float x, f
 __device__ __forceinline__ uint32_t first_part(float x, float y, float2& back) {
   const __half2 h = __floats2half2_rn(x, y);
   back = __half22float2(h);
-  uint32_t u;
-  memcpy(&u, &h, 4);
-  return u;
+  return bits(h);
 }
 // bits [0, n) of a word, any n
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
