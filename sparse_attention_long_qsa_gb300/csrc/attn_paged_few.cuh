@@ -83,6 +83,7 @@ struct Smem {
   alignas(1024) unsigned char stage[kStages][Row<KV>::kParts * kPartBytes];
   alignas(16) unsigned char raw[kAhead][kCells * kPitch];   // rows as they come, codes then scales
   float max[2][2][128];                      // of half a row, by tile parity
+  bool alone[2][2][128];                     // (see tile_top)
   float sum[2][128];
   alignas(16) float out[kSoft / 32][32][kOutPitch];   // see write_rows
   int ids[2][kSuper];
@@ -274,6 +275,7 @@ __global__ void __launch_bounds__(KV == QSA_KV_F16 ? 896 : 768, 1) k_paged_few(c
       int next = stretch;   // where the next one begins
       float fs = 0.f;       // of the stretches' sums so far
       float m = mine ? kNoMax : 0.f, high = kNoMax, l = 0.f;   // the row's reference, the highest, this half's sum relative to it
+      bool big = false;   // (see is_big)
       for (int i = 0; i < n; ++i) {
         const int b = (base + i) & 1;
         const uint32_t ts = tl + kColS + kCells * b + 32 * half;
@@ -298,14 +300,17 @@ __global__ void __launch_bounds__(KV == QSA_KV_F16 ? 896 : 768, 1) k_paged_few(c
           float t4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
           for (int j = 4; j < 32; ++j) t4[j & 3] = fmaxf(t4[j & 3], s[j]);
-          const float top = tile_top(t4, scale2);
+          bool alone;
+          const float top = tile_top(t4, scale2, alone);
           sm.max[b][half][row] = top;
+          sm.alone[b][half][row] = alone;
           bar_named(2 + quarter, 64);   // the row's two threads
-          const float nm = mine ? next_reference(m, high, top, sm.max[b][half ^ 1][row], scale2) : m;
+          const float nm = mine ? next_reference(m, high, top, sm.max[b][half ^ 1][row], alone || sm.alone[b][half ^ 1][row], big, scale2) : m;
           if (__any_sync(kFull, nm != m)) {
             const float f = ex2(m - nm);
             l *= f;
             m = nm;
+            big = is_big(m);
             raised = f;
             if (i > 0 && !begins) {   // O holds the tiles before
               if (!mbar_wait(bpv + 8 * (b ^ 1), (uint32_t)((base + i - 1) >> 1) & 1u)) timed_out = true;
@@ -322,7 +327,12 @@ __global__ void __launch_bounds__(KV == QSA_KV_F16 ? 896 : 768, 1) k_paged_few(c
             }
           }
           // probabilities, in place: of 16 cells first parts in 8 columns, second parts in the next 8
-          const float ref = kUp - m;
+          float ref = kUp - m, by = scale2;
+          if (big) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[j] = __fsub_rn(__fmul_rn(s[j], scale2), m);
+            ref = kUp, by = 1.f;
+          }
           float sx = 0.f, sy = 0.f;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -331,7 +341,7 @@ __global__ void __launch_bounds__(KV == QSA_KV_F16 ? 896 : 768, 1) k_paged_few(c
             for (int j = 0; j < 8; ++j) {
               const int c = 16 * k + 2 * j;
               float x = s[c], y = s[c + 1];
-              fma2(x, y, scale2, ref);
+              fma2(x, y, by, ref);
               x = ex2(x), y = ex2(y);
               add2(sx, sy, x, y);
               if constexpr (kWeigh) s[c] = x, s[c + 1] = y;

@@ -32,31 +32,36 @@ __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
 }
 // Probabilities of a tile are 2^(s - reference + kUp) of each row, in two fp16 parts, the second what the first leaves:
 // 22 bits down to 2^-2 and less below, as a part ends at 2^-24.  So the reference follows the tiles.  It goes up where a
-// tile's largest score is kSlack above it (they stay below 2^16), and down where the largest is kLow below (of the tile:
+// tile's largest score is kSlack above it (they stay below 2^15.2), and down where the largest is kLow below (of the tile:
 // what the cells of other tiles weigh does not cost its weights their bits); what has been summed up is scaled along, which
 // fp32 holds as long as no reference is kFar below another.  Ordinary rows are scaled once or twice a run: their tiles'
 // largest scores lie a few places apart.  Where a few cells of a tile stand out (kAlone above some eighth of the tile's,
 // or above the other half's), the others get what is left of fp16's range: the largest weight starts at its top.
 // (With a reference that only went up, 2^7 for the largest: 24 places below a sink without value outputs were 8e-4 off, and
-// 40 below meaningless.  Rows of ordinary scores take the same time; scores spread by 11 places 3 to 8 % more.)
-constexpr float kUp = 8.f, kSlack = 7.9f, kLow = 14.f, kFar = 64.f, kAlone = 14.f;
-// The largest of a row's scores in half a tile, from that of four interleaved parts of it; its last bit says whether it
-// stands out (-inf: nothing is visible).
-__device__ __forceinline__ float tile_top(const float (&t)[4], float scale2) {
+// 40 below meaningless.  Rows of ordinary scores take the same time; scores that spread by 6 places and more take 4 to 10 % more.)
+constexpr float kUp = 7.f, kSlack = 8.f, kLow = 13.f, kFar = 64.f, kAlone = 13.f;
+// From kBig on a score's last place is so much that its product with the scale, the reference and their difference are
+// rounded one by one, so that the largest comes to the reference exactly, which then follows every rise.  (In one rounding
+// scores of 1e7 and more were NaN.)
+constexpr float kBig = 1048576.f;
+__device__ __forceinline__ bool is_big(float m) { return fabsf(m) > kBig && fabsf(m) < -kNoMax; }
+// The largest of a row's scores in half a tile, from that of four interleaved parts of it (-inf: nothing is visible), and
+// whether it stands out.
+__device__ __forceinline__ float tile_top(const float (&t)[4], float scale2, bool& alone) {
   const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
   float low = top;
 #pragma unroll
   for (int j = 0; j < 4; ++j) low = t[j] == -INFINITY ? low : fminf(low, t[j]);
-  const float gap = (top - low) * scale2;
-  return __uint_as_float((__float_as_uint(top) & ~1u) | (gap > kAlone && gap < INFINITY ? 1u : 0u));
+  alone = (top - low) * scale2 > kAlone;
+  return top;
 }
-// The row's reference after a tile whose halves' tile_top are x and y.  `high`: the highest so far.
-__device__ __forceinline__ float next_reference(float m, float& high, float x, float y, float scale2) {
+// The row's reference after a tile whose halves' largest are x and y.  `high`: the highest so far.
+__device__ __forceinline__ float next_reference(float m, float& high, float x, float y, bool alone, bool big, float scale2) {
   const float top2 = fmaxf(x, y), top = top2 == -INFINITY ? top2 : top2 * scale2;   // (-inf times zero would be NaN)
   float nm = m;
-  if (top > m + kSlack || top != top) {
-    const bool alone = ((__float_as_uint(x) | __float_as_uint(y)) & 1u) || fabsf(x - y) * scale2 > kAlone;
-    nm = alone && fminf(x, y) > -INFINITY ? top - kSlack : top;
+  if (top > m + (big ? 0.f : kSlack) || top != top) {
+    alone = alone || fabsf(x - y) * scale2 > kAlone;
+    nm = alone && fminf(x, y) > -INFINITY && fabsf(top) <= kBig ? top - kSlack : top;
   } else if (top < m - kLow && top > -INFINITY) {
     nm = fminf(m, fmaxf(top, high - kFar));
   }
