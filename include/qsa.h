@@ -587,8 +587,8 @@ qsa_status qsa_cache_sweep(const qsa_config* cfg, uint32_t flags, const int32_t*
  * qsa_paged_attn_workspace_size bytes for this n_tokens (or more) and max_len, weigh
  * = whether block_weight is given; 256-byte aligned, any contents.
  * q, tok_seq, tok_pos and out may be page-locked host memory.  r must be 1, 2, 4 or
- * 8 (QSA_ERR_UNSUPPORTED); n_tokens <= 65535.  Indices out of range are masked and
- * flagged. */
+ * 8, so that 16 cells are whole blocks (QSA_ERR_UNSUPPORTED); n_tokens <= 65535.
+ * Indices out of range are masked and flagged. */
 size_t qsa_paged_attn_workspace_size(const qsa_config* cfg, int32_t n_tokens, int64_t max_len, int32_t weigh);
 qsa_status qsa_paged_attn(const qsa_config* cfg, int32_t n_tokens, int32_t window, int32_t n_sink, const void* q,
                           const int32_t* tok_seq, const int32_t* tok_pos, const void* k_cache, const void* v_cache,

@@ -6,18 +6,21 @@
 // Three kernels share the work split.  Consecutive tokens of one sequence form
 // groups, which read their cells once.  A group's positions are cut into tiles, and
 // the tiles of all groups, laid end to end, are dealt in equal runs to the CTAs of a
-// KV head, however long each sequence is.  A run that covers a group whole writes its
-// output; the others leave (max, sum, o) in the workspace, and k_paged_join adds them
-// in the order of the runs.
+// KV head, however long each sequence is (or, where no part gets much more than its
+// share for that, in whole groups, see plan).  A run that covers a group whole writes
+// its output; the others leave (max, sum, o) in the workspace, and k_paged_join adds
+// them in the order of the runs.
 //   attn_paged_one.cu   single tokens: bound by the reading of the rows
-//   attn_paged_few.cu   several tokens of a sequence, rows of any type: by forming
+//   attn_paged_few.cuh  several tokens of a sequence, rows of any type: by forming
 //                       operands
 //   attn_paged_tc.cu    many tokens of fp16 rows: by the tensor cores; pairs of CTAs
 //                       gather half the bytes that the kernel for few tokens would
+// A call of both kinds goes to two of them (see route).
 //
-// Nothing is rounded below fp32.  K and V enter the products as they are stored, or
+// Sums and the softmax are fp32.  K and V enter the products as they are stored, or
 // codes times scales in parts that hold them exactly; probabilities go in as two fp16
-// parts (22 bits).
+// parts: 22 bits, less where they lie far below others that are read with them (each
+// kernel says how far).
 #include <algorithm>
 #include <atomic>
 

@@ -31,13 +31,14 @@
 // would not keep out: it is replaced by zero, and what it does to the rows that see
 // it is added when the run's result is written.
 //
-// What bounds it: a tile of codes takes some 3,900 cycles, its products 2,560 (1,024
+// What bounds it: a tile of codes takes some 4,200 cycles, its products 2,560 (1,024
 // and 1,536), its operands 2 x 1,250; they alternate in two stages, which is all that
-// shared memory holds of 64 KB each, so neither is ever alone.  Five tokens over 250k
-// q8_0 cells: 105 us with their join, 0.39 of the row bandwidth (the kernel before,
-// on mma.sync, took 310); with block weights 158 us.  512 tokens in a window of 1,024
-// over q8_0: 50 us (157).  With half of the products left out the five tokens take 10 %
-// less: it is the chain, not a unit, that is full.
+// shared memory holds of 64 KB each, so neither is ever alone (tensor pipe 52 %).  Five
+// tokens over 250k q8_0 cells: 128 us with their join, 0.31 of the row bandwidth (the
+// kernel before, on mma.sync, took 310); with block weights 160 us.  512 tokens in a
+// window of 1,024 over q8_0: 47 us (157); over all of 50k: 0.70 ms.  With half of the
+// products left out the five tokens take 10 % less: it is the chain, not a unit, that
+// is full.
 #pragma once
 
 #include <atomic>

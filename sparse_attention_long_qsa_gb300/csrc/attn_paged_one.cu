@@ -10,9 +10,9 @@
 // of all tokens, laid end to end, are dealt in equal runs to the CTAs of a KV head,
 // one CTA an SM.
 //
-// Nothing is rounded below fp32: codes enter the products as
+// Codes enter the products as
 // integers, K scales apply to a block's sum, V scales to the probabilities, which go
-// in as two fp16 parts (22 bits).  A half keeps its bits 30 binary places below the
+// in as two fp16 parts (22 bits); sums are fp32.  A half keeps its bits 30 binary places below the
 // largest only, so the weights p * d_V are relative to the chunk's largest
 // probability (2^15) and largest scale ([1/4, 1/2)): they are off by 2^-22 of
 // themselves or by 2^-39 of that largest product.  Where a chunk's scales of V lie
@@ -20,10 +20,10 @@
 // block do, or are infinite or NaN, its cells are added one by one, each relative to
 // its own.
 //
-// What bounds it: fp16 rows the gather (64 sequences of up to 8,000 cells: 133 us,
-// 5.3 TB/s; a gather of rows reaches 5.7 to 6.3), codes the warps' chains of dependent
-// instructions (250k q8_0: 62 us, 4.4 TB/s, 54 % of the issue slots; 5 x 250k q4_0:
-// 147 us, 64 %), as shared memory holds rows for 12 warps and registers sums for 16.
+// What bounds it: fp16 rows the gather (64 sequences of up to 8,000 cells: 134 us,
+// 5.2 TB/s; a gather of rows reaches 5.7 to 6.3), codes the warps' chains of dependent
+// instructions (250k q8_0: 63 us, 4.3 TB/s, 50 % of the issue slots; 5 x 250k q4_0:
+// 144 us, 63 %), as shared memory holds rows for 12 warps and registers sums for 16.
 // One token over 50k fp16 cells takes 30 us, of which the rows take 17: the plan 1, the
 // ids 2, the merge and the join 7.
 #include <atomic>

@@ -32,8 +32,8 @@
 // The two parts of P cost a half more than one would (3,072 instead of 2,048 tensor
 // cycles a tile): the output is fp32, and one part would leave it 2e-4 off.
 //
-// What bounds it: the tensor pipe is 73 % busy (512 tokens over 50k cells, 0.45 ms,
-// 930 TFLOP/s of the definition's products, 1.37 PFLOP/s of those that are made).  The
+// What bounds it: the tensor pipe is 75 % busy (512 tokens over 50k cells, 0.455 ms,
+// 915 TFLOP/s of the definition's products, 1.37 PFLOP/s of those that are made).  The
 // rest is Q's reading from shared memory (36 cycles of each score product; tensor
 // memory has no room for it) and 4 us for each stretch of sums that leaves.  8,192
 // tokens in a window of 4,096: 0.62 ms, of which a run's beginning and end take a
