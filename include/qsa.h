@@ -568,8 +568,8 @@ qsa_status qsa_cache_sweep(const qsa_config* cfg, uint32_t flags, const int32_t*
  * 16 to 128 cells that are read together, 2^-39 of the largest where that stands out;
  * where neighbouring tokens share their reading a sum is cut to 24 bits at each
  * addition of up to 288.  Against 64 bits outputs of N(0, 1) rows are off by 4e-7 to
- * 7e-6 of their norm, and by no more below a sink that takes all but 2^-24 of a
- * cell's weight.  Within a sequence's
+ * 7e-6 of their norm, and by no more where they are what a sink leaves that lies up to
+ * 24 binary places above all other cells.  Within a sequence's
  * range the sums run over tiles whose order depends on the call's shape and the
  * device, not on timing.  An infinite fp16 value of a visible V is one of the output.
  * An infinite or NaN scale of a visible K block gives NaN,

@@ -402,9 +402,10 @@ __global__ void __launch_bounds__(KV == QSA_KV_F16 ? 896 : 768, 1) k_paged_few(c
       const bool stray = *reinterpret_cast<volatile unsigned*>(&sm.stray[runs & 7]) != 0u;   // (one value for the warp)
       const int64_t stride = (whole ? G : 1) * (kGqa * kHeadDim);
       write_rows<false>(tl + 128 * half, sm.out[warp], w, rows, stride, stretch < n ? sums : nullptr, fs, 32 * quarter, gr.nt);
-      if (stray) {
+      if (stray) {   // (a row whose sum is not finite is NaN throughout)
         put_not_finite(
-            a, run, v_first, min(gr.nv, v_first + n * kCells), mine ? rows + tok * stride + head * kHeadDim : nullptr,
+            a, run, v_first, min(gr.nv, v_first + n * kCells),
+            mine && l - l == 0.f ? rows + tok * stride + head * kHeadDim : nullptr,
             [&](int p) { return p <= pos && (a.window == 0 || p > pos - a.window || p < a.n_sink); },
             [&](int c, int k, uint32_t (&x)[8]) {
               if constexpr (kF16) {

@@ -38,3 +38,32 @@ def test_an_infinite_value_is_one_of_the_output(n, T, window, sinks):
     for d, x in want.items():
         got = out[:, 8:, d]
         assert torch.all(got.isnan() if x != x else got == x), (d, x, got.flatten()[:8].tolist())
+
+
+@pytest.mark.parametrize("kv", ["f16", "q8_0", "q4_0"])
+@pytest.mark.parametrize("n,T", [(200, 1), (200, 5), (200, 40), (5_000, 1), (5_000, 5), (5_000, 40)])
+def test_a_token_whose_scores_are_nan_is_nan(kv, n, T):
+    """Beside infinite values of V, too; tokens before the cell, and the other KV head, are as they were."""
+    P = Paged(kv, (n,), seed=n + T)
+    q, s, p = P.tokens([0] * T, list(range(n - T, n)))
+    first = n - 1 - T // 2                                   # the first token to see the cell
+    clean = P.attend(q, s, p)
+    cells = P.visible(0, n - 1)[1]
+    if kv == "f16":
+        P.k[cells[first], 1, 17] = NAN
+        P.v[cells[n // 2], 1, 40] = INF
+        dims = [40]
+    else:
+        codes = P.n_cells * 2 * (256 if kv == "q8_0" else 128)
+        for raw, c, block in ((P.k, cells[first], 0), (P.v, cells[n // 2], 1)):
+            raw[codes:].view(torch.float16).view(P.n_cells, 2, 8)[c, 1, block] = INF
+        dims = list(range(32, 64))
+    out = P.attend(q, s, p)
+    no_errors()
+    sees = p >= first
+    assert sees.any() and out[sees][:, 8:].isnan().all()
+    assert torch.equal(out[:, :8], clean[:, :8])
+    rest = [d for d in range(D) if d not in dims]
+    assert torch.equal(out[~sees][:, 8:][..., rest], clean[~sees][:, 8:][..., rest])
+    hit = out[~sees][:, 8:][..., dims]
+    assert torch.all(hit == INF if kv == "f16" else hit.isnan())
