@@ -14,8 +14,8 @@ KV = ["f16", "q8_0", "q4_0"]
 
 
 def bound(P, T, much):
-    """max_len with which reading the rows of T tokens one by one would take `much` bytes: from 1.25e9 on a call goes to two
-    kernels where its average says one by one, from 2e10 on where it says groups of 16."""
+    """max_len with which reading the rows of T tokens one by one takes `much` bytes: with 1.25e9 of T lists or more a call
+    goes to a kernel for single tokens and one for groups, with 2e10 of a few lists to one for groups of 16 and one of 32."""
     row = {"f16": 512, "q8_0": 272, "q4_0": 144}[P.kv]
     return max(max(P.lens), int(1.05 * much / (2 * P.G * row * T)))
 
@@ -56,6 +56,17 @@ def test_a_chunk_among_single_tokens(kv, singles, chunk, much):
     out = P.attend(q, s, p, max_len=bound(P, q.shape[0], much))
     no_errors()
     P.check(out, q, s, p, only=set(range(half)) | set(range(half, half + chunk, 13)) | set(range(half + chunk, q.shape[0])))
+
+
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("G,r,lists", [(1, 1, 300), (3, 8, 300), (8, 2, 300), (3, 4, 5), (64, 4, 300)])
+def test_heads_of_mixed_calls(kv, G, r, lists):
+    P = Paged(kv, (500, 90, 333, 64, 200) + (1,) * (lists - 5), G=G, r=r, seed=G)
+    q, s, p = runs(P, [(0, 40), (1, 1), (2, 2), (3, 16), (4, 1), (1, 3)])
+    for much in (1.25e9, 2e10):
+        out = P.attend(q, s, p, max_len=bound(P, q.shape[0], much))
+        no_errors()
+        P.check(out, q, s, p)
 
 
 def test_a_window_over_long_lists():
